@@ -27,7 +27,9 @@ __all__ = [
     "rdot_forward_combine", "rdot_grad_weight_mxfp8", "router_topk", "ragged_dot_combine", "grad_weight_mxfp8",
     "moe_permute", "moe_unpermute", "ragged_dot", "grad_weight",
     "grad_input", "ragged_dot_gated",
-    "ragged_dot_mxfp8", "padded_ragged_dot", "EXPORTED_SYMBOLS",
+    "ragged_dot_mxfp8", "padded_ragged_dot",
+    "rdot_moe_unpermute_grad", "rdot_moe_permute_grad", "rdot_router_topk_grad",
+    "moe_unpermute_grad", "moe_permute_grad", "router_topk_grad", "EXPORTED_SYMBOLS",
 ]
 
 RDOT_OK, RDOT_ERR_INVALID_ARG, RDOT_ERR_UNSUPPORTED, RDOT_ERR_CUDA = 0, 1, 2, 3
@@ -52,6 +54,7 @@ EXPORTED_SYMBOLS = (
     "rdot_forward_no_alloc", "rdot_no_alloc_read_status", "rdot_grad_input", "rdot_moe_route_workspace_size",
     "rdot_moe_permute", "rdot_moe_unpermute", "rdot_forward_gated", "rdot_grad_input_mxfp8", "rdot_router_topk",
     "rdot_forward_combine", "rdot_grad_weight_mxfp8",
+    "rdot_moe_unpermute_grad", "rdot_moe_permute_grad", "rdot_router_topk_grad",
 )
 
 _DTYPE_CODES = {"f32": RDOT_F32, "bf16": RDOT_BF16, "e4m3": RDOT_E4M3}
@@ -127,6 +130,10 @@ def load():
             "rdot_forward_combine": ([vp, vp, vp, vp, vp, vp, i64, ctypes.c_int32, vp, vp, vp], st),
             "rdot_router_topk": ([vp, ctypes.c_int32, i64, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, vp, vp, vp],
                                  st),
+            "rdot_moe_unpermute_grad": ([vp, vp, vp, vp, vp, i64, ctypes.c_int32, i64, vp, vp, vp], st),
+            "rdot_moe_permute_grad": ([vp, ctypes.c_int32, vp, i64, ctypes.c_int32, i64, vp, vp], st),
+            "rdot_router_topk_grad": ([vp, ctypes.c_int32, vp, vp, vp, i64, ctypes.c_int32, ctypes.c_int32,
+                                       ctypes.c_int32, vp, vp], st),
         }
         for name, (args, res) in sig.items():
             f = getattr(lib, name)
@@ -245,6 +252,40 @@ def rdot_router_topk(logits, topk: int, weights_mode: int, topk_ids, topk_weight
         raise TypeError("logits must be float32 or bfloat16")
     _check(load().rdot_router_topk(_ptr(logits), dt, int(t), int(e), int(topk), int(weights_mode), _ptr(topk_ids),
                                    _ptr(topk_weights), _stream(stream, logits.device)), "rdot_router_topk")
+
+
+def _float_dtype(t, what: str) -> int:
+    import torch
+    dt = {torch.float32: RDOT_F32, torch.bfloat16: RDOT_BF16}.get(t.dtype)
+    if dt is None:
+        raise TypeError(f"{what} must be float32 or bfloat16")
+    return dt
+
+
+def rdot_moe_unpermute_grad(dout, y_sorted, order, inv, topk_weights, dy_sorted, dweights, stream=None) -> None:
+    """dout bf16 [T, N], y_sorted bf16 [T*k, N] -> dy_sorted bf16 [T*k, N], dweights fp32 [T, k]."""
+    t, k = topk_weights.shape
+    _check(load().rdot_moe_unpermute_grad(_ptr(dout), _ptr(y_sorted), _ptr(order), _ptr(inv), _ptr(topk_weights),
+                                          int(t), int(k), int(y_sorted.shape[1]), _ptr(dy_sorted), _ptr(dweights),
+                                          _stream(stream, dout.device)), "rdot_moe_unpermute_grad")
+
+
+def rdot_moe_permute_grad(dx_sorted, inv, dx, stream=None) -> None:
+    """dx_sorted [T*k, N] (fp32 or bf16) -> dx [T, N], the same dtype."""
+    t = dx.shape[0]
+    _check(load().rdot_moe_permute_grad(_ptr(dx_sorted), _float_dtype(dx_sorted, "dx_sorted"), _ptr(inv), int(t),
+                                        inv.numel() // t if t else 1, int(dx.shape[1]), _ptr(dx),
+                                        _stream(stream, dx.device)), "rdot_moe_permute_grad")
+
+
+def rdot_router_topk_grad(logits, topk_ids, topk_weights, dweights, weights_mode: int, dlogits, stream=None) -> None:
+    """The logits' gradient, dlogits [T, E] (fp32 or bf16), from the weights' (fp32 [T, k]); logits
+    (the same dtype) may be None unless the weights are the softmax over all experts."""
+    t, e = dlogits.shape
+    _check(load().rdot_router_topk_grad(_ptr(logits), _float_dtype(dlogits, "dlogits"), _ptr(topk_ids),
+                                        _ptr(topk_weights), _ptr(dweights), int(t), int(e), int(topk_ids.shape[1]),
+                                        int(weights_mode), _ptr(dlogits), _stream(stream, dlogits.device)),
+           "rdot_router_topk_grad")
 
 
 def rdot_padded_workspace_size(plan, capacity: int) -> int:
@@ -567,6 +608,54 @@ def moe_unpermute(y_sorted, inv, topk_weights, out=None, stream=None):
             out = torch.empty((t, y_sorted.shape[1]), dtype=torch.bfloat16, device=y_sorted.device)
         rdot_moe_unpermute(y_sorted.contiguous(), inv, topk_weights.to(torch.float32).contiguous(), out, s)
     return out
+
+
+def moe_unpermute_grad(dout, y_sorted, order, inv, topk_weights, stream=None):
+    """The gradient of :func:`moe_unpermute`: returns ``(dy_sorted bf16 [T*k, N], dw fp32 [T, k])`` for
+    the combined rows' gradient dout bf16 [T, N], the expert outputs y_sorted bf16 [T*k, N] that the
+    forward combined, and :func:`moe_permute`'s order and inv."""
+    import torch
+    t, k = topk_weights.shape
+    if dout.dtype != torch.bfloat16 or y_sorted.dtype != torch.bfloat16:
+        raise TypeError("dout and y_sorted must be bfloat16")
+    if dout.shape != (t, y_sorted.shape[1]) or y_sorted.shape[0] != t * k or order.numel() != t * k or inv.numel() != t * k:
+        raise ValueError("shape mismatch between dout, y_sorted, order, inv and topk_weights")
+    s = _run_stream(stream, dout.device)
+    with torch.cuda.stream(s):
+        dy = torch.empty_like(y_sorted, memory_format=torch.contiguous_format)
+        dw = torch.empty((t, k), dtype=torch.float32, device=dout.device)
+        rdot_moe_unpermute_grad(dout.contiguous(), y_sorted.contiguous(), order.to(torch.int32).contiguous(),
+                                inv.to(torch.int32).contiguous(), topk_weights.to(torch.float32).contiguous(), dy, dw, s)
+    return dy, dw
+
+
+def moe_permute_grad(dx_sorted, inv, k, stream=None):
+    """The gradient of :func:`moe_permute`'s gather: dx [T, N] with ``dx[t]`` the sum of the rows of
+    dx_sorted [T*k, N] (fp32 or bf16) that token t's kept copies were sorted to."""
+    import torch
+    if k < 1 or dx_sorted.dim() != 2 or dx_sorted.shape[0] % k or inv.numel() != dx_sorted.shape[0]:
+        raise ValueError("dx_sorted must have T*k rows and inv T*k elements")
+    s = _run_stream(stream, dx_sorted.device)
+    with torch.cuda.stream(s):
+        dx = torch.empty((dx_sorted.shape[0] // k, dx_sorted.shape[1]), dtype=dx_sorted.dtype, device=dx_sorted.device)
+        rdot_moe_permute_grad(dx_sorted.contiguous(), inv.to(torch.int32).contiguous(), dx, s)
+    return dx
+
+
+def router_topk_grad(logits, topk_ids, topk_weights, dweights, weights="softmax_topk", stream=None):
+    """The gradient of :func:`router_topk`: dlogits (the logits' shape and dtype, fp32 or bf16) from the
+    weights' gradient dweights [T, k]."""
+    import torch
+    t, _ = logits.shape
+    if topk_ids.shape != topk_weights.shape or topk_ids.shape != dweights.shape or topk_ids.shape[0] != t:
+        raise ValueError("topk_ids, topk_weights and dweights must all be [T, k]")
+    s = _run_stream(stream, logits.device)
+    with torch.cuda.stream(s):
+        dlogits = torch.empty_like(logits, memory_format=torch.contiguous_format)
+        rdot_router_topk_grad(logits.contiguous(), topk_ids.to(torch.int32).contiguous(),
+                              topk_weights.to(torch.float32).contiguous(), dweights.to(torch.float32).contiguous(),
+                              _ROUTER_MODES[weights], dlogits, s)
+    return dlogits
 
 
 def ragged_dot_mxfp8(lhs_q, lhs_scale, rhs_q, rhs_scale, group_sizes, out=None, stream=None):

@@ -1344,6 +1344,63 @@ rdot_status rdot_router_topk(const void* logits, int32_t dtype, int64_t tokens, 
     return e == cudaSuccess ? RDOT_OK : cuda_fail(e, "router top-k launch");
 }
 
+rdot_status rdot_moe_unpermute_grad(const void* dout, const void* y_sorted, const int32_t* order, const int32_t* inv,
+                                    const float* topk_weights, int64_t tokens, int32_t topk, int64_t n, void* dy_sorted,
+                                    float* dweights, void* stream) {
+    if (tokens < 0 || topk < 1 || n < 1) return RDOT_ERR_INVALID_ARG;
+    if (n % 8 || n / 8 > 0x3fffffffLL || tokens > 0x7fffffffLL || tokens * topk > 0x7fffffffLL)
+        return RDOT_ERR_UNSUPPORTED;
+    if (tokens == 0) return RDOT_OK;
+    if (!dout || !y_sorted || !order || !inv || !topk_weights || !dy_sorted || !dweights) return RDOT_ERR_INVALID_ARG;
+    if (!aligned16(dout) || !aligned16(y_sorted) || !aligned16(dy_sorted) || !aligned4(order) || !aligned4(inv) ||
+        !aligned4(topk_weights) || !aligned4(dweights))
+        return RDOT_ERR_INVALID_ARG;
+    const int sms = current_sm_count();
+    if (sms <= 0) return cuda_fail(cudaGetLastError(), "cudaDeviceGetAttribute");
+    cudaError_t e = launch_moe_unpermute_grad(dout, y_sorted, order, inv, topk_weights, tokens, topk, n, dy_sorted,
+                                              dweights, sms, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? RDOT_OK : cuda_fail(e, "moe un-permute gradient launch");
+}
+
+rdot_status rdot_moe_permute_grad(const void* dx_sorted, int32_t dtype, const int32_t* inv, int64_t tokens, int32_t topk,
+                                  int64_t n, void* dx, void* stream) {
+    if (tokens < 0 || topk < 1 || n < 1 || (dtype != RDOT_F32 && dtype != RDOT_BF16)) return RDOT_ERR_INVALID_ARG;
+    const int64_t per_vec = dtype == RDOT_BF16 ? 8 : 4;
+    if (n % per_vec || n / per_vec > 0x3fffffffLL || tokens > 0x7fffffffLL || tokens * topk > 0x7fffffffLL)
+        return RDOT_ERR_UNSUPPORTED;
+    if (tokens == 0) return RDOT_OK;
+    if (!dx_sorted || !inv || !dx) return RDOT_ERR_INVALID_ARG;
+    if (!aligned16(dx_sorted) || !aligned16(dx) || !aligned4(inv)) return RDOT_ERR_INVALID_ARG;
+    const int sms = current_sm_count();
+    if (sms <= 0) return cuda_fail(cudaGetLastError(), "cudaDeviceGetAttribute");
+    cudaError_t e = launch_moe_permute_grad(dx_sorted, dtype == RDOT_BF16, inv, tokens, topk, n, dx, sms,
+                                            static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? RDOT_OK : cuda_fail(e, "moe permute gradient launch");
+}
+
+rdot_status rdot_router_topk_grad(const void* logits, int32_t dtype, const int32_t* topk_ids, const float* topk_weights,
+                                  const float* dweights, int64_t tokens, int32_t n_experts, int32_t topk, int32_t weights,
+                                  void* dlogits, void* stream) {
+    if (tokens < 0 || n_experts < 1 || topk < 1 || topk > n_experts || (dtype != RDOT_F32 && dtype != RDOT_BF16) ||
+        (weights != RDOT_ROUTER_VALUES && weights != RDOT_ROUTER_SOFTMAX && weights != RDOT_ROUTER_SOFTMAX_TOPK))
+        return RDOT_ERR_INVALID_ARG;
+    if (n_experts > RDOT_MAX_GROUPS || topk > RDOT_ROUTER_MAX_TOPK || tokens > 0x7fffffffLL ||
+        tokens * topk > 0x7fffffffLL)
+        return RDOT_ERR_UNSUPPORTED;
+    if (tokens == 0) return RDOT_OK;
+    if (!topk_ids || !topk_weights || !dweights || !dlogits || (weights == RDOT_ROUTER_SOFTMAX && !logits))
+        return RDOT_ERR_INVALID_ARG;
+    const uintptr_t elem = dtype == RDOT_F32 ? 3u : 1u;
+    if ((reinterpret_cast<uintptr_t>(logits) & elem) || (reinterpret_cast<uintptr_t>(dlogits) & elem) ||
+        !aligned4(topk_ids) || !aligned4(topk_weights) || !aligned4(dweights))
+        return RDOT_ERR_INVALID_ARG;
+    const int sms = current_sm_count();
+    if (sms <= 0) return cuda_fail(cudaGetLastError(), "cudaDeviceGetAttribute");
+    cudaError_t e = launch_router_topk_grad(logits, dtype == RDOT_BF16, topk_ids, topk_weights, dweights, tokens,
+                                            n_experts, topk, weights, dlogits, sms, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? RDOT_OK : cuda_fail(e, "router top-k gradient launch");
+}
+
 const char* rdot_status_string(rdot_status status) {
     switch (status) {
         case RDOT_OK: return "RDOT_OK";

@@ -204,6 +204,17 @@ cudaError_t launch_mxw(const CUtensorMap& tmap_x, const CUtensorMap& tmap_dy, co
 cudaError_t launch_router_topk(const void* logits, bool bf16, long long tokens, int E, int k, int mode, int32_t* ids,
                                float* weights, int sm_count, cudaStream_t stream);
 
+// Gradients of the routing steps (route_grad.cu). order / inv as moe_permute wrote them; rows of n
+// elements, 16-byte vectors; k <= 32 and E <= 1024 for the router.
+cudaError_t launch_moe_unpermute_grad(const void* dout, const void* y_sorted, const int32_t* order, const int32_t* inv,
+                                      const float* weights, long long tokens, int k, long long n, void* dy_sorted,
+                                      float* dweights, int sm_count, cudaStream_t stream);
+cudaError_t launch_moe_permute_grad(const void* dx_sorted, bool bf16, const int32_t* inv, long long tokens, int k,
+                                    long long n, void* dx, int sm_count, cudaStream_t stream);
+cudaError_t launch_router_topk_grad(const void* logits, bool bf16, const int32_t* ids, const float* weights,
+                                    const float* dweights, long long tokens, int E, int k, int mode, void* dlogits,
+                                    int sm_count, cudaStream_t stream);
+
 // Padded-dense baseline data movement (padded.cu).
 cudaError_t launch_pad_scatter(const void* lhs, const int32_t* gs, void* lhs_pad, int32_t* uniform_gs, int M, int G,
                                int C, long long row_bytes, int grid, int32_t* status, cudaStream_t stream);

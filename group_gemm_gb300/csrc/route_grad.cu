@@ -1,0 +1,247 @@
+// route_grad.cu -- the gradients of the routing steps of route.cu: permute, un-permute, router top-k.
+//
+// With order / inv the index outputs of the permute (row p of the sorted order holds copy order[p] =
+// t*k + j, inv the other way round, -1 for none):
+//   un-permute  out[t] = sum_j w[t,j] y[inv[t,j]]    dy[p] = w[order[p]] dout[order[p] / k]
+//                                                   dw[t,j] = <dout[t], y[inv[t,j]]>
+//   permute     x_sorted[p] = x[order[p] / k]        dx[t] = sum_j dx_sorted[inv[t,j]]
+//   router      w = top-k logits, or their softmax   dlogits, see router_topk_grad_kernel
+// All three are bound by HBM: each input row is read once, each output row written once, sums are
+// kept in fp32 in a fixed order (no atomics), and rows move as 16-byte vectors.
+#include <cuda_bf16.h>
+
+#include "kernels.h"
+#include "pdl.cuh"
+#include "ptx.cuh"
+
+namespace rdot {
+
+namespace {
+
+constexpr int VEC_UNROLL = 4;   // 16-byte loads in flight per lane and operand
+
+// One 16-byte vector of E elements as fp32: 8 bf16 or 4 fp32.
+template <bool BF16>
+struct Vec {
+    static constexpr int E = BF16 ? 8 : 4;
+    __device__ __forceinline__ static void unpack(uint4 u, float (&f)[E]) {
+        const uint32_t q[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if constexpr (BF16) {
+                f[2 * i] = __uint_as_float(q[i] << 16);
+                f[2 * i + 1] = __uint_as_float(q[i] & 0xffff0000u);
+            } else {
+                f[i] = __uint_as_float(q[i]);
+            }
+        }
+    }
+    // the sum of up to 2^31 fp32 terms rounded to the output type once, to nearest even
+    __device__ __forceinline__ static uint4 pack(const float (&f)[E]) {
+        if constexpr (BF16)
+            return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
+                              pack_bf16x2(f[6], f[7]));
+        else
+            return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
+                              __float_as_uint(f[3]));
+    }
+};
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+    return v;
+}
+
+// One warp per copy f = t*k + j: reads dout[t] and y[inv[f]], writes dy[inv[f]] and dw[f]; then zeroes
+// row f of dy if no copy is placed there. Index values outside [0, T*k) count as none.
+__global__ void __launch_bounds__(256) unpermute_grad_kernel(const uint4* __restrict__ dout,
+                                                             const uint4* __restrict__ y,
+                                                             const int32_t* __restrict__ order,
+                                                             const int32_t* __restrict__ inv,
+                                                             const float* __restrict__ w, long long total, int k,
+                                                             int vec_per_row, uint4* __restrict__ dy,
+                                                             float* __restrict__ dw) {
+    grid_dependency_enter();
+    const int lane = threadIdx.x & 31;
+    const long long warp = (static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
+    const long long nwarps = (static_cast<long long>(gridDim.x) * blockDim.x) >> 5;
+    for (long long f = warp; f < total; f += nwarps) {
+        const int32_t p = __ldg(inv + f);
+        const bool kept = p >= 0 && p < total;
+        float dot = 0.f;
+        if (kept) {
+            const float wf = __ldg(w + f);
+            const uint4* d = dout + (f / k) * vec_per_row;
+            const uint4* src = y + static_cast<long long>(p) * vec_per_row;
+            uint4* dst = dy + static_cast<long long>(p) * vec_per_row;
+            for (int i0 = lane; i0 < vec_per_row; i0 += 32 * VEC_UNROLL) {
+                uint4 a[VEC_UNROLL], b[VEC_UNROLL];
+#pragma unroll
+                for (int u = 0; u < VEC_UNROLL; ++u)
+                    if (i0 + 32 * u < vec_per_row) {
+                        a[u] = __ldg(d + i0 + 32 * u);
+                        b[u] = __ldg(src + i0 + 32 * u);
+                    }
+#pragma unroll
+                for (int u = 0; u < VEC_UNROLL; ++u) {
+                    if (i0 + 32 * u >= vec_per_row) continue;
+                    float x[8], v[8];
+                    Vec<true>::unpack(a[u], x);
+                    Vec<true>::unpack(b[u], v);
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) {
+                        dot += x[c] * v[c];
+                        x[c] *= wf;
+                    }
+                    dst[i0 + 32 * u] = Vec<true>::pack(x);
+                }
+            }
+            __syncwarp();
+            dot = warp_sum(dot);
+        }
+        if (lane == 0) dw[f] = dot;
+        const int32_t o = __ldg(order + f);
+        if (o < 0 || o >= total)
+            for (int i = lane; i < vec_per_row; i += 32) dy[f * vec_per_row + i] = make_uint4(0, 0, 0, 0);
+    }
+}
+
+// One warp per (token, 32 * VEC_UNROLL vectors of its row): sums the kept copies' vectors in fp32.
+template <bool BF16>
+__global__ void __launch_bounds__(256) permute_grad_kernel(const uint4* __restrict__ dxs,
+                                                           const int32_t* __restrict__ inv, long long tokens, int k,
+                                                           int vec_per_row, uint4* __restrict__ dx) {
+    using V = Vec<BF16>;
+    grid_dependency_enter();
+    const int lane = threadIdx.x & 31;
+    const long long warp = (static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
+    const long long nwarps = (static_cast<long long>(gridDim.x) * blockDim.x) >> 5;
+    const long long chunks = (vec_per_row + 32 * VEC_UNROLL - 1) / (32 * VEC_UNROLL);
+    const long long total = tokens * k;
+    for (long long it = warp; it < tokens * chunks; it += nwarps) {
+        const long long t = it / chunks;
+        const int i0 = static_cast<int>(it - t * chunks) * 32 * VEC_UNROLL + lane;
+        float a[VEC_UNROLL][V::E];
+#pragma unroll
+        for (int u = 0; u < VEC_UNROLL; ++u)
+#pragma unroll
+            for (int c = 0; c < V::E; ++c) a[u][c] = 0.f;
+        for (int j = 0; j < k; ++j) {
+            const int32_t p = __ldg(inv + t * k + j);
+            if (p < 0 || p >= total) continue;
+            const uint4* src = dxs + static_cast<long long>(p) * vec_per_row + i0;
+            uint4 v[VEC_UNROLL];
+#pragma unroll
+            for (int u = 0; u < VEC_UNROLL; ++u)
+                if (i0 + 32 * u < vec_per_row) v[u] = __ldg(src + 32 * u);
+#pragma unroll
+            for (int u = 0; u < VEC_UNROLL; ++u) {
+                if (i0 + 32 * u >= vec_per_row) continue;
+                float x[V::E];
+                V::unpack(v[u], x);
+#pragma unroll
+                for (int c = 0; c < V::E; ++c) a[u][c] += x[c];
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < VEC_UNROLL; ++u)
+            if (i0 + 32 * u < vec_per_row) dx[t * vec_per_row + i0 + 32 * u] = V::pack(a[u]);
+    }
+}
+
+template <bool BF16>
+__device__ __forceinline__ float load_elem(const void* p, long long i) {
+    if (BF16) return __uint_as_float(static_cast<uint32_t>(__ldg(static_cast<const unsigned short*>(p) + i)) << 16);
+    return __ldg(static_cast<const float*>(p) + i);
+}
+
+template <bool BF16>
+__device__ __forceinline__ void store_elem(void* p, long long i, float v) {
+    if (BF16) static_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(v);
+    else static_cast<float*>(p)[i] = v;
+}
+
+// One warp per token. With e_j the token's k experts, w_j the router's weights, g_j their gradients
+// and s = sum_j w_j g_j:
+//   values        dl[e_j] = g_j
+//   softmax       dl[e]   = [e = e_j] w_j g_j - p_e s,  p = softmax over all E logits (recomputed)
+//   softmax_topk  dl[e_j] = w_j (g_j - s)
+// and zero for the other experts. Lane j holds copy j's expert and its term.
+template <bool BF16>
+__global__ void __launch_bounds__(256) router_topk_grad_kernel(const void* __restrict__ logits,
+                                                               const int32_t* __restrict__ ids,
+                                                               const float* __restrict__ w,
+                                                               const float* __restrict__ dw, long long tokens, int E,
+                                                               int k, int mode, void* __restrict__ dlogits) {
+    grid_dependency_enter();
+    const int lane = threadIdx.x & 31;
+    const long long warp = (static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
+    const long long nwarps = (static_cast<long long>(gridDim.x) * blockDim.x) >> 5;
+    for (long long t = warp; t < tokens; t += nwarps) {
+        const int id = lane < k ? __ldg(ids + t * k + lane) : -1;
+        const float wj = lane < k ? __ldg(w + t * k + lane) : 0.f;
+        const float gj = lane < k ? __ldg(dw + t * k + lane) : 0.f;
+        const float s = mode == RDOT_ROUTER_VALUES ? 0.f : warp_sum(wj * gj);
+        const float term = mode == RDOT_ROUTER_VALUES ? gj : mode == RDOT_ROUTER_SOFTMAX ? wj * gj : wj * (gj - s);
+        float m = 0.f, inv_sum = 0.f;
+        if (mode == RDOT_ROUTER_SOFTMAX) {
+            m = -INFINITY;
+            for (int e = lane; e < E; e += 32) m = fmaxf(m, load_elem<BF16>(logits, t * E + e));
+            __syncwarp();
+#pragma unroll
+            for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+            float sum = 0.f;
+            for (int e = lane; e < E; e += 32) sum += expf(load_elem<BF16>(logits, t * E + e) - m);
+            __syncwarp();
+            inv_sum = 1.f / warp_sum(sum);
+        }
+        for (int e0 = 0; e0 < E; e0 += 32) {
+            const int e = e0 + lane;
+            float v = 0.f;
+            if (mode == RDOT_ROUTER_SOFTMAX && e < E) v = -(expf(load_elem<BF16>(logits, t * E + e) - m) * inv_sum) * s;
+            for (int j = 0; j < k; ++j) {
+                const int ej = __shfl_sync(0xffffffffu, id, j);
+                const float tj = __shfl_sync(0xffffffffu, term, j);
+                if (ej == e) v += tj;
+            }
+            if (e < E) store_elem<BF16>(dlogits, t * E + e, v);
+        }
+    }
+}
+
+int warps_grid(long long warps, int sm_count) {
+    const long long want = (warps + 7) / 8;
+    return static_cast<int>(want < 8LL * sm_count ? want : 8LL * sm_count);
+}
+
+}  // namespace
+
+cudaError_t launch_moe_unpermute_grad(const void* dout, const void* y_sorted, const int32_t* order, const int32_t* inv,
+                                      const float* weights, long long tokens, int k, long long n, void* dy_sorted,
+                                      float* dweights, int sm_count, cudaStream_t stream) {
+    const long long total = tokens * k;
+    return launch_pdl(unpermute_grad_kernel, dim3(warps_grid(total, sm_count)), dim3(256), 0, stream,
+                      static_cast<const uint4*>(dout), static_cast<const uint4*>(y_sorted), order, inv, weights, total, k,
+                      static_cast<int>(n / 8), static_cast<uint4*>(dy_sorted), dweights);
+}
+
+cudaError_t launch_moe_permute_grad(const void* dx_sorted, bool bf16, const int32_t* inv, long long tokens, int k,
+                                    long long n, void* dx, int sm_count, cudaStream_t stream) {
+    const int vec = static_cast<int>(n / (bf16 ? 8 : 4));
+    const long long chunks = (vec + 32 * VEC_UNROLL - 1) / (32 * VEC_UNROLL);
+    const int grid = warps_grid(tokens * chunks, sm_count);
+    auto kern = bf16 ? permute_grad_kernel<true> : permute_grad_kernel<false>;
+    return launch_pdl(kern, dim3(grid), dim3(256), 0, stream, static_cast<const uint4*>(dx_sorted), inv, tokens, k, vec,
+                      static_cast<uint4*>(dx));
+}
+
+cudaError_t launch_router_topk_grad(const void* logits, bool bf16, const int32_t* ids, const float* weights,
+                                    const float* dweights, long long tokens, int E, int k, int mode, void* dlogits,
+                                    int sm_count, cudaStream_t stream) {
+    auto kern = bf16 ? router_topk_grad_kernel<true> : router_topk_grad_kernel<false>;
+    return launch_pdl(kern, dim3(warps_grid(tokens, sm_count)), dim3(256), 0, stream, logits, ids, weights, dweights,
+                      tokens, E, k, mode, dlogits);
+}
+
+}  // namespace rdot

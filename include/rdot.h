@@ -319,6 +319,53 @@ RDOT_API rdot_status rdot_router_topk(const void* logits, int32_t dtype, int64_t
 RDOT_API rdot_status rdot_moe_unpermute(const void* y_sorted, const int32_t* inv, const float* topk_weights,
                                int64_t tokens, int32_t topk, int64_t n, void* out, void* stream);
 
+/* Gradients of the routing steps, for training through the layer. They take the index outputs and
+ * the weights of the forward calls and, like them, run on the calling thread's current device and
+ * never synchronise the host. Sums are fp32 in a fixed order, rounded once. An index outside its
+ * range counts as none. T = 0 launches nothing.
+ *
+ * rdot_moe_unpermute_grad, of rdot_moe_unpermute (and of rdot_forward_combine's combine step):
+ *   dout          device bf16 [T, n]: the gradient of the combined rows
+ *   y_sorted      device bf16 [T*k, n]: the expert outputs the forward combined
+ *   order, inv    device int32 [T*k] each (from rdot_moe_permute)
+ *   topk_weights  device fp32 [T, k]
+ *   dy_sorted     device bf16 [T*k, n] out: dy_sorted[p] = topk_weights[order[p]] * dout[order[p] / k];
+ *                 zero rows where order[p] = -1 (past sum(group_sizes))
+ *   dweights      device fp32 [T, k] out: <dout[t], y_sorted[inv[t*k + j]]>; 0 for a dropped copy
+ *   n % 8 == 0 (16-byte rows), T*k < 2^31, else RDOT_ERR_UNSUPPORTED; 16-byte alignment for the
+ *   row tensors, 4 for the rest. */
+RDOT_API rdot_status rdot_moe_unpermute_grad(const void* dout, const void* y_sorted, const int32_t* order,
+                                             const int32_t* inv, const float* topk_weights, int64_t tokens,
+                                             int32_t topk, int64_t n, void* dy_sorted, float* dweights, void* stream);
+
+/* rdot_moe_permute_grad, of rdot_moe_permute's gather:
+ *   dx_sorted  device [T*k, n], dtype RDOT_F32 or RDOT_BF16: the gradient of the sorted rows
+ *   inv        device int32 [T*k] (from rdot_moe_permute)
+ *   dx         device [T, n], the same dtype, out: dx[t] = sum over the kept copies j of
+ *              dx_sorted[inv[t*k + j]], accumulated in fp32; a zero row for a token without one
+ *   rows are 16-byte multiples (n % 8 == 0 for bf16, n % 4 == 0 for fp32), T*k < 2^31, else
+ *   RDOT_ERR_UNSUPPORTED; 16-byte alignment for the row tensors, 4 for inv. */
+RDOT_API rdot_status rdot_moe_permute_grad(const void* dx_sorted, int32_t dtype, const int32_t* inv, int64_t tokens,
+                                           int32_t topk, int64_t n, void* dx, void* stream);
+
+/* rdot_router_topk_grad, of rdot_router_topk: the selection is piecewise constant, so the gradient
+ * flows through the weights alone. With e_j = topk_ids[t, j], w_j = topk_weights[t, j], g_j =
+ * dweights[t, j] and s = sum_j w_j g_j, row t of dlogits is, by `weights` (as in the forward call),
+ *   RDOT_ROUTER_VALUES        g_j at e_j
+ *   RDOT_ROUTER_SOFTMAX       [e = e_j] w_j g_j - p_e s for every e, p = softmax over all E logits
+ *   RDOT_ROUTER_SOFTMAX_TOPK  w_j (g_j - s) at e_j
+ * and 0 elsewhere.
+ *   logits        device [T, E], dtype RDOT_F32 or RDOT_BF16; only read (and only needed, else it may
+ *                 be null) for RDOT_ROUTER_SOFTMAX
+ *   topk_ids      device int32 [T, k], topk_weights device fp32 [T, k] (from rdot_router_topk)
+ *   dweights      device fp32 [T, k] (from rdot_moe_unpermute_grad)
+ *   dlogits       device [T, E] out, the same dtype as the logits; every element is written
+ * The bounds of rdot_router_topk hold. */
+RDOT_API rdot_status rdot_router_topk_grad(const void* logits, int32_t dtype, const int32_t* topk_ids,
+                                           const float* topk_weights, const float* dweights, int64_t tokens,
+                                           int32_t n_experts, int32_t topk, int32_t weights, void* dlogits,
+                                           void* stream);
+
 /* Bytes of the padded baseline's scratch for a capacity of `capacity` rows per group
  * (the padded lhs [G, capacity, K] plus the padded output [G, capacity, N] plus a small table). */
 RDOT_API rdot_status rdot_padded_workspace_size(rdot_plan_t plan, int64_t capacity, size_t* bytes);
