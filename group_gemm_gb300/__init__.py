@@ -29,14 +29,17 @@ __all__ = [
     "grad_input", "ragged_dot_gated",
     "ragged_dot_mxfp8", "padded_ragged_dot",
     "rdot_moe_unpermute_grad", "rdot_moe_permute_grad", "rdot_router_topk_grad",
+    "rdot_quantize_mxfp4", "rdot_quantize_mxfp4_weight", "rdot_mxfp4_weight_scale_bytes", "rdot_forward_mxfp4",
+    "quantize_mxfp4", "quantize_mxfp4_weight", "ragged_dot_mxfp4",
     "moe_unpermute_grad", "moe_permute_grad", "router_topk_grad", "EXPORTED_SYMBOLS",
 ]
 
 RDOT_OK, RDOT_ERR_INVALID_ARG, RDOT_ERR_UNSUPPORTED, RDOT_ERR_CUDA = 0, 1, 2, 3
 RDOT_ERR_DEVICE_TIMEOUT, RDOT_WARN_GROUP_SIZES = 4, 5
-RDOT_F32, RDOT_BF16, RDOT_E4M3 = 0, 1, 2
+RDOT_F32, RDOT_BF16, RDOT_E4M3, RDOT_E2M1 = 0, 1, 2, 3
 RDOT_MODE_FORWARD, RDOT_MODE_GRAD_WEIGHT, RDOT_MODE_FORWARD_MXFP8, RDOT_MODE_GRAD_INPUT = 0, 1, 2, 3
 RDOT_MODE_FORWARD_GATED, RDOT_MODE_GRAD_INPUT_MXFP8, RDOT_MODE_GRAD_WEIGHT_MXFP8 = 4, 5, 6
+RDOT_MODE_FORWARD_MXFP4 = 8
 RDOT_STATUS_BIT_GROUP_SIZES, RDOT_STATUS_BIT_TIMEOUT = 0x1, 0x2
 RDOT_FLAG_ROW_TILES_INNER, RDOT_FLAG_COL_TILES_INNER = 0x1, 0x2
 RDOT_FLAG_CTA_PAIR, RDOT_FLAG_NO_CTA_PAIR, RDOT_FLAG_NATURAL_ORDER = 0x4, 0x8, 0x10
@@ -55,13 +58,14 @@ EXPORTED_SYMBOLS = (
     "rdot_moe_permute", "rdot_moe_unpermute", "rdot_forward_gated", "rdot_grad_input_mxfp8", "rdot_router_topk",
     "rdot_forward_combine", "rdot_grad_weight_mxfp8",
     "rdot_moe_unpermute_grad", "rdot_moe_permute_grad", "rdot_router_topk_grad",
+    "rdot_quantize_mxfp4", "rdot_quantize_mxfp4_weight", "rdot_mxfp4_weight_scale_bytes", "rdot_forward_mxfp4",
 )
 
-_DTYPE_CODES = {"f32": RDOT_F32, "bf16": RDOT_BF16, "e4m3": RDOT_E4M3}
+_DTYPE_CODES = {"f32": RDOT_F32, "bf16": RDOT_BF16, "e4m3": RDOT_E4M3, "e2m1": RDOT_E2M1}
 _MODE_CODES = {"forward": RDOT_MODE_FORWARD, "grad_weight": RDOT_MODE_GRAD_WEIGHT,
                "forward_mxfp8": RDOT_MODE_FORWARD_MXFP8, "grad_input": RDOT_MODE_GRAD_INPUT,
                "forward_gated": RDOT_MODE_FORWARD_GATED, "grad_input_mxfp8": RDOT_MODE_GRAD_INPUT_MXFP8,
-               "grad_weight_mxfp8": RDOT_MODE_GRAD_WEIGHT_MXFP8}
+               "grad_weight_mxfp8": RDOT_MODE_GRAD_WEIGHT_MXFP8, "forward_mxfp4": RDOT_MODE_FORWARD_MXFP4}
 
 
 class RdotError(RuntimeError):
@@ -130,6 +134,10 @@ def load():
             "rdot_forward_combine": ([vp, vp, vp, vp, vp, vp, i64, ctypes.c_int32, vp, vp, vp], st),
             "rdot_router_topk": ([vp, ctypes.c_int32, i64, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, vp, vp, vp],
                                  st),
+            "rdot_quantize_mxfp4": ([vp, ctypes.c_int32, i64, i64, vp, vp, vp, vp], st),
+            "rdot_quantize_mxfp4_weight": ([vp, ctypes.c_int32, ctypes.c_int32, i64, i64, vp, vp, vp, vp], st),
+            "rdot_mxfp4_weight_scale_bytes": ([ctypes.c_int32, i64, i64, ctypes.POINTER(ctypes.c_size_t)], st),
+            "rdot_forward_mxfp4": ([vp, vp, vp, vp, vp, vp, vp, vp, vp], st),
             "rdot_moe_unpermute_grad": ([vp, vp, vp, vp, vp, i64, ctypes.c_int32, i64, vp, vp, vp], st),
             "rdot_moe_permute_grad": ([vp, ctypes.c_int32, vp, i64, ctypes.c_int32, i64, vp, vp], st),
             "rdot_router_topk_grad": ([vp, ctypes.c_int32, vp, vp, vp, i64, ctypes.c_int32, ctypes.c_int32,
@@ -260,6 +268,34 @@ def _float_dtype(t, what: str) -> int:
     if dt is None:
         raise TypeError(f"{what} must be float32 or bfloat16")
     return dt
+
+
+def rdot_quantize_mxfp4(x, codes, scales, values=None, stream=None) -> None:
+    """x [rows, K] (fp32 or bf16) -> codes uint8 [rows, K/2], scales uint8 [rows, K/32], values bf16 [rows, K]."""
+    _check(load().rdot_quantize_mxfp4(_ptr(x), _float_dtype(x, "x"), int(x.shape[0]), int(x.shape[1]), _ptr(codes),
+                                      _ptr(scales), _ptr(values), _stream(stream, x.device)), "rdot_quantize_mxfp4")
+
+
+def rdot_mxfp4_weight_scale_bytes(groups: int, k: int, n: int) -> int:
+    b = ctypes.c_size_t()
+    _check(load().rdot_mxfp4_weight_scale_bytes(int(groups), int(k), int(n), ctypes.byref(b)),
+           "rdot_mxfp4_weight_scale_bytes")
+    return b.value
+
+
+def rdot_quantize_mxfp4_weight(w, codes, scales, values=None, stream=None) -> None:
+    """w [G, K, N] (fp32 or bf16) -> codes uint8 [G, N, K/2], scales uint8 [G, ceil(N/128), ceil(K/128), 512],
+    values bf16 [G, K, N]."""
+    g, k, n = w.shape
+    _check(load().rdot_quantize_mxfp4_weight(_ptr(w), _float_dtype(w, "w"), int(g), int(k), int(n), _ptr(codes),
+                                             _ptr(scales), _ptr(values), _stream(stream, w.device)),
+           "rdot_quantize_mxfp4_weight")
+
+
+def rdot_forward_mxfp4(plan, lhs, lhs_scale, rhs, rhs_scale, group_sizes, out, workspace, stream=None) -> None:
+    _check(load().rdot_forward_mxfp4(plan, _ptr(lhs), _ptr(lhs_scale), _ptr(rhs), _ptr(rhs_scale),
+                                     _ptr(group_sizes), _ptr(out), _ptr(workspace), _stream(stream, out.device)),
+           "rdot_forward_mxfp4")
 
 
 def rdot_moe_unpermute_grad(dout, y_sorted, order, inv, topk_weights, dy_sorted, dweights, stream=None) -> None:
@@ -607,6 +643,63 @@ def moe_unpermute(y_sorted, inv, topk_weights, out=None, stream=None):
         if out is None:
             out = torch.empty((t, y_sorted.shape[1]), dtype=torch.bfloat16, device=y_sorted.device)
         rdot_moe_unpermute(y_sorted.contiguous(), inv, topk_weights.to(torch.float32).contiguous(), out, s)
+    return out
+
+
+def quantize_mxfp4(x, values=False, stream=None):
+    """MXFP4 quantisation of x [rows, K] (fp32 or bf16) in blocks of 32 along K: returns ``(codes uint8
+    [rows, K/2], scales uint8 [rows, K/32])``, and with ``values`` also the bf16 [rows, K] they stand for."""
+    import torch
+    if x.dim() != 2:
+        raise ValueError("x must be [rows, K]")
+    m, k = x.shape
+    s = _run_stream(stream, x.device)
+    with torch.cuda.stream(s):
+        codes = torch.empty((m, k // 2), dtype=torch.uint8, device=x.device)
+        scales = torch.empty((m, k // 32), dtype=torch.uint8, device=x.device)
+        v = torch.empty((m, k), dtype=torch.bfloat16, device=x.device) if values else None
+        rdot_quantize_mxfp4(x.contiguous(), codes, scales, v, s)
+    return (codes, scales, v) if values else (codes, scales)
+
+
+def quantize_mxfp4_weight(w, values=False, stream=None):
+    """MXFP4 quantisation of weights w [G, K, N] (fp32 or bf16) along K, laid out for
+    :func:`ragged_dot_mxfp4`: returns ``(codes uint8 [G, N, K/2], scales uint8 [G, ceil(N/128), ceil(K/128),
+    512])``, and with ``values`` also the bf16 [G, K, N] they stand for."""
+    import torch
+    if w.dim() != 3:
+        raise ValueError("w must be [G, K, N]")
+    g, k, n = w.shape
+    s = _run_stream(stream, w.device)
+    with torch.cuda.stream(s):
+        codes = torch.empty((g, n, k // 2), dtype=torch.uint8, device=w.device)
+        scales = torch.empty((g, -(-n // 128), -(-k // 128), 512), dtype=torch.uint8, device=w.device)
+        v = torch.empty((g, k, n), dtype=torch.bfloat16, device=w.device) if values else None
+        rdot_quantize_mxfp4_weight(w.contiguous(), codes, scales, v, s)
+    return (codes, scales, v) if values else (codes, scales)
+
+
+def ragged_dot_mxfp4(lhs_q, lhs_scale, rhs_q, rhs_scale, group_sizes, out=None, stream=None):
+    """MXFP4 forward: codes and scales of :func:`quantize_mxfp4` (lhs, M rows in group order) and of
+    :func:`quantize_mxfp4_weight` (rhs); bf16 out [M, N], rows past ``sum(group_sizes)`` zero."""
+    import torch
+    m, kh = lhs_q.shape
+    g, n, kh2 = rhs_q.shape
+    k = 2 * kh
+    if (kh2 != kh or group_sizes.shape != (g,) or lhs_scale.shape != (m, k // 32)
+            or rhs_scale.shape != (g, -(-n // 128), -(-k // 128), 512)):
+        raise ValueError("shape mismatch between lhs, rhs, their scales and group_sizes")
+    if any(t.dtype != torch.uint8 for t in (lhs_q, lhs_scale, rhs_q, rhs_scale)):
+        raise TypeError("codes and scales must be uint8")
+    s = _run_stream(stream, lhs_q.device)
+    key = ("mxfp4", m, k, n, g, lhs_q.device)
+    plan, ws = _cached_plan(key, s, m=m, k=k, n=n, groups=g, mode="forward_mxfp4", in_dtype="e2m1", out_dtype="bf16",
+                            device=lhs_q.device)
+    with torch.cuda.stream(s):
+        if out is None:
+            out = torch.empty((m, n), dtype=torch.bfloat16, device=lhs_q.device)
+        rdot_forward_mxfp4(plan.handle, lhs_q.contiguous(), lhs_scale.contiguous(), rhs_q.contiguous(),
+                           rhs_scale.contiguous(), group_sizes.to(torch.int32).contiguous(), out, ws, s)
     return out
 
 

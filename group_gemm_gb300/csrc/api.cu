@@ -82,7 +82,8 @@ struct rdot_plan_s {
     int cc_major = 0, cc_minor = 0;
     int kind = 0;          // 0: SIMT fp32 forward, 1: tcgen05 bf16 forward, 2: tcgen05 grad-weight, 3: MXFP8,
                            // 4: tcgen05 data gradient (the forward kernels, K-major B),
-                           // 5: gated up projection (CTA pairs), 6: MXFP8 data gradient
+                           // 5: gated up projection (CTA pairs), 6: MXFP8 data gradient, 7: MXFP8
+                           // grad-weight, 8: MXFP4 forward
     int tile_m = 0, tile_n = 0;
     int m_inner = 1;
     int grid = 1;
@@ -188,6 +189,18 @@ bool want_mx_skinny(const rdot_problem& p) {
     return p.tile_n == 0 && p.m <= kSkinnyMaxRows;
 }
 
+// The MXFP4 forward takes its swapped kernel (mxfp4_skinny.cu) while the rows, spread evenly over
+// min(M, G) groups, come to at most kMx4SkinnyRows a group: then it streams weights and the 128 token
+// rows of a pair tile would be mostly empty.
+constexpr long long kMx4SkinnyRows = 32;
+
+bool want_mx4_skinny(const rdot_problem& p) {
+    if (p.flags & RDOT_FLAG_SKINNY) return true;
+    if (p.flags & (RDOT_FLAG_NO_SKINNY | RDOT_FLAG_CTA_PAIR)) return false;
+    const long long routed = std::max<long long>(1, std::min<long long>(p.m, p.groups));
+    return (p.m + routed - 1) / routed <= kMx4SkinnyRows;
+}
+
 // Token rows per tile of that kernel: 16 (a sixth stage of weights in flight) when, with the
 // rows spread evenly over min(M, G) groups, 16-row tiles still leave at most two work items per
 // SM; else 32 (half the token tiles re-reading each weight slab).
@@ -223,10 +236,10 @@ rdot_status check_problem(const rdot_problem* p) {
     if ((p->flags & RDOT_FLAG_CTA_PAIR) && (p->flags & RDOT_FLAG_NO_CTA_PAIR)) return RDOT_ERR_INVALID_ARG;
     if ((p->flags & RDOT_FLAG_SKINNY) && (p->flags & RDOT_FLAG_NO_SKINNY)) return RDOT_ERR_INVALID_ARG;
     // the swapped small-row kernels: the bf16 forward (64- or 128-column items) and the MXFP8
-    // forward (128-column items), on single CTAs
+    // forward (128-column items), on single CTAs; the MXFP4 forward has its own (no tile choice)
     if (p->flags & RDOT_FLAG_SKINNY) {
         const bool bf16_fwd = p->mode == RDOT_MODE_FORWARD && p->in_dtype == RDOT_BF16;
-        const bool mx_fwd = p->mode == RDOT_MODE_FORWARD_MXFP8;
+        const bool mx_fwd = p->mode == RDOT_MODE_FORWARD_MXFP8 || p->mode == RDOT_MODE_FORWARD_MXFP4;
         if ((!bf16_fwd && !mx_fwd) || (p->flags & RDOT_FLAG_CTA_PAIR) ||
             (p->tile_n != 0 && p->tile_n != SKINNY_BN && !(bf16_fwd && p->tile_n == 64)))
             return RDOT_ERR_UNSUPPORTED;
@@ -280,6 +293,11 @@ rdot_status check_problem(const rdot_problem* p) {
         case RDOT_MODE_FORWARD_MXFP8:
             if (p->in_dtype != RDOT_E4M3 || p->out_dtype != RDOT_BF16) return RDOT_ERR_UNSUPPORTED;
             if (p->k % 32 || p->n % 16) return RDOT_ERR_UNSUPPORTED;   // MX block 32; 16-byte row pitch
+            return RDOT_OK;
+        case RDOT_MODE_FORWARD_MXFP4:
+            if (p->in_dtype != RDOT_E2M1 || p->out_dtype != RDOT_BF16 || p->tile_n != 0) return RDOT_ERR_UNSUPPORTED;
+            if ((p->flags & RDOT_FLAG_NO_CTA_PAIR) && !(p->flags & RDOT_FLAG_SKINNY)) return RDOT_ERR_UNSUPPORTED;
+            if (p->k % 32 || p->n % 8) return RDOT_ERR_UNSUPPORTED;   // MX block 32; 16-byte output rows
             return RDOT_OK;
         default:
             return RDOT_ERR_INVALID_ARG;
@@ -380,6 +398,35 @@ rdot_status rdot_plan(const rdot_problem* problem, int device, rdot_plan_t* plan
         // small average groups: interleave the tiles of groups with 2+ row tiles with the
         // others so every wave mixes tensor-core-bound and weight-streaming work
         pl->big_mt = (!want_pair && !(p.flags & RDOT_FLAG_NATURAL_ORDER)) ? 2 : 0;
+    } else if (p.mode == RDOT_MODE_FORWARD_MXFP4) {
+        if (prop.major != 10) {
+            delete pl;
+            return RDOT_ERR_UNSUPPORTED;
+        }
+        pl->kind = 8;
+        pl->skinny = want_mx4_skinny(p);
+        pl->pair = !pl->skinny;
+        pl->tile_m = pl->skinny ? MX4_SKINNY_ROWS : TC2_BM;
+        pl->tile_n = pl->skinny ? 32 : 256;   // the swapped kernel's work is counted in 32-column quarters
+        if (pl->skinny) pl->m_inner = 0;
+        const long long nt = (p.n + pl->tile_n - 1) / pl->tile_n;
+        // tiles, and the rows of the weight scales' tensor map, are numbered in 32 bits
+        if (((p.m + pl->tile_m - 1) / pl->tile_m + p.groups) > 0x7fffffffLL / nt ||
+            (p.n + 127) / 128 > 0x7fffffffLL / p.groups) {
+            delete pl;
+            return RDOT_ERR_UNSUPPORTED;
+        }
+        const long long bound = forward_tile_bound(p.m, p.groups, pl->tile_m, static_cast<int>(nt));
+        if (pl->pair) {
+            const int clusters = mxfp4_pair_max_clusters(p.groups);
+            if (clusters <= 0) {
+                delete pl;
+                return cuda_fail(cudaGetLastError(), "cudaOccupancyMaxActiveClusters");
+            }
+            pl->grid = 2 * static_cast<int>(std::max<long long>(1, std::min<long long>(bound, clusters)));
+        } else {
+            pl->grid = static_cast<int>(std::max<long long>(1, std::min<long long>(bound, pl->sm_count)));
+        }
     } else if (p.mode == RDOT_MODE_GRAD_WEIGHT_MXFP8) {
         if (prop.major != 10) {
             delete pl;
@@ -1342,6 +1389,99 @@ rdot_status rdot_router_topk(const void* logits, int32_t dtype, int64_t tokens, 
     cudaError_t e = launch_router_topk(logits, dtype == RDOT_BF16, tokens, n_experts, topk, weights, topk_ids,
                                        topk_weights, sms, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? RDOT_OK : cuda_fail(e, "router top-k launch");
+}
+
+rdot_status rdot_quantize_mxfp4(const void* x, int32_t dtype, int64_t rows, int64_t k, uint8_t* codes,
+                                uint8_t* scales, void* values, void* stream) {
+    if (rows < 0 || k < 1 || (dtype != RDOT_F32 && dtype != RDOT_BF16)) return RDOT_ERR_INVALID_ARG;
+    if (k % 32 || k > 0x7fffffffLL || rows > (1LL << 46) / k) return RDOT_ERR_UNSUPPORTED;
+    if (rows == 0) return RDOT_OK;
+    if (!x || !codes || !scales) return RDOT_ERR_INVALID_ARG;
+    if (!aligned16(x) || !aligned16(codes) || (values && !aligned16(values))) return RDOT_ERR_INVALID_ARG;
+    const int sms = current_sm_count();
+    if (sms <= 0) return cuda_fail(cudaGetLastError(), "cudaDeviceGetAttribute");
+    cudaError_t e = launch_quantize_rows(x, dtype == RDOT_BF16, rows * k, codes, scales, values, sms,
+                                         static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? RDOT_OK : cuda_fail(e, "mxfp4 quantise launch");
+}
+
+rdot_status rdot_mxfp4_weight_scale_bytes(int32_t groups, int64_t k, int64_t n, size_t* bytes) {
+    if (!bytes || groups < 1 || k < 1 || n < 1) return RDOT_ERR_INVALID_ARG;
+    if (groups > RDOT_MAX_GROUPS || k % 32 || k > 0x7fffffffLL || n > 0x7fffffffLL) return RDOT_ERR_UNSUPPORTED;
+    *bytes = static_cast<size_t>(groups) * static_cast<size_t>((n + 127) / 128) * static_cast<size_t>((k + 127) / 128) *
+             MX4_ATOM_BYTES;
+    return RDOT_OK;
+}
+
+rdot_status rdot_quantize_mxfp4_weight(const void* w, int32_t dtype, int32_t groups, int64_t k, int64_t n,
+                                       uint8_t* codes, uint8_t* scales, void* values, void* stream) {
+    if (groups < 1 || k < 1 || n < 1 || (dtype != RDOT_F32 && dtype != RDOT_BF16)) return RDOT_ERR_INVALID_ARG;
+    if (groups > RDOT_MAX_GROUPS || k % 32 || n % 8 || k > 0x7fffffffLL || n > 0x7fffffffLL ||
+        2 * ((n + 127) / 128) * ((k + 255) / 256) > 0x7fffffffLL / groups)
+        return RDOT_ERR_UNSUPPORTED;
+    if (!w || !codes || !scales) return RDOT_ERR_INVALID_ARG;
+    if (!aligned16(w) || !aligned16(codes) || !aligned16(scales) || (values && !aligned16(values)))
+        return RDOT_ERR_INVALID_ARG;
+    cudaError_t e = launch_quantize_weight(w, dtype == RDOT_BF16, groups, static_cast<int>(k), static_cast<int>(n), codes,
+                                           scales, values, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? RDOT_OK : cuda_fail(e, "mxfp4 weight quantise launch");
+}
+
+rdot_status rdot_forward_mxfp4(rdot_plan_t plan, const void* lhs, const uint8_t* lhs_scale, const void* rhs,
+                               const uint8_t* rhs_scale, const int32_t* group_sizes, void* out, void* workspace,
+                               void* stream) {
+    if (!plan || !group_sizes || !workspace) return RDOT_ERR_INVALID_ARG;
+    const rdot_problem& p = plan->p;
+    if (p.mode != RDOT_MODE_FORWARD_MXFP4 || plan->kind != 8) return RDOT_ERR_INVALID_ARG;
+    if (p.m == 0) return RDOT_OK;
+    if (!lhs || !rhs || !out || !lhs_scale || !rhs_scale) return RDOT_ERR_INVALID_ARG;
+    if (!aligned16(lhs) || !aligned16(rhs) || !aligned16(rhs_scale) || !aligned16(out) || !aligned16(workspace) ||
+        !aligned4(group_sizes))
+        return RDOT_ERR_INVALID_ARG;
+    DeviceGuard dg(plan->device);
+    if (!dg.ok) return cuda_fail(cudaGetLastError(), "cudaSetDevice");
+    Mx4Args a{};
+    a.group_sizes = group_sizes;
+    a.lhs_scale = lhs_scale;
+    a.rhs_scale = rhs_scale;
+    a.out = out;
+    a.M = static_cast<int>(p.m);
+    a.K = static_cast<int>(p.k);
+    a.N = static_cast<int>(p.n);
+    a.G = p.groups;
+    a.NT = static_cast<int>((p.n + plan->tile_n - 1) / plan->tile_n);
+    a.NB = static_cast<int>((p.n + 127) / 128);
+    a.KA = static_cast<int>((p.k + 127) / 128);
+    a.KS = static_cast<int>((p.k + MX4_STAGE_K - 1) / MX4_STAGE_K);
+    a.KB = static_cast<int>(p.k / 32);
+    // rows of lhs scales are read 8 or 4 bytes at a time where every row starts on such a boundary
+    const uintptr_t sp = reinterpret_cast<uintptr_t>(lhs_scale);
+    a.scale_vec = (a.KB % 8 == 0 && sp % 8 == 0) ? 8 : (a.KB % 4 == 0 && sp % 4 == 0) ? 4 : 1;
+    a.m_inner = plan->m_inner;
+    a.status = static_cast<int32_t*>(workspace);
+    a.timeout_ns = plan->timeout_ns;
+    // code rows of K/2 bytes, boxes of 128 bytes (256 elements) x the kernel's rows or columns
+    const uint64_t kb = static_cast<uint64_t>(p.k / 2);
+    CUtensorMap map_a, map_b;
+    rdot_status st = encode_2d(&map_a, CU_TENSOR_MAP_DATA_TYPE_UINT8, lhs, kb, p.m, kb, MX4_STAGE_BYTES,
+                               plan->skinny ? 16 : 128);
+    if (st == RDOT_OK)
+        st = encode_3d(&map_b, CU_TENSOR_MAP_DATA_TYPE_UINT8, rhs, kb, p.n, p.groups, kb, p.n * kb, MX4_STAGE_BYTES,
+                       plan->skinny ? 32 : 128, 1);
+    if (st != RDOT_OK) return st;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    cudaError_t e;
+    if (plan->skinny) {
+        e = launch_mxfp4_skinny(map_a, map_b, a, plan->grid, s);
+    } else {
+        CUtensorMap map_sfb;
+        st = encode_2d(&map_sfb, CU_TENSOR_MAP_DATA_TYPE_UINT32, rhs_scale,
+                       static_cast<uint64_t>(a.KA) * (MX4_ATOM_BYTES / 4), static_cast<uint64_t>(p.groups) * a.NB,
+                       static_cast<uint64_t>(a.KA) * MX4_ATOM_BYTES, 2 * MX4_ATOM_BYTES / 4, 2, CU_TENSOR_MAP_SWIZZLE_NONE);
+        if (st != RDOT_OK) return st;
+        e = launch_mxfp4_pair(map_a, map_b, map_sfb, a, plan->grid, s);
+    }
+    return e == cudaSuccess ? RDOT_OK : cuda_fail(e, "mxfp4 launch");
 }
 
 rdot_status rdot_moe_unpermute_grad(const void* dout, const void* y_sorted, const int32_t* order, const int32_t* inv,

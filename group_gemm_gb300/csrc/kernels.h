@@ -204,6 +204,46 @@ cudaError_t launch_mxw(const CUtensorMap& tmap_x, const CUtensorMap& tmap_dy, co
 cudaError_t launch_router_topk(const void* logits, bool bf16, long long tokens, int E, int k, int mode, int32_t* ids,
                                float* weights, int sm_count, cudaStream_t stream);
 
+// MXFP4 (mxfp4.cuh): E2M1 codes [rows, K/2], one E8M0 scale per 32 elements of K.
+constexpr int MX4_STAGE_BYTES = 128;   // code bytes of a row per K stage
+constexpr int MX4_STAGE_K = 256;       // elements of a row per K stage
+constexpr int MX4_ATOM_BYTES = 512;    // scales of 128 rows x 4 blocks of 32
+
+struct Mx4Args {
+    const int32_t* group_sizes;   // device [G]
+    const uint8_t* lhs_scale;     // device [M, K/32]
+    const uint8_t* rhs_scale;     // device [G, NB, KA, 512]
+    void* out;                    // device bf16 [M, N]
+    int M, K, N, G;
+    int NT;                       // column tiles: 256 wide (pairs), 32 wide (the swapped kernel)
+    int NB;                       // 128-column scale atoms across N
+    int KA;                       // 128-element scale atoms along K
+    int KS;                       // K stages of 256 elements
+    int KB;                       // scale blocks along K (K / 32)
+    int scale_vec;                // bytes a lhs scale row can be read by: 8, 4 or 1
+    int m_inner;
+    int32_t* status;
+    uint64_t timeout_ns;
+};
+
+// MXFP4 forward on CTA pairs (mxfp4_tc2.cu), 256 x 256 tiles. tmap_a: lhs codes [M, K/2] uint8, box
+// (128, 128); tmap_b: rhs codes [G, N, K/2] as (K/2, N, G), box (128, 128, 1); both 128-byte swizzled;
+// tmap_sfb: the rhs scale atoms as words, rows (G NB) of 128 KA words, box (256, 2), no swizzle.
+cudaError_t launch_mxfp4_pair(const CUtensorMap& tmap_a, const CUtensorMap& tmap_b, const CUtensorMap& tmap_sfb,
+                              const Mx4Args& a, int grid, cudaStream_t stream);
+int mxfp4_pair_max_clusters(int G);
+// MXFP4 forward for a few rows per group (mxfp4_skinny.cu): tmap_x: lhs codes, box (128, 16); tmap_w: rhs
+// codes, box (128, 32, 1); a.NT counts 32-column quarters.
+constexpr int MX4_SKINNY_ROWS = 64;   // token rows per tile
+cudaError_t launch_mxfp4_skinny(const CUtensorMap& tmap_x, const CUtensorMap& tmap_w, const Mx4Args& a, int grid,
+                                cudaStream_t stream);
+// MXFP4 quantisation (mxfp4_quant.cu) of fp32 or bf16 elements: rows as one array of 32-element blocks, and
+// weights [groups, K, N] to codes [groups, N, K/2] and scale atoms. values (bf16, x's layout) may be null.
+cudaError_t launch_quantize_rows(const void* x, bool bf16, long long elements, uint8_t* codes, uint8_t* scales,
+                                 void* values, int sm_count, cudaStream_t stream);
+cudaError_t launch_quantize_weight(const void* w, bool bf16, int groups, int K, int N, uint8_t* codes, uint8_t* scales,
+                                   void* values, cudaStream_t stream);
+
 // Gradients of the routing steps (route_grad.cu). order / inv as moe_permute wrote them; rows of n
 // elements, 16-byte vectors; k <= 32 and E <= 1024 for the router.
 cudaError_t launch_moe_unpermute_grad(const void* dout, const void* y_sorted, const int32_t* order, const int32_t* inv,

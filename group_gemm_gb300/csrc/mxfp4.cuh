@@ -1,0 +1,78 @@
+// mxfp4.cuh -- what the MXFP4 kernels share: the block-scaled 4-bit MMA and the scale blocks.
+//
+// Number format (OCP Microscaling Formats v1.0, MXFP4): E2M1 elements, two per byte with the lower
+// index in the low nibble, one E8M0 scale (value 2^(s-127), 255 = NaN) per 32 consecutive elements
+// along the contraction. Both operands are K-major: a row's codes are K/2 contiguous bytes.
+//
+// A K stage is 128 code bytes (256 elements) of a row, one 128-byte swizzle row: four MMAs of K = 64
+// (tcgen05.mma kind::mxf4, scale_vec::2X: two scales per row and MMA). The scales of 128 rows x 4
+// consecutive scale blocks (128 elements) form a 512-byte atom, byte 16 (r % 32) + 4 (r / 32) + kblock;
+// tcgen05.cp .32x128b.warpx4 copies it into 4 tensor-memory columns, replicated over the four lane
+// quarters, and the MMA reads the scales of rows 32q .. 32q+31 from column q. One atom serves two
+// MMAs: scale-factor id 0 picks the word's bytes 0-1, id 2 its bytes 2-3.
+#pragma once
+
+#include <stdint.h>
+
+#include "kernels.h"
+#include "ptx.cuh"
+
+namespace rdot {
+
+// Instruction descriptor for kind::mxf4 (32 bits): [4,6) B scale-factor id, [7,10) A format (1 = E2M1),
+// [10,12) B format (1 = E2M1), [17,23) N >> 3, [23] scale type (1 = UE8M0), [27,29) M >> 7, [29,31) A
+// scale-factor id, [31] 0: K = 64. Both operands are K-major; D is fp32.
+__device__ __forceinline__ constexpr uint32_t idesc_mxf4(int m, int n, uint32_t sf_id) {
+    return (sf_id << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(n >> 3) << 17) | (1u << 23) |
+           (static_cast<uint32_t>(m >> 7) << 27) | (sf_id << 29);
+}
+
+template <int CTAS>
+__device__ __forceinline__ void mma_mxf4(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                         uint32_t sfa_tmem, uint32_t sfb_tmem, uint32_t accumulate) {
+    if constexpr (CTAS == 1)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "setp.ne.b32 p, %6, 0;\n\t"
+            "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(
+                d_tmem),
+            "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sfa_tmem), "r"(sfb_tmem), "r"(accumulate)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "setp.ne.b32 p, %6, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(
+                d_tmem),
+            "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sfa_tmem), "r"(sfb_tmem), "r"(accumulate)
+            : "memory");
+}
+
+template <int CTAS>
+__device__ __forceinline__ void tmem_cp_scales(uint32_t taddr, uint64_t sdesc) {
+    if constexpr (CTAS == 1)
+        tmem_cp_32x128b_warpx4(taddr, sdesc);
+    else
+        asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(sdesc) : "memory");
+}
+
+// The 8 scale bytes of K stage ks of row `row`; blocks past K read as 0 (their codes are zeros).
+__device__ __forceinline__ uint2 lhs_scale_stage(const Mx4Args& a, long long row, int ks) {
+    const uint8_t* p = a.lhs_scale + row * a.KB + 8 * ks;
+    if (a.scale_vec == 8) return __ldg(reinterpret_cast<const uint2*>(p));
+    const int avail = a.KB - 8 * ks;
+    uint2 v = make_uint2(0u, 0u);
+    if (a.scale_vec == 4) {
+        v.x = __ldg(reinterpret_cast<const uint32_t*>(p));
+        if (avail > 4) v.y = __ldg(reinterpret_cast<const uint32_t*>(p) + 1);
+        return v;
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        if (j < avail) v.x |= static_cast<uint32_t>(__ldg(p + j)) << (8 * j);
+        if (j + 4 < avail) v.y |= static_cast<uint32_t>(__ldg(p + 4 + j)) << (8 * j);
+    }
+    return v;
+}
+
+}  // namespace rdot

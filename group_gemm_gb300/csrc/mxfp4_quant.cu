@@ -1,0 +1,232 @@
+// mxfp4_quant.cu -- MXFP4 quantisation of activation rows and of a layer's weights.
+//
+// Rule (OCP Microscaling Formats v1.0): a block of 32 elements along the contraction with largest
+// magnitude amax gets the scale 2^(floor(log2 amax) - 2), at least 2^-127 (2 = the largest E2M1
+// exponent); each element is divided by it (exact: a power of two), rounded to E2M1 to nearest even
+// and saturated at 6, its sign kept. With E the biased fp32 exponent of amax the scale byte is
+// max(E - 2, 0). A block with a NaN or an infinity has no finite scale: byte 255, codes 0, values NaN.
+// The optional values, code x scale, are bf16 without rounding: two significant bits and exponents
+// from -128 to 127 fit it (its subnormals reach 2^-133).
+//
+// Both kernels are HBM-bound streams: each element is read once.
+#include <cuda_bf16.h>
+
+#include "kernels.h"
+#include "pdl.cuh"
+#include "ptx.cuh"
+
+namespace rdot {
+
+namespace {
+
+// Scale byte of a block from the largest |x| as fp32 bits (NaN and infinity compare above all numbers).
+__device__ __forceinline__ uint32_t scale_byte(uint32_t amax_bits) {
+    if (amax_bits >= 0x7f800000u) return 255u;
+    const uint32_t e = amax_bits >> 23;
+    return e > 2u ? e - 2u : 0u;
+}
+
+// 2^(127 - s) and 2^(s - 127) as fp32; s <= 252.
+__device__ __forceinline__ float inverse_scale(uint32_t s) { return __uint_as_float((254u - s) << 23); }
+__device__ __forceinline__ float scale_value(uint32_t s) { return __uint_as_float(s ? s << 23 : 0x00400000u); }
+
+// Eight elements (already divided by the scale) as E2M1 codes, element 0 in the lowest nibble.
+__device__ __forceinline__ uint32_t e2m1x8(const float (&v)[8]) {
+    uint32_t r;
+    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b2, %6, %5;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n\t"
+        "mov.b32 %0, {b0, b1, b2, b3};\n\t}"
+        : "=r"(r)
+        : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]));
+    return r;
+}
+
+// The value of an E2M1 code in the low nibble of c: magnitudes 0, 1/2, 1, 3/2, 2, 3, 4, 6. Codes >= 2
+// are (1 + m/2) 2^(e-1), which is the code's bits moved into an fp32's.
+__device__ __forceinline__ float e2m1_value(uint32_t c) {
+    const uint32_t mag = c & 7u;
+    const float f = mag < 2u ? 0.5f * static_cast<float>(mag) : __uint_as_float((mag << 22) + (126u << 23));
+    return (c & 8u) ? -f : f;
+}
+
+__device__ __forceinline__ float unpack_bf16(uint32_t w, int hi) {
+    return __uint_as_float(hi ? (w & 0xffff0000u) : (w << 16));
+}
+
+// Rows: the blocks of all rows are consecutive, so the tensor is one array of 32-element blocks. Four
+// lanes hold a block, 8 elements each.
+template <bool BF16, bool VALUES>
+__global__ void __launch_bounds__(256) quantize_rows_kernel(const uint4* __restrict__ x, long long vecs,
+                                                            uint32_t* __restrict__ codes,
+                                                            uint8_t* __restrict__ scales,
+                                                            uint4* __restrict__ values) {
+    grid_dependency_enter();
+    const long long step = static_cast<long long>(gridDim.x) * blockDim.x;
+    // vecs is a multiple of 4: the four lanes of a block run together
+    for (long long i = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x; i < vecs; i += step) {
+        float v[8];
+        if (BF16) {
+            const uint4 u = __ldg(x + i);
+            const uint32_t q[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = unpack_bf16(q[j >> 1], j & 1);
+        } else {
+            const uint4 u0 = __ldg(x + 2 * i), u1 = __ldg(x + 2 * i + 1);
+            const uint32_t q[8] = {u0.x, u0.y, u0.z, u0.w, u1.x, u1.y, u1.z, u1.w};
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = __uint_as_float(q[j]);
+        }
+        uint32_t amax = 0;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) amax = max(amax, __float_as_uint(v[j]) & 0x7fffffffu);
+        const uint32_t group = 0xfu << (threadIdx.x & 28);
+        amax = max(amax, __shfl_xor_sync(group, amax, 1));
+        amax = max(amax, __shfl_xor_sync(group, amax, 2));
+        const uint32_t s = scale_byte(amax);
+        const bool nan = s == 255u;
+        const float inv = nan ? 0.f : inverse_scale(s);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] *= inv;
+        const uint32_t c = nan ? 0u : e2m1x8(v);
+        codes[i] = c;
+        if ((threadIdx.x & 3) == 0) scales[i >> 2] = static_cast<uint8_t>(s);
+        if (VALUES) {
+            const float sv = nan ? __uint_as_float(0x7fffffffu) : scale_value(s);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = e2m1_value(c >> (4 * j)) * sv;
+            values[i] = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                                   pack_bf16x2(v[6], v[7]));
+        }
+    }
+}
+
+// Weights [G, K, N] -> codes [G, N, K/2] and scale atoms. A block of 8 warps takes 64 columns x 256 rows
+// of one group: warp w the 32 rows of scale block w, lane l columns 2l and 2l + 1, so a scale block of
+// a column lies in one thread's registers; the codes are turned through shared memory into rows of
+// up to 128 bytes.
+constexpr int QW_COLS = 64;
+constexpr int QW_BLOCKS = 8;    // scale blocks (32 rows each) per thread block
+constexpr int QW_PITCH = 144;   // shared bytes of a column's codes (128) plus 16 against bank conflicts
+
+template <bool BF16, bool VALUES>
+__global__ void __launch_bounds__(256) quantize_weight_kernel(const void* __restrict__ w, int K, int N, int NT, int KC,
+                                                              uint8_t* __restrict__ codes,
+                                                              uint8_t* __restrict__ scales,
+                                                              uint32_t* __restrict__ values) {
+    __shared__ __align__(16) uint8_t tile[QW_COLS * QW_PITCH];
+    __shared__ __align__(8) uint8_t sc[QW_COLS][QW_BLOCKS];
+    grid_dependency_enter();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int kc = blockIdx.x % KC;
+    const int nt = (blockIdx.x / KC) % NT;
+    const long long g = blockIdx.x / KC / NT;
+    const int KB = K / 32;
+    const int kb = kc * QW_BLOCKS + warp;
+    const int n = nt * QW_COLS + 2 * lane;   // N is even: both columns are inside or both past it
+    const bool live = kb < KB && n < N;
+    uint32_t s0 = 0, s1 = 0;
+    if (live) {
+        const long long base = (g * K + 32LL * kb) * N + n;   // element index of (row 0, column n)
+        float c0[32], c1[32];
+#pragma unroll
+        for (int r = 0; r < 32; ++r) {
+            if (BF16) {
+                const uint32_t u = __ldg(reinterpret_cast<const uint32_t*>(w) + ((base + static_cast<long long>(r) * N) >> 1));
+                c0[r] = unpack_bf16(u, 0);
+                c1[r] = unpack_bf16(u, 1);
+            } else {
+                const float2 u = __ldg(reinterpret_cast<const float2*>(w) + ((base + static_cast<long long>(r) * N) >> 1));
+                c0[r] = u.x;
+                c1[r] = u.y;
+            }
+        }
+        uint32_t m0 = 0, m1 = 0;
+#pragma unroll
+        for (int r = 0; r < 32; ++r) {
+            m0 = max(m0, __float_as_uint(c0[r]) & 0x7fffffffu);
+            m1 = max(m1, __float_as_uint(c1[r]) & 0x7fffffffu);
+        }
+        s0 = scale_byte(m0);
+        s1 = scale_byte(m1);
+        const bool nan0 = s0 == 255u, nan1 = s1 == 255u;
+        const float i0 = nan0 ? 0.f : inverse_scale(s0), i1 = nan1 ? 0.f : inverse_scale(s1);
+        const float v0 = nan0 ? __uint_as_float(0x7fffffffu) : scale_value(s0);
+        const float v1 = nan1 ? __uint_as_float(0x7fffffffu) : scale_value(s1);
+        uint32_t q0[4], q1[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float a[8], b[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                a[j] = c0[8 * i + j] * i0;
+                b[j] = c1[8 * i + j] * i1;
+            }
+            q0[i] = nan0 ? 0u : e2m1x8(a);
+            q1[i] = nan1 ? 0u : e2m1x8(b);
+            if (VALUES) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    values[(base + static_cast<long long>(8 * i + j) * N) >> 1] =
+                        pack_bf16x2(e2m1_value(q0[i] >> (4 * j)) * v0, e2m1_value(q1[i] >> (4 * j)) * v1);
+            }
+        }
+        *reinterpret_cast<uint4*>(tile + (2 * lane) * QW_PITCH + 16 * warp) = make_uint4(q0[0], q0[1], q0[2], q0[3]);
+        *reinterpret_cast<uint4*>(tile + (2 * lane + 1) * QW_PITCH + 16 * warp) = make_uint4(q1[0], q1[1], q1[2], q1[3]);
+    }
+    sc[2 * lane][warp] = static_cast<uint8_t>(s0);       // 0 past K and N
+    sc[2 * lane + 1][warp] = static_cast<uint8_t>(s1);
+    __syncthreads();
+    // codes: four threads per column, 32 bytes (two scale blocks) each
+    {
+        const int c = threadIdx.x >> 2, part = threadIdx.x & 3;
+        const int col = nt * QW_COLS + c;
+        if (col < N) {
+            uint4* dst = reinterpret_cast<uint4*>(codes + ((g * N + col) * KB + kc * QW_BLOCKS) * 16);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int b = 2 * part + i;
+                if (kc * QW_BLOCKS + b < KB) dst[b] = *reinterpret_cast<const uint4*>(tile + c * QW_PITCH + 16 * b);
+            }
+        }
+    }
+    // scales: one 4-byte word per column and atom of 4 blocks
+    if (threadIdx.x < 2 * QW_COLS) {
+        const int c = threadIdx.x & (QW_COLS - 1), half = threadIdx.x / QW_COLS;
+        const int KA = (KB + 3) / 4, NB = (N + 127) / 128;
+        const int ka = kc * (QW_BLOCKS / 4) + half;
+        const int col = (nt * QW_COLS + c) & 127;
+        if (ka < KA) {
+            uint8_t* atom = scales + ((g * NB + nt / 2) * KA + ka) * 512;
+            *reinterpret_cast<uint32_t*>(atom + 16 * (col & 31) + 4 * (col >> 5)) =
+                *reinterpret_cast<const uint32_t*>(&sc[c][4 * half]);
+        }
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_quantize_rows(const void* x, bool bf16, long long elements, uint8_t* codes, uint8_t* scales,
+                                 void* values, int sm_count, cudaStream_t stream) {
+    const long long vecs = elements / 8;
+    const long long want = (vecs + 255) / 256;
+    const int grid = static_cast<int>(want < 16LL * sm_count ? want : 16LL * sm_count);
+    auto kern = bf16 ? (values ? quantize_rows_kernel<true, true> : quantize_rows_kernel<true, false>)
+                     : (values ? quantize_rows_kernel<false, true> : quantize_rows_kernel<false, false>);
+    return launch_pdl(kern, dim3(grid), dim3(256), 0, stream, static_cast<const uint4*>(x), vecs,
+                      reinterpret_cast<uint32_t*>(codes), scales, static_cast<uint4*>(values));
+}
+
+cudaError_t launch_quantize_weight(const void* w, bool bf16, int groups, int K, int N, uint8_t* codes, uint8_t* scales,
+                                   void* values, cudaStream_t stream) {
+    const int NT = 2 * ((N + 127) / 128);   // both halves of every 128-column atom
+    const int KC = (K / 32 + QW_BLOCKS - 1) / QW_BLOCKS;
+    const dim3 grid(static_cast<unsigned>(static_cast<long long>(groups) * NT * KC));
+    auto kern = bf16 ? (values ? quantize_weight_kernel<true, true> : quantize_weight_kernel<true, false>)
+                     : (values ? quantize_weight_kernel<false, true> : quantize_weight_kernel<false, false>);
+    return launch_pdl(kern, grid, dim3(256), 0, stream, w, K, N, NT, KC, codes, scales, static_cast<uint32_t*>(values));
+}
+
+}  // namespace rdot

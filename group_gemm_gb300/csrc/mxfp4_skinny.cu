@@ -1,0 +1,325 @@
+// mxfp4_skinny.cu -- MXFP4 ragged-dot forward for a few rows per group (decode), operands swapped.
+//
+// out[i, :] = A[i, :] B[g(i)] with A, B in MXFP4 (mxfp4.cuh), fp32 accumulation, bf16 out, computed as
+// out_g^T = B_g A_g^T: 128 weight columns on the MMA's M, up to 64 token rows on its N. What bounds it
+// is streaming the routed experts' codes and scales (17/32 byte per weight) from HBM, so the work is
+// cut by weight bytes: the column quarters (32 columns, 16 KB of codes at K = 1024) of all token tiles
+// are numbered in group order and split evenly over the CTAs, one contiguous range each. A CTA walks
+// its range in tiles of up to four quarters that lie in one 128-column atom; a tile of fewer loads only
+// its quarters' rows, at their natural place in the stage, and the MMA's other rows are not read out.
+// So the last round costs 32-column steps instead of whole 128-column items.
+//
+// Warp 0 streams codes and weight scales (TMA, a ring of STAGES stages of 256 K elements), warp 6
+// gathers the token rows' scale bytes into the atom layout (their row offsets depend on the group
+// sizes, so no fixed layout serves), warp 1 copies scales to tensor memory and issues the MMAs, warps
+// 2..5 read out one 32-column quarter each.
+#include <cuda_bf16.h>
+
+#include "kernels.h"
+#include "mxfp4.cuh"
+#include "pdl.cuh"
+#include "ptx.cuh"
+#include "sched.cuh"
+
+namespace rdot {
+
+namespace {
+
+constexpr int THREADS = 224;
+constexpr int TT = MX4_SKINNY_ROWS;             // token rows per tile (64)
+constexpr int STAGES = 8;
+constexpr int Q_BYTES = 32 * MX4_STAGE_BYTES;   // one quarter's codes of a stage: 4 KB
+constexpr int W_BYTES = 4 * Q_BYTES;
+constexpr int X_BOX = 16 * MX4_STAGE_BYTES;     // 16 token rows: 2 KB
+constexpr int X_BYTES = TT * MX4_STAGE_BYTES;
+constexpr int SF_BYTES = 2 * MX4_ATOM_BYTES;    // a stage's two scale atoms
+constexpr int STAGE_BYTES = W_BYTES + X_BYTES + 2 * SF_BYTES;
+constexpr int RING_BYTES = STAGES * STAGE_BYTES;
+constexpr int BAR_BYTES = (3 * STAGES + 5) * 8;   // full, sfull, empty; tfull[2], tempty[2], drain
+constexpr int MISC_BYTES = 16;
+constexpr int TMEM_SF_BASE = 2 * TT;              // after the two accumulators
+constexpr int SF_COLS = 16;                       // per stage: two weight atoms, two token atoms
+constexpr int TMEM_COLS = 256;
+static_assert(STAGE_BYTES % 1024 == 0, "swizzle atoms stay 1 KB aligned");
+static_assert(TMEM_SF_BASE + STAGES * SF_COLS <= TMEM_COLS, "tensor memory budget");
+
+size_t smem_bytes(int G) { return 1024 + RING_BYTES + BAR_BYTES + MISC_BYTES + sizeof(int32_t) * 2 * (G + 1); }
+
+__device__ __forceinline__ void tmem_ld_32x16(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr)
+        : "memory");
+}
+
+// A tile: quarters [q0, q1) of 128-column atom nb, for one token tile of a group.
+struct SkinnyTile {
+    int g, row0, rows, nb, q0, q1;
+};
+
+// The tile at unit u of a range that ends at `end`; u advances past it. Units: (group, token tile,
+// 32-column quarter), the quarter fastest; a.NT quarters cover N.
+__device__ __forceinline__ SkinnyTile next_tile(int& u, int end, const Mx4Args& a, const int32_t* tprefix,
+                                                const int32_t* off) {
+    const Tile t = decode_tile(u, tprefix, off, a.G, TT, a.NT, false);
+    SkinnyTile s;
+    s.g = t.g;
+    s.row0 = t.row0;
+    s.rows = t.rows;
+    s.nb = t.nt >> 2;
+    s.q0 = t.nt & 3;
+    s.q1 = min(min(4, s.q0 + (end - u)), a.NT - 4 * s.nb);
+    u += s.q1 - s.q0;
+    return s;
+}
+
+__global__ void __launch_bounds__(THREADS, 1)
+    mxfp4_skinny_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant__ CUtensorMap tmap_w,
+                        Mx4Args a) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + RING_BYTES);
+    uint64_t* sfull = full + STAGES;
+    uint64_t* empty = sfull + STAGES;
+    uint64_t* tfull = empty + STAGES;
+    uint64_t* tempty = tfull + 2;
+    uint64_t* drain = tempty + 2;
+    uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(drain + 1);
+    int* abort_flag = reinterpret_cast<int*>(tmem_holder + 1);
+    int32_t* off = reinterpret_cast<int32_t*>(smem + RING_BYTES + BAR_BYTES + MISC_BYTES);
+    int32_t* tprefix = off + a.G + 1;
+
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < STAGES; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&sfull[s], 1);
+            mbar_init(&empty[s], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&tfull[i], 1);
+            mbar_init(&tempty[i], 128);
+        }
+        mbar_init(drain, 1);
+        *abort_flag = 0;
+        fence_mbar_init();
+        tma_prefetch_desc(&tmap_x);
+        tma_prefetch_desc(&tmap_w);
+    }
+    if (warp == 1) {
+        tmem_alloc(tmem_holder, TMEM_COLS);
+        tmem_relinquish();
+    }
+    grid_dependency_enter();   // group sizes and the token codes come from earlier kernels
+    if (warp == 2) {
+        const int bad = group_scan_warp(a.group_sizes, a.G, a.M, TT, a.NT, off, tprefix);
+        if (bad && lane == 0 && blockIdx.x == 0 && a.status) atomicOr(a.status, bad);
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+
+    const uint32_t tmem_base = *tmem_holder;
+    const long long U = tprefix[a.G];
+    const int u0 = static_cast<int>(U * blockIdx.x / gridDim.x);
+    const int u1 = static_cast<int>(U * (blockIdx.x + 1) / gridDim.x);
+    const WaitGuard guard{abort_flag, a.status, a.timeout_ns};
+
+    if (warp == 0) {
+        // ------------------------------------------------------------------ TMA producer
+        if (lane == 0) {
+            const uint64_t x_policy = l2_policy_evict_last();   // a token tile is read by every column tile
+            uint32_t stage = 0, phase = 0, issued_mask = 0, issued_phase = 0;
+            bool ok = true;
+            for (int u = u0; u < u1 && ok;) {
+                const SkinnyTile t = next_tile(u, u1, a, tprefix, off);
+                const int nx = (t.rows + 15) / 16;
+                const uint8_t* sfw = a.rhs_scale + (static_cast<long long>(t.g) * a.NB + t.nb) * a.KA * MX4_ATOM_BYTES;
+                for (int ks = 0; ks < a.KS; ++ks) {
+                    if (!mbar_wait(&empty[stage], phase ^ 1, guard)) {
+                        ok = false;
+                        break;
+                    }
+                    uint8_t* st = smem + stage * STAGE_BYTES;
+                    const int atoms = min(2, a.KA - 2 * ks);
+                    mbar_arrive_expect_tx(&full[stage],
+                                          (t.q1 - t.q0) * Q_BYTES + nx * X_BOX + atoms * MX4_ATOM_BYTES);
+                    // rows past N and bytes past K arrive as zeros
+                    for (int q = t.q0; q < t.q1; ++q)
+                        tma_load_3d(st + q * Q_BYTES, &tmap_w, &full[stage], ks * MX4_STAGE_BYTES,
+                                    t.nb * 128 + 32 * q, t.g);
+                    for (int j = 0; j < nx; ++j)
+                        tma_load_2d_hint(st + W_BYTES + j * X_BOX, &tmap_x, &full[stage], ks * MX4_STAGE_BYTES,
+                                         t.row0 + 16 * j, x_policy);
+                    bulk_load(st + W_BYTES + X_BYTES, sfw + static_cast<long long>(ks) * SF_BYTES,
+                              atoms * MX4_ATOM_BYTES, &full[stage]);
+                    issued_mask |= 1u << stage;
+                    issued_phase = (issued_phase & ~(1u << stage)) | (phase << stage);
+                    if (++stage == STAGES) {
+                        stage = 0;
+                        phase ^= 1;
+                    }
+                }
+            }
+            if (!ok) {
+                // stopping early: let every load still in flight land before the CTA exits
+                int dummy;
+                const WaitGuard dguard = drain_guard(guard, &dummy);
+                for (int s = 0; s < STAGES; ++s)
+                    if (issued_mask & (1u << s)) (void)mbar_wait(&full[s], (issued_phase >> s) & 1u, dguard);
+            }
+        }
+        __syncwarp();
+    } else if (warp == 6) {
+        // ------------------------------------------------------------------ token scale gather
+        // lane l holds rows l and l + 32 of the token tile: 16 bytes of each atom
+        uint32_t stage = 0, phase = 0;
+        bool ok = true;
+        for (int u = u0; u < u1 && ok;) {
+            const SkinnyTile t = next_tile(u, u1, a, tprefix, off);
+            const bool r0 = lane < t.rows, r1 = lane + 32 < t.rows;
+            uint2 c0 = make_uint2(0u, 0u), c1 = c0;
+            if (r0) c0 = lhs_scale_stage(a, t.row0 + lane, 0);
+            if (r1) c1 = lhs_scale_stage(a, t.row0 + lane + 32, 0);
+            for (int ks = 0; ks < a.KS; ++ks) {
+                uint2 n0 = make_uint2(0u, 0u), n1 = n0;   // the next stage's, in flight while this one is stored
+                if (r0 && ks + 1 < a.KS) n0 = lhs_scale_stage(a, t.row0 + lane, ks + 1);
+                if (r1 && ks + 1 < a.KS) n1 = lhs_scale_stage(a, t.row0 + lane + 32, ks + 1);
+                if (!mbar_wait_warp(&empty[stage], phase ^ 1, guard)) {
+                    ok = false;
+                    break;
+                }
+                uint8_t* sf = smem + stage * STAGE_BYTES + W_BYTES + X_BYTES + SF_BYTES;
+                reinterpret_cast<uint4*>(sf)[lane] = make_uint4(c0.x, c1.x, 0u, 0u);
+                reinterpret_cast<uint4*>(sf + MX4_ATOM_BYTES)[lane] = make_uint4(c0.y, c1.y, 0u, 0u);
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sfull[stage]);
+                c0 = n0;
+                c1 = n1;
+                if (++stage == STAGES) {
+                    stage = 0;
+                    phase ^= 1;
+                }
+            }
+        }
+    } else if (warp == 1) {
+        // ------------------------------------------------------------------ MMA issuer
+        if (lane == 0) {
+            uint32_t stage = 0, phase = 0, acc = 0, acc_phase = 0;
+            bool ok = true;
+            for (int u = u0; u < u1 && ok;) {
+                const SkinnyTile t = next_tile(u, u1, a, tprefix, off);
+                const int n = 16 * ((t.rows + 15) / 16);
+                if (!mbar_wait(&tempty[acc], acc_phase ^ 1, guard)) break;
+                tc_fence_after();
+                const uint32_t d_tmem = tmem_base + acc * TT;
+                for (int ks = 0; ks < a.KS; ++ks) {
+                    if (!mbar_wait(&full[stage], phase, guard) || !mbar_wait(&sfull[stage], phase, guard)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t sw = smem_u32(smem + stage * STAGE_BYTES);
+                    const uint32_t sx = sw + W_BYTES;
+                    const uint32_t sf = sx + X_BYTES;
+                    const uint32_t sf_t = tmem_base + TMEM_SF_BASE + SF_COLS * stage;
+                    const int steps = min(4, (a.K - ks * MX4_STAGE_K + 63) / 64);   // MMAs of K = 64 with data
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk) {
+                        if (kk >= steps) break;
+                        const uint32_t w_t = sf_t + 8 * (kk >> 1), x_t = w_t + 4;
+                        if ((kk & 1) == 0) {
+                            tmem_cp_scales<1>(w_t, smem_desc_rows16(sf + (kk >> 1) * MX4_ATOM_BYTES));
+                            tmem_cp_scales<1>(x_t, smem_desc_rows16(sf + SF_BYTES + (kk >> 1) * MX4_ATOM_BYTES));
+                        }
+                        mma_mxf4<1>(d_tmem, smem_desc_sw128(sw + kk * 32, 16, 1024), smem_desc_sw128(sx + kk * 32, 16, 1024),
+                                    idesc_mxf4(128, n, 2 * (kk & 1)), w_t, x_t, (ks | kk) != 0 ? 1u : 0u);
+                    }
+                    mma_commit(&empty[stage]);
+                    if (++stage == STAGES) {
+                        stage = 0;
+                        phase ^= 1;
+                    }
+                }
+                if (!ok) break;
+                mma_commit(&tfull[acc]);
+                acc ^= 1;
+                if (acc == 0) acc_phase ^= 1;
+            }
+            // all MMAs issued by this thread complete before teardown frees TMEM
+            mma_commit(drain);
+            int dummy;
+            const WaitGuard dguard = drain_guard(guard, &dummy);
+            (void)mbar_wait(drain, 0, dguard);
+        }
+        __syncwarp();
+    } else {
+        // ------------------------------------------------------------------ epilogue
+        const int q = warp & 3;   // TMEM lane quarter: columns 32 q + lane of the tile's atom
+        uint32_t acc = 0, acc_phase = 0;
+        __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out);
+        for (int u = u0; u < u1;) {
+            const SkinnyTile t = next_tile(u, u1, a, tprefix, off);
+            if (!mbar_wait_warp(&tfull[acc], acc_phase, guard)) break;
+            tc_fence_after();
+            const int col = t.nb * 128 + q * 32 + lane;
+            if (q >= t.q0 && q < t.q1) {
+                for (int j0 = 0; j0 < t.rows; j0 += 16) {
+                    uint32_t v[16];   // v[j]: token row row0 + j0 + j
+                    tmem_ld_32x16(tmem_base + acc * TT + j0 + (static_cast<uint32_t>(q * 32) << 16), v);
+                    tmem_ld_wait();
+                    if (col < a.N) {
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) {
+                            if (j0 + j >= t.rows) break;
+                            out[(static_cast<long long>(t.row0) + j0 + j) * a.N + col] =
+                                __float2bfloat16_rn(__uint_as_float(v[j]));
+                        }
+                    }
+                    __syncwarp();
+                }
+            }
+            tc_fence_before();
+            mbar_arrive(&tempty[acc]);
+            acc ^= 1;
+            if (acc == 0) acc_phase ^= 1;
+        }
+        // zero rows [off[G], M): one contiguous range, split over CTAs and the 128 epilogue threads
+        const long long b0 = static_cast<long long>(off[a.G]) * a.N * 2;
+        const long long b1 = static_cast<long long>(a.M) * a.N * 2;   // both multiples of 16
+        const long long nv = (b1 - b0) / 16;
+        if (nv > 0) {
+            uint4* base = reinterpret_cast<uint4*>(static_cast<uint8_t*>(a.out) + b0);
+            const long long per = (nv + gridDim.x - 1) / gridDim.x;
+            const long long s = per * blockIdx.x;
+            const long long e = min(nv, s + per);
+            for (long long i = s + (threadIdx.x - 64); i < e; i += 128) base[i] = make_uint4(0, 0, 0, 0);
+        }
+    }
+
+    // ---------------------------------------------------------------------- teardown
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem_base, TMEM_COLS);
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_mxfp4_skinny(const CUtensorMap& tmap_x, const CUtensorMap& tmap_w, const Mx4Args& a, int grid,
+                                cudaStream_t stream) {
+    const size_t shm = smem_bytes(a.G);
+    cudaError_t e = cudaFuncSetAttribute(mxfp4_skinny_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         static_cast<int>(shm));
+    if (e != cudaSuccess) return e;
+    return launch_pdl(mxfp4_skinny_kernel, dim3(grid), dim3(THREADS), shm, stream, tmap_x, tmap_w, a);
+}
+
+}  // namespace rdot

@@ -1,0 +1,343 @@
+// mxfp4_tc2.cu -- MXFP4 ragged-dot forward on CTA pairs (tcgen05 cta_group::2), 256 x 256 tiles.
+//
+// out[i, :] = A[i, :] B[g(i)] with A, B in MXFP4 (mxfp4.cuh), fp32 accumulation, bf16 out; rows past
+// the last group end are zero. The pair mapping of fwd_tc2.cu and mxfp8_tc2.cu: per K stage (128 code
+// bytes, 256 elements) CTA r stages rows [row0 + 128 r, +128) of the lhs codes, columns
+// [n0 + 128 r, +128) of the rhs codes (16 KB each), the scale atoms of its rows (1 KB) and those of all
+// 256 columns (2 KB). A pair tile asks half the operand bytes per SM of a 128 x 256 tile: at four bits
+// the tensor cores consume a stage in 512 clocks, so a lone 128 x 256 tile would ask 100 bytes per
+// clock and SM of L2, a pair tile 68.
+//
+// The weight scales come in the atom layout (laid out once, by the quantiser) and are fetched by TMA
+// with the codes; their bytes complete on the even CTA's "full" barrier. The rows' scales are plain
+// [M, K/32], because a tile starts at its group's first row: warp 10 of each CTA gathers its 128 rows'
+// 8 bytes a stage into the atom layout and arrives on the even CTA's "sfull" barrier. The even CTA
+// copies scales to tensor memory and issues M = 256, N = 256, K = 64 MMAs. Eight epilogue warps per
+// CTA read the accumulator out as bf16 and hand it back before they store.
+#include <cuda_bf16.h>
+
+#include "epilogue.cuh"
+#include "kernels.h"
+#include "mxfp4.cuh"
+#include "pairdrain.cuh"
+#include "pdl.cuh"
+#include "ptx.cuh"
+#include "sched.cuh"
+
+namespace rdot {
+
+namespace {
+
+constexpr int EPI_WARPS = 8;
+constexpr int SCALE_WARP = 2 + EPI_WARPS;
+constexpr int THREADS = 32 * (SCALE_WARP + 1);
+constexpr int BM = 256;                // rows per cluster tile
+constexpr int BN = 256;
+constexpr int STAGES = 5;
+constexpr int A_BYTES = 128 * MX4_STAGE_BYTES;       // this CTA's 128 rows
+constexpr int B_BYTES = 128 * MX4_STAGE_BYTES;       // this CTA's 128 columns
+constexpr int SFA_BYTES = 2 * MX4_ATOM_BYTES;        // its rows, 256 elements
+constexpr int SFB_BYTES = 4 * MX4_ATOM_BYTES;        // all 256 columns, 256 elements
+constexpr int STAGE_BYTES = A_BYTES + B_BYTES + SFA_BYTES + SFB_BYTES;
+constexpr int RING_BYTES = STAGES * STAGE_BYTES;
+constexpr int EPI_BYTES = EPI_WARPS * EpiStage<false>::BYTES;
+constexpr int BAR_BYTES = (3 * STAGES + 3) * 8;      // full, sfull, empty, tfull, tempty, drain
+constexpr int MISC_BYTES = 16;
+constexpr int XCH_BYTES = (sizeof(PairExchange<STAGES>) + 15) / 16 * 16;
+constexpr int TMEM_COLS = 512;
+constexpr int TMEM_SF_BASE = BN;                     // after the accumulator
+constexpr int SF_COLS = 2 * (4 + 8);                 // per stage: two atoms of A and two of B (256 columns)
+static_assert(STAGE_BYTES % 1024 == 0, "swizzle atoms stay 1 KB aligned");
+static_assert(TMEM_SF_BASE + STAGES * SF_COLS <= TMEM_COLS, "tensor memory budget");
+constexpr uint32_t EMPTY_ARRIVALS = 2 * EPI_WARPS;
+
+size_t smem_bytes(int G) {
+    return 1024 + RING_BYTES + EPI_BYTES + BAR_BYTES + MISC_BYTES + XCH_BYTES + sizeof(int32_t) * 2 * (G + 1);
+}
+
+// mbar_wait with cluster-scope acquire: what the other CTA wrote before its arrive is visible.
+__device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity, const WaitGuard& g) {
+    if (mbar_try_wait_cluster(bar, parity)) return true;
+    const uint64_t t0 = global_timer_ns();
+    while (true) {
+        if (mbar_try_wait_cluster(bar, parity)) return true;
+        if (*g.abort) return false;
+        if (global_timer_ns() - t0 > g.timeout_ns) {
+            guard_fail(g, RDOT_STATUS_BIT_TIMEOUT);
+            return false;
+        }
+    }
+}
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
+    mxfp4_tc2_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ CUtensorMap tmap_b,
+                     const __grid_constant__ CUtensorMap tmap_sfb, Mx4Args a) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint32_t* epi_stage = reinterpret_cast<uint32_t*>(smem + RING_BYTES);
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + RING_BYTES + EPI_BYTES);
+    uint64_t* sfull = full + STAGES;
+    uint64_t* empty = sfull + STAGES;
+    uint64_t* tfull = empty + STAGES;
+    uint64_t* tempty = tfull + 1;
+    uint64_t* drain = tempty + 1;
+    uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(drain + 1);
+    int* abort_flag = reinterpret_cast<int*>(tmem_holder + 1);
+    auto* xch = reinterpret_cast<PairExchange<STAGES>*>(smem + RING_BYTES + EPI_BYTES + BAR_BYTES + MISC_BYTES);
+    int32_t* off = reinterpret_cast<int32_t*>(smem + RING_BYTES + EPI_BYTES + BAR_BYTES + MISC_BYTES + XCH_BYTES);
+    int32_t* tprefix = off + a.G + 1;
+
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_ctarank();
+    const bool leader = rank == 0;
+    const int cluster = static_cast<int>(cluster_id_x());
+    const int nclusters = static_cast<int>(cluster_count_x());
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < STAGES; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&sfull[s], 2);   // one arrival per CTA, on the even CTA's barrier
+            mbar_init(&empty[s], 1);
+        }
+        mbar_init(tfull, 1);
+        mbar_init(tempty, EMPTY_ARRIVALS);
+        mbar_init(drain, 1);
+        mbar_init(&xch->bar, 1);
+        *abort_flag = 0;
+        fence_mbar_init();
+        tma_prefetch_desc(&tmap_a);
+        tma_prefetch_desc(&tmap_b);
+        tma_prefetch_desc(&tmap_sfb);
+    }
+    if (warp == 1) {
+        tmem_alloc_pair(tmem_holder, TMEM_COLS);
+        tmem_relinquish_pair();
+    }
+    grid_dependency_enter();   // group sizes and operands may come from the previous kernel
+    if (warp == 2) {
+        const int bad = group_scan_warp(a.group_sizes, a.G, a.M, BM, a.NT, off, tprefix);
+        if (bad && lane == 0 && blockIdx.x == 0 && a.status) atomicOr(a.status, bad);
+    }
+    tc_fence_before();
+    cluster_sync();
+    tc_fence_after();
+
+    const uint32_t tmem_base = *tmem_holder;
+    const int W = tprefix[a.G];
+    const bool m_inner = a.m_inner != 0;
+    const WaitGuard guard{abort_flag, a.status, a.timeout_ns};
+
+    if (warp == 0) {
+        // ------------------------------------------------------------------ TMA producer (both CTAs)
+        if (lane == 0) {
+            uint32_t stage = 0, phase = 0;
+            int pos = 0;   // load iterations issued (see pairdrain.cuh)
+            bool ok = true;
+            const int r = static_cast<int>(rank);
+            for (int w = cluster; w < W && ok; w += nclusters) {
+                const Tile t = decode_tile(w, tprefix, off, a.G, BM, a.NT, m_inner);
+                const int n0 = t.nt * BN;
+                // the odd CTA's A half unless wholly past the group, its B half unless wholly past N:
+                // what is not loaded only feeds rows or columns that are not stored
+                const int a1 = t.rows > 128 ? A_BYTES : 0;
+                const int b1 = (n0 + 128 < a.N) ? B_BYTES : 0;
+                const int my_a = r ? a1 : A_BYTES, my_b = r ? b1 : B_BYTES;
+                const int sfb_row = t.g * a.NB + 2 * t.nt;   // two atom rows, 128 columns each
+                for (int ks = 0; ks < a.KS; ++ks) {
+                    if (!mbar_wait(&empty[stage], phase ^ 1, guard)) {
+                        ok = false;
+                        break;
+                    }
+                    uint8_t* st = smem + stage * STAGE_BYTES;
+                    if (leader) mbar_arrive_expect_tx(&full[stage], A_BYTES + a1 + B_BYTES + b1 + 2 * SFB_BYTES);
+                    const uint32_t fb = mapa_shared(smem_u32(&full[stage]), 0);
+                    if (my_a) tma_load_2d_pair(st, &tmap_a, fb, ks * MX4_STAGE_BYTES, t.row0 + 128 * r);
+                    if (my_b) tma_load_3d_pair(st + A_BYTES, &tmap_b, fb, ks * MX4_STAGE_BYTES, n0 + 128 * r, t.g);
+                    // 2 x 256 words: the two column atoms' scales of this stage (zeros past the tensor)
+                    tma_load_2d_pair(st + A_BYTES + B_BYTES + SFA_BYTES, &tmap_sfb, fb, ks * (SFA_BYTES / 4), sfb_row);
+                    xch->share[stage] = a1 + b1 + SFB_BYTES;   // the odd CTA's bytes of this iteration
+                    ++pos;
+                    if (++stage == STAGES) {
+                        stage = 0;
+                        phase ^= 1;
+                    }
+                }
+            }
+            // every load either CTA issued lands before either CTA can leave (pairdrain.cuh)
+            pair_drain(xch, full, pos, leader, guard);
+        }
+        __syncwarp();
+    } else if (warp == SCALE_WARP) {
+        // ------------------------------------------------------------------ row scale gather (both CTAs)
+        // lane l holds rows l, l + 32, l + 64, l + 96 of this CTA's half: 16 bytes of each atom
+        uint32_t stage = 0, phase = 0;
+        bool ok = true;
+        for (int w = cluster; w < W && ok; w += nclusters) {
+            const Tile t = decode_tile(w, tprefix, off, a.G, BM, a.NT, m_inner);
+            const int first = 128 * static_cast<int>(rank) + lane;
+            const long long row = static_cast<long long>(t.row0) + first;
+            uint2 cur[4], nxt[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                cur[i] = make_uint2(0u, 0u);
+                if (first + 32 * i < t.rows) cur[i] = lhs_scale_stage(a, row + 32 * i, 0);
+            }
+            for (int ks = 0; ks < a.KS; ++ks) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {   // the next stage's, in flight while this one is stored
+                    nxt[i] = make_uint2(0u, 0u);
+                    if (ks + 1 < a.KS && first + 32 * i < t.rows) nxt[i] = lhs_scale_stage(a, row + 32 * i, ks + 1);
+                }
+                if (!mbar_wait_warp(&empty[stage], phase ^ 1, guard)) {
+                    ok = false;
+                    break;
+                }
+                uint8_t* sf = smem + stage * STAGE_BYTES + A_BYTES + B_BYTES;
+                reinterpret_cast<uint4*>(sf)[lane] = make_uint4(cur[0].x, cur[1].x, cur[2].x, cur[3].x);
+                reinterpret_cast<uint4*>(sf + MX4_ATOM_BYTES)[lane] = make_uint4(cur[0].y, cur[1].y, cur[2].y, cur[3].y);
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&sfull[stage]), 0));
+#pragma unroll
+                for (int i = 0; i < 4; ++i) cur[i] = nxt[i];
+                if (++stage == STAGES) {
+                    stage = 0;
+                    phase ^= 1;
+                }
+            }
+        }
+    } else if (warp == 1) {
+        // ------------------------------------------------------------------ MMA issuer (even CTA)
+        if (lane == 0 && leader) {
+            uint32_t stage = 0, phase = 0, acc_phase = 0;
+            bool ok = true;
+            for (int w = cluster; w < W && ok; w += nclusters) {
+                if (!mbar_wait(tempty, acc_phase ^ 1, guard)) break;
+                tc_fence_after();
+                for (int ks = 0; ks < a.KS; ++ks) {
+                    if (!mbar_wait(&full[stage], phase, guard) || !mbar_wait_cluster(&sfull[stage], phase, guard)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t sa = smem_u32(smem + stage * STAGE_BYTES);
+                    const uint32_t sb = sa + A_BYTES;
+                    const uint32_t sfa = sb + B_BYTES, sfb = sfa + SFA_BYTES;
+                    const uint32_t sf_t = tmem_base + TMEM_SF_BASE + SF_COLS * stage;
+                    const int steps = min(4, (a.K - ks * MX4_STAGE_K + 63) / 64);   // MMAs of K = 64 with data
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk) {
+                        if (kk >= steps) break;
+                        const uint32_t a_t = sf_t + 12 * (kk >> 1), b_t = a_t + 4;
+                        if ((kk & 1) == 0) {
+                            const uint32_t atom = (kk >> 1) * MX4_ATOM_BYTES;
+                            tmem_cp_scales<2>(a_t, smem_desc_rows16(sfa + atom));
+                            tmem_cp_scales<2>(b_t, smem_desc_rows16(sfb + atom));
+                            tmem_cp_scales<2>(b_t + 4, smem_desc_rows16(sfb + 2 * MX4_ATOM_BYTES + atom));
+                        }
+                        mma_mxf4<2>(tmem_base, smem_desc_sw128(sa + kk * 32, 16, 1024),
+                                    smem_desc_sw128(sb + kk * 32, 16, 1024), idesc_mxf4(BM, BN, 2 * (kk & 1)), a_t, b_t,
+                                    (ks | kk) != 0 ? 1u : 0u);
+                    }
+                    mma_commit_pair_multicast(&empty[stage], 0x3);
+                    if (++stage == STAGES) {
+                        stage = 0;
+                        phase ^= 1;
+                    }
+                }
+                if (!ok) break;
+                mma_commit_pair_multicast(tfull, 0x3);
+                acc_phase ^= 1;
+            }
+            mma_commit_pair(drain);
+            int dummy;
+            (void)mbar_wait(drain, 0, drain_guard(guard, &dummy));
+        }
+        __syncwarp();
+    } else {
+        // ------------------------------------------------------------------ epilogue (both CTAs)
+        const int q = warp & 3;
+        const int half = (warp - 2) / 4;
+        uint32_t* stage_buf = epi_stage + (warp - 2) * EpiStage<false>::WORDS;
+        uint32_t acc_phase = 0;
+        for (int w = cluster; w < W; w += nclusters) {
+            const Tile t = decode_tile(w, tprefix, off, a.G, BM, a.NT, m_inner);
+            const int n0 = t.nt * BN + half * (BN / 2);
+            const bool ready = mbar_wait_warp(tfull, acc_phase, guard);
+            if (!ready) break;
+            tc_fence_after();
+            const uint32_t tbase = tmem_base + half * (BN / 2) + (static_cast<uint32_t>(q * 32) << 16);
+            const int first = 128 * static_cast<int>(rank) + q * 32;
+            const int rows_valid = t.rows - first;
+            __nv_bfloat16* out_rows =
+                static_cast<__nv_bfloat16*>(a.out) + (static_cast<long long>(t.row0) + first) * a.N;
+            // read this warp's 32 x 128 block out as bf16, hand the accumulator back, then store
+            // while the pair's next tile runs
+            uint32_t pk[4][16];
+            tmem_read_bf16_32x128(tbase, pk);
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(tempty), 0));
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                const int col = n0 + c * 32;
+                if (rows_valid > 0 && col < a.N)
+                    store_packed_bf16_32x32(pk[c], stage_buf, out_rows + col, a.N, rows_valid, a.N - col);
+            }
+            acc_phase ^= 1;
+        }
+        {
+            const long long b0 = static_cast<long long>(off[a.G]) * a.N * 2;
+            const long long b1 = static_cast<long long>(a.M) * a.N * 2;
+            const long long nv = (b1 - b0) / 16;
+            if (nv > 0) {
+                uint4* base = reinterpret_cast<uint4*>(static_cast<uint8_t*>(a.out) + b0);
+                const long long per = (nv + gridDim.x - 1) / gridDim.x;
+                const long long s = per * blockIdx.x;
+                const long long e = min(nv, s + per);
+                for (long long i = s + (threadIdx.x - 64); i < e; i += 32 * EPI_WARPS) base[i] = make_uint4(0, 0, 0, 0);
+            }
+        }
+    }
+
+    tc_fence_before();
+    cluster_sync();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc_pair(tmem_base, TMEM_COLS);
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_mxfp4_pair(const CUtensorMap& tmap_a, const CUtensorMap& tmap_b, const CUtensorMap& tmap_sfb,
+                              const Mx4Args& a, int grid, cudaStream_t stream) {
+    if (grid % 2) return cudaErrorInvalidValue;
+    const size_t shm = smem_bytes(a.G);
+    cudaError_t e = cudaFuncSetAttribute(mxfp4_tc2_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         static_cast<int>(shm));
+    if (e != cudaSuccess) return e;
+    return launch_pdl(mxfp4_tc2_kernel, dim3(grid), dim3(THREADS), shm, stream, tmap_a, tmap_b, tmap_sfb, a);
+}
+
+int mxfp4_pair_max_clusters(int G) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2, 1, 1);
+    cfg.blockDim = dim3(THREADS, 1, 1);
+    cfg.dynamicSmemBytes = smem_bytes(G);
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = 2;
+    attr.val.clusterDim.y = 1;
+    attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    cudaError_t e = cudaFuncSetAttribute(mxfp4_tc2_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         static_cast<int>(cfg.dynamicSmemBytes));
+    if (e == cudaSuccess) e = cudaOccupancyMaxActiveClusters(&n, mxfp4_tc2_kernel, &cfg);
+    return e == cudaSuccess ? n : 0;
+}
+
+}  // namespace rdot

@@ -51,7 +51,7 @@ typedef enum {
     RDOT_WARN_GROUP_SIZES = 5   /* rdot_read_status: group_sizes were clamped on the device */
 } rdot_status;
 
-typedef enum { RDOT_F32 = 0, RDOT_BF16 = 1, RDOT_E4M3 = 2 } rdot_dtype;
+typedef enum { RDOT_F32 = 0, RDOT_BF16 = 1, RDOT_E4M3 = 2, RDOT_E2M1 = 3 } rdot_dtype;
 
 typedef enum {
     RDOT_MODE_FORWARD = 0,       /* out[M,N] = lhs[M,K] @ rhs[g(i),K,N] (non-contracting ragged M) */
@@ -60,7 +60,8 @@ typedef enum {
     RDOT_MODE_GRAD_INPUT = 3,    /* dlhs[M,K] = dy[M,N] @ rhs[g(i),K,N]^T (contracts rhs's N axis) */
     RDOT_MODE_FORWARD_GATED = 4, /* out[M,N] = silu(lhs @ w0[g(i)]) * (lhs @ w1[g(i)]) (gated up projection) */
     RDOT_MODE_GRAD_INPUT_MXFP8 = 5, /* the data gradient on MXFP8 operands (scales along N) */
-    RDOT_MODE_GRAD_WEIGHT_MXFP8 = 6 /* the weight gradient on MXFP8 operands (scales along the rows) */
+    RDOT_MODE_GRAD_WEIGHT_MXFP8 = 6, /* the weight gradient on MXFP8 operands (scales along the rows) */
+    RDOT_MODE_FORWARD_MXFP4 = 8  /* forward with E2M1 operands and E8M0 scales per 32 K elements */
 } rdot_mode;
 
 /* Bits of the device status word (int32 at offset 0 of the workspace). */
@@ -110,7 +111,8 @@ typedef struct {
     int64_t n;          /* output width: rhs.shape[2] (forward) or dy width (grad-weight) */
     int32_t groups;     /* G, 1 .. RDOT_MAX_GROUPS */
     int32_t mode;       /* rdot_mode */
-    int32_t in_dtype;   /* rdot_dtype of lhs/rhs (forward, grad-weight); RDOT_E4M3 for MXFP8 */
+    int32_t in_dtype;   /* rdot_dtype of lhs/rhs (forward, grad-weight); RDOT_E4M3 for MXFP8,
+                           RDOT_E2M1 for MXFP4 */
     int32_t out_dtype;  /* RDOT_F32 or RDOT_BF16 (forward); RDOT_F32 (grad-weight) */
     int32_t tile_n;     /* 0 = choose; otherwise the N tile width of the tensor-core kernels */
     int32_t flags;      /* RDOT_FLAG_* bits; 0 lets the plan choose */
@@ -185,6 +187,55 @@ RDOT_API rdot_status rdot_forward_mxfp8(rdot_plan_t plan, const void* lhs, const
                                const void* rhs, const uint8_t* rhs_scale,
                                const int32_t* group_sizes, void* out, void* workspace,
                                void* stream);
+
+/* MXFP4 (OCP Microscaling Formats v1.0): E2M1 codes (magnitudes 0, 1/2, 1, 3/2, 2, 3, 4, 6; bit 3 the
+ * sign), two per byte with the lower index in the low nibble, and one E8M0 scale byte s per 32
+ * consecutive elements along the contraction: value = e2m1(code) * 2^(s-127), s = 255 is NaN.
+ *
+ * Quantisation rule: the scale of a block is 2^(floor(log2 amax) - 2), at least 2^-127 (amax the
+ * largest magnitude; a block of zeros gets 2^-127); an element is divided by it, rounded to E2M1 to
+ * nearest even, saturated at 6, and keeps its sign. A block holding a NaN or an infinity gets s = 255
+ * and codes 0. The values the codes stand for are exact in bf16; the quantisers write them on request
+ * (values not null), for a backward pass that differentiates through the quantised operands. Both
+ * run on the calling thread's current device and never synchronise the host.
+ *
+ * rdot_quantize_mxfp4: rows along whose width the product contracts (activations)
+ *   x       device [rows, k], dtype RDOT_F32 or RDOT_BF16
+ *   codes   device uint8 [rows, k/2] out;  scales  device uint8 [rows, k/32] out
+ *   values  device bf16 [rows, k] out, or null
+ * k % 32 == 0, else RDOT_ERR_UNSUPPORTED; 16-byte alignment for x, codes and values. rows = 0
+ * launches nothing. */
+RDOT_API rdot_status rdot_quantize_mxfp4(const void* x, int32_t dtype, int64_t rows, int64_t k, uint8_t* codes,
+                                         uint8_t* scales, void* values, void* stream);
+
+/* rdot_quantize_mxfp4_weight: a layer's weights, laid out once for rdot_forward_mxfp4
+ *   w       device [G, K, N] (as for rdot_forward), dtype RDOT_F32 or RDOT_BF16
+ *   codes   device uint8 [G, N, K/2] out: each output column's codes contiguous along K
+ *   scales  device uint8 [G, NB, KA, 512] out, NB = ceil(N / 128), KA = ceil(K / 128): atoms of 128
+ *           columns x 4 scale blocks, the scale of column n and block b at byte
+ *           16 (n % 32) + 4 ((n / 32) % 4) + b % 4 of atom (n / 128, b / 4); zeros past N and K/32
+ *   values  device bf16 [G, K, N] out, or null
+ * K % 32 == 0, N % 8 == 0, G <= RDOT_MAX_GROUPS, else RDOT_ERR_UNSUPPORTED; 16-byte alignment for all.
+ * rdot_mxfp4_weight_scale_bytes gives the size of `scales`. */
+RDOT_API rdot_status rdot_mxfp4_weight_scale_bytes(int32_t groups, int64_t k, int64_t n, size_t* bytes);
+RDOT_API rdot_status rdot_quantize_mxfp4_weight(const void* w, int32_t dtype, int32_t groups, int64_t k, int64_t n,
+                                                uint8_t* codes, uint8_t* scales, void* values, void* stream);
+
+/* MXFP4 forward: rdot_forward on MXFP4 operands, fp32 accumulation, bf16 out (zero rows past the sum).
+ *   lhs        device uint8 [M, K/2]     codes;  lhs_scale  device uint8 [M, K/32]
+ *   rhs        device uint8 [G, N, K/2]  codes;  rhs_scale  device uint8 [G, NB, KA, 512]
+ *              (both as rdot_quantize_mxfp4_weight lays them out; its zero padding is read)
+ *   out        device bf16 [M, N]
+ * Plan: mode RDOT_MODE_FORWARD_MXFP4, in_dtype RDOT_E2M1, out_dtype RDOT_BF16, tile_n 0, K % 32 == 0,
+ * N % 8 == 0. Few rows per group (at most 32, spread evenly over min(M, G) groups) run on the swapped
+ * kernel (tile_m 64, tile_n 32: its work is dealt in 32-column steps), more on CTA pairs (256 x 256);
+ * RDOT_FLAG_SKINNY, RDOT_FLAG_NO_SKINNY and RDOT_FLAG_CTA_PAIR force either, and
+ * RDOT_FLAG_NO_CTA_PAIR is RDOT_ERR_UNSUPPORTED without RDOT_FLAG_SKINNY. lhs_scale may have any
+ * alignment (8 bytes is fastest), the others 16 bytes; same workspace, status and stream rules as
+ * rdot_forward, and every call can be captured in a CUDA graph (nothing is kept between calls). */
+RDOT_API rdot_status rdot_forward_mxfp4(rdot_plan_t plan, const void* lhs, const uint8_t* lhs_scale, const void* rhs,
+                                        const uint8_t* rhs_scale, const int32_t* group_sizes, void* out,
+                                        void* workspace, void* stream);
 
 /* Weight gradient: the ragged dimension is the contraction ("Group-GEMM in XLA", Part 3
  * "Contracting"; Part 4 Table 7, class wgrad_wi).
