@@ -56,6 +56,15 @@ __device__ __forceinline__ void tmem_cp_scales(uint32_t taddr, uint64_t sdesc) {
         asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(sdesc) : "memory");
 }
 
+// Eight 32-bit registers of each lane to eight tensor-memory columns of the warp's lane quarter.
+__device__ __forceinline__ void tmem_st_32x8(uint32_t taddr, uint4 a, uint4 b) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(a.x),
+                 "r"(a.y), "r"(a.z), "r"(a.w), "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w)
+                 : "memory");
+}
+
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
 // The 8 scale bytes of K stage ks of row `row`; blocks past K read as 0 (their codes are zeros).
 __device__ __forceinline__ uint2 lhs_scale_stage(const Mx4Args& a, long long row, int ks) {
     const uint8_t* p = a.lhs_scale + row * a.KB + 8 * ks;
@@ -73,6 +82,39 @@ __device__ __forceinline__ uint2 lhs_scale_stage(const Mx4Args& a, long long row
         if (j + 4 < avail) v.y |= static_cast<uint32_t>(__ldg(p + 4 + j)) << (8 * j);
     }
     return v;
+}
+
+// Scale gather of a token or row tile. The rows' scales are plain [M, K/32]: a tile starts at its
+// group's first row, so no fixed layout could hold them as atoms. A warp loads one row per lane, the
+// scales of MX4_GROUP consecutive K stages (one 32-byte sector) at a time and one group ahead of the
+// one in use, and puts them into shared memory as atoms, from which the warps that fill tensor memory
+// read 16 bytes a lane. (Loading four rows a lane in each of them instead cost 512 uncoalesced L1
+// lookups per stage and SM, as much as the stage's MMAs.)
+constexpr int MX4_GROUP = 4;
+constexpr int MX4_GROUP_BYTES = MX4_GROUP * 2 * MX4_ATOM_BYTES;   // atoms of a group: 4 KB
+
+__device__ __forceinline__ void load_scale_group(const Mx4Args& a, long long row, bool live, int ks0,
+                                                 uint2 (&v)[MX4_GROUP]) {
+#pragma unroll
+    for (int j = 0; j < MX4_GROUP; ++j) {
+        v[j] = make_uint2(0u, 0u);
+        if (live && ks0 + j < a.KS) v[j] = lhs_scale_stage(a, row, ks0 + j);
+    }
+}
+
+// Row r of the tile (0 .. 127) into the group's atoms.
+__device__ __forceinline__ void put_scale_group(uint8_t* atoms, int r, const uint2 (&v)[MX4_GROUP]) {
+    uint8_t* p = atoms + 16 * (r & 31) + 4 * (r >> 5);
+#pragma unroll
+    for (int j = 0; j < MX4_GROUP; ++j) {
+        *reinterpret_cast<uint32_t*>(p + 2 * j * MX4_ATOM_BYTES) = v[j].x;
+        *reinterpret_cast<uint32_t*>(p + (2 * j + 1) * MX4_ATOM_BYTES) = v[j].y;
+    }
+}
+
+// Barrier of `threads` threads on hardware barrier `id` (1 .. 15; __syncthreads is 0).
+__device__ __forceinline__ void named_barrier(int id, int threads) {
+    asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
 
 }  // namespace rdot

@@ -176,34 +176,54 @@ __global__ void __launch_bounds__(THREADS, 1)
         __syncwarp();
     } else if (warp == 6) {
         // ------------------------------------------------------------------ token scale gather
-        // lane l holds rows l and l + 32 of the token tile: 16 bytes of each atom
+        // lane l holds rows l and l + 32 of the token tile: 16 bytes of each atom. (tn, kn) is the group
+        // of stages being loaded, one ahead of the one being stored, across tiles too
         uint32_t stage = 0, phase = 0;
         bool ok = true;
+        uint2 c0[MX4_GROUP], c1[MX4_GROUP], n0[MX4_GROUP], n1[MX4_GROUP];
+        int un = u0, kn = 0;
+        bool more = un < u1;
+        SkinnyTile tn{};
+        const auto load = [&] {
+            load_scale_group(a, static_cast<long long>(tn.row0) + lane, lane < tn.rows, kn, n0);
+            load_scale_group(a, static_cast<long long>(tn.row0) + lane + 32, lane + 32 < tn.rows, kn, n1);
+        };
+        if (more) {
+            tn = next_tile(un, u1, a, tprefix, off);
+            load();
+        }
         for (int u = u0; u < u1 && ok;) {
-            const SkinnyTile t = next_tile(u, u1, a, tprefix, off);
-            const bool r0 = lane < t.rows, r1 = lane + 32 < t.rows;
-            uint2 c0 = make_uint2(0u, 0u), c1 = c0;
-            if (r0) c0 = lhs_scale_stage(a, t.row0 + lane, 0);
-            if (r1) c1 = lhs_scale_stage(a, t.row0 + lane + 32, 0);
-            for (int ks = 0; ks < a.KS; ++ks) {
-                uint2 n0 = make_uint2(0u, 0u), n1 = n0;   // the next stage's, in flight while this one is stored
-                if (r0 && ks + 1 < a.KS) n0 = lhs_scale_stage(a, t.row0 + lane, ks + 1);
-                if (r1 && ks + 1 < a.KS) n1 = lhs_scale_stage(a, t.row0 + lane + 32, ks + 1);
-                if (!mbar_wait_warp(&empty[stage], phase ^ 1, guard)) {
-                    ok = false;
-                    break;
+            (void)next_tile(u, u1, a, tprefix, off);
+            for (int k0 = 0; k0 < a.KS && ok; k0 += MX4_GROUP) {
+#pragma unroll
+                for (int j = 0; j < MX4_GROUP; ++j) {
+                    c0[j] = n0[j];
+                    c1[j] = n1[j];
                 }
-                uint8_t* sf = smem + stage * STAGE_BYTES + W_BYTES + X_BYTES + SF_BYTES;
-                reinterpret_cast<uint4*>(sf)[lane] = make_uint4(c0.x, c1.x, 0u, 0u);
-                reinterpret_cast<uint4*>(sf + MX4_ATOM_BYTES)[lane] = make_uint4(c0.y, c1.y, 0u, 0u);
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&sfull[stage]);
-                c0 = n0;
-                c1 = n1;
-                if (++stage == STAGES) {
-                    stage = 0;
-                    phase ^= 1;
+                kn += MX4_GROUP;
+                if (kn >= a.KS) {
+                    kn = 0;
+                    more = un < u1;
+                    if (more) tn = next_tile(un, u1, a, tprefix, off);
+                }
+                if (more) load();
+#pragma unroll
+                for (int j = 0; j < MX4_GROUP; ++j) {
+                    if (k0 + j >= a.KS) break;
+                    if (!mbar_wait_warp(&empty[stage], phase ^ 1, guard)) {
+                        ok = false;
+                        break;
+                    }
+                    uint8_t* sf = smem + stage * STAGE_BYTES + W_BYTES + X_BYTES + SF_BYTES;
+                    reinterpret_cast<uint4*>(sf)[lane] = make_uint4(c0[j].x, c1[j].x, 0u, 0u);
+                    reinterpret_cast<uint4*>(sf + MX4_ATOM_BYTES)[lane] = make_uint4(c0[j].y, c1[j].y, 0u, 0u);
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&sfull[stage]);
+                    if (++stage == STAGES) {
+                        stage = 0;
+                        phase ^= 1;
+                    }
                 }
             }
         }

@@ -8,12 +8,14 @@
 // the tensor cores consume a stage in 512 clocks, so a lone 128 x 256 tile would ask 100 bytes per
 // clock and SM of L2, a pair tile 68.
 //
-// The weight scales come in the atom layout (laid out once, by the quantiser) and are fetched by TMA
-// with the codes; their bytes complete on the even CTA's "full" barrier. The rows' scales are plain
-// [M, K/32], because a tile starts at its group's first row: warp 10 of each CTA gathers its 128 rows'
-// 8 bytes a stage into the atom layout and arrives on the even CTA's "sfull" barrier. The even CTA
-// copies scales to tensor memory and issues M = 256, N = 256, K = 64 MMAs. Eight epilogue warps per
-// CTA read the accumulator out as bf16 and hand it back before they store.
+// Scales reach tensor memory through registers, not through tcgen05.cp: the six copies a stage
+// would need run in order with the MMAs on the tensor pipe and cost 145 of 531 us at 16384 rows x 4096
+// -> 14336 (8 experts). Four scale warps per CTA, one for each lane quarter, write the stage's 24
+// columns with tcgen05.st: the rows' scales, gathered from global memory a group of stages ahead (each
+// warp a quarter of the rows) and shared as atoms; the weights' atoms (laid out once, by the
+// quantiser) brought by TMA with the codes, completing on a barrier of their own CTA. The even CTA
+// issues M = 256, N = 256, K = 64 MMAs. Eight epilogue warps per CTA read the accumulator out as bf16
+// and hand it back before they store.
 #include <cuda_bf16.h>
 
 #include "epilogue.cuh"
@@ -29,20 +31,20 @@ namespace rdot {
 namespace {
 
 constexpr int EPI_WARPS = 8;
-constexpr int SCALE_WARP = 2 + EPI_WARPS;
-constexpr int THREADS = 32 * (SCALE_WARP + 1);
+constexpr int SCALE_WARP = 2 + EPI_WARPS;   // the first of four
+constexpr int THREADS = 32 * (SCALE_WARP + 4);
 constexpr int BM = 256;                // rows per cluster tile
 constexpr int BN = 256;
 constexpr int STAGES = 5;
 constexpr int A_BYTES = 128 * MX4_STAGE_BYTES;       // this CTA's 128 rows
 constexpr int B_BYTES = 128 * MX4_STAGE_BYTES;       // this CTA's 128 columns
-constexpr int SFA_BYTES = 2 * MX4_ATOM_BYTES;        // its rows, 256 elements
-constexpr int SFB_BYTES = 4 * MX4_ATOM_BYTES;        // all 256 columns, 256 elements
-constexpr int STAGE_BYTES = A_BYTES + B_BYTES + SFA_BYTES + SFB_BYTES;
+constexpr int SFB_BYTES = 4 * MX4_ATOM_BYTES;        // the scales of all 256 columns, 256 elements
+constexpr int STAGE_BYTES = A_BYTES + B_BYTES + SFB_BYTES;
 constexpr int RING_BYTES = STAGES * STAGE_BYTES;
 constexpr int EPI_BYTES = EPI_WARPS * EpiStage<false>::BYTES;
-constexpr int BAR_BYTES = (3 * STAGES + 3) * 8;      // full, sfull, empty, tfull, tempty, drain
+constexpr int BAR_BYTES = (4 * STAGES + 4) * 8;      // full, bfull, sfull, empty; tfull, tempty, drain
 constexpr int MISC_BYTES = 16;
+constexpr int SFA_BYTES = 2 * MX4_GROUP_BYTES;       // the rows' scale atoms, two groups of stages
 constexpr int XCH_BYTES = (sizeof(PairExchange<STAGES>) + 15) / 16 * 16;
 constexpr int TMEM_COLS = 512;
 constexpr int TMEM_SF_BASE = BN;                     // after the accumulator
@@ -52,21 +54,15 @@ static_assert(TMEM_SF_BASE + STAGES * SF_COLS <= TMEM_COLS, "tensor memory budge
 constexpr uint32_t EMPTY_ARRIVALS = 2 * EPI_WARPS;
 
 size_t smem_bytes(int G) {
-    return 1024 + RING_BYTES + EPI_BYTES + BAR_BYTES + MISC_BYTES + XCH_BYTES + sizeof(int32_t) * 2 * (G + 1);
+    return 1024 + RING_BYTES + SFA_BYTES + EPI_BYTES + BAR_BYTES + MISC_BYTES + XCH_BYTES + sizeof(int32_t) * 2 * (G + 1);
 }
 
-// mbar_wait with cluster-scope acquire: what the other CTA wrote before its arrive is visible.
-__device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity, const WaitGuard& g) {
-    if (mbar_try_wait_cluster(bar, parity)) return true;
-    const uint64_t t0 = global_timer_ns();
-    while (true) {
-        if (mbar_try_wait_cluster(bar, parity)) return true;
-        if (*g.abort) return false;
-        if (global_timer_ns() - t0 > g.timeout_ns) {
-            guard_fail(g, RDOT_STATUS_BIT_TIMEOUT);
-            return false;
-        }
-    }
+// Arrive on a barrier of the even CTA for work whose only data is tensor memory (scales written, an
+// accumulator read): tcgen05.wait and tcgen05.fence order that data, so the arrive itself need not
+// release this thread's other writes to the cluster. A release at cluster scope took about as long as a
+// stage's MMAs, and one per stage set the kernel's pace (678 against 448 us at the shapes above).
+__device__ __forceinline__ void mbar_arrive_tmem(uint32_t cluster_addr) {
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
@@ -74,17 +70,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                      const __grid_constant__ CUtensorMap tmap_sfb, Mx4Args a) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    uint32_t* epi_stage = reinterpret_cast<uint32_t*>(smem + RING_BYTES);
-    uint64_t* full = reinterpret_cast<uint64_t*>(smem + RING_BYTES + EPI_BYTES);
-    uint64_t* sfull = full + STAGES;
+    uint8_t* sfa_buf = smem + RING_BYTES;
+    uint32_t* epi_stage = reinterpret_cast<uint32_t*>(sfa_buf + SFA_BYTES);
+    uint8_t* bars = sfa_buf + SFA_BYTES + EPI_BYTES;
+    uint64_t* full = reinterpret_cast<uint64_t*>(bars);
+    uint64_t* bfull = full + STAGES;    // this CTA's weight scales of the stage are in shared memory
+    uint64_t* sfull = bfull + STAGES;   // even CTA: both CTAs' scales of the stage are in tensor memory
     uint64_t* empty = sfull + STAGES;
     uint64_t* tfull = empty + STAGES;
     uint64_t* tempty = tfull + 1;
     uint64_t* drain = tempty + 1;
     uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(drain + 1);
     int* abort_flag = reinterpret_cast<int*>(tmem_holder + 1);
-    auto* xch = reinterpret_cast<PairExchange<STAGES>*>(smem + RING_BYTES + EPI_BYTES + BAR_BYTES + MISC_BYTES);
-    int32_t* off = reinterpret_cast<int32_t*>(smem + RING_BYTES + EPI_BYTES + BAR_BYTES + MISC_BYTES + XCH_BYTES);
+    auto* xch = reinterpret_cast<PairExchange<STAGES>*>(bars + BAR_BYTES + MISC_BYTES);
+    int32_t* off = reinterpret_cast<int32_t*>(bars + BAR_BYTES + MISC_BYTES + XCH_BYTES);
     int32_t* tprefix = off + a.G + 1;
 
     const int warp = threadIdx.x >> 5;
@@ -97,7 +96,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; ++s) {
             mbar_init(&full[s], 1);
-            mbar_init(&sfull[s], 2);   // one arrival per CTA, on the even CTA's barrier
+            mbar_init(&bfull[s], 1);
+            mbar_init(&sfull[s], 8);   // the four scale warps of each CTA
             mbar_init(&empty[s], 1);
         }
         mbar_init(tfull, 1);
@@ -131,7 +131,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     if (warp == 0) {
         // ------------------------------------------------------------------ TMA producer (both CTAs)
         if (lane == 0) {
-            uint32_t stage = 0, phase = 0;
+            uint32_t stage = 0, phase = 0, issued_mask = 0, issued_phase = 0;
             int pos = 0;   // load iterations issued (see pairdrain.cuh)
             bool ok = true;
             const int r = static_cast<int>(rank);
@@ -150,13 +150,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                         break;
                     }
                     uint8_t* st = smem + stage * STAGE_BYTES;
-                    if (leader) mbar_arrive_expect_tx(&full[stage], A_BYTES + a1 + B_BYTES + b1 + 2 * SFB_BYTES);
+                    if (leader) mbar_arrive_expect_tx(&full[stage], A_BYTES + a1 + B_BYTES + b1);
                     const uint32_t fb = mapa_shared(smem_u32(&full[stage]), 0);
                     if (my_a) tma_load_2d_pair(st, &tmap_a, fb, ks * MX4_STAGE_BYTES, t.row0 + 128 * r);
                     if (my_b) tma_load_3d_pair(st + A_BYTES, &tmap_b, fb, ks * MX4_STAGE_BYTES, n0 + 128 * r, t.g);
                     // 2 x 256 words: the two column atoms' scales of this stage (zeros past the tensor)
-                    tma_load_2d_pair(st + A_BYTES + B_BYTES + SFA_BYTES, &tmap_sfb, fb, ks * (SFA_BYTES / 4), sfb_row);
-                    xch->share[stage] = a1 + b1 + SFB_BYTES;   // the odd CTA's bytes of this iteration
+                    mbar_arrive_expect_tx(&bfull[stage], SFB_BYTES);
+                    tma_load_2d(st + A_BYTES + B_BYTES, &tmap_sfb, &bfull[stage], ks * (2 * MX4_ATOM_BYTES / 4), sfb_row);
+                    issued_mask |= 1u << stage;
+                    issued_phase = (issued_phase & ~(1u << stage)) | (phase << stage);
+                    xch->share[stage] = a1 + b1;   // the odd CTA's bytes of this iteration
                     ++pos;
                     if (++stage == STAGES) {
                         stage = 0;
@@ -164,46 +167,67 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                     }
                 }
             }
-            // every load either CTA issued lands before either CTA can leave (pairdrain.cuh)
+            // every load either CTA issued lands before either CTA can leave: the scales, which complete
+            // on this CTA's own barriers, then the codes (pairdrain.cuh)
+            if (!ok) {
+                int dummy;
+                const WaitGuard dguard = drain_guard(guard, &dummy);
+                for (int s = 0; s < STAGES; ++s)
+                    if (issued_mask & (1u << s)) (void)mbar_wait(&bfull[s], (issued_phase >> s) & 1u, dguard);
+            }
             pair_drain(xch, full, pos, leader, guard);
         }
         __syncwarp();
-    } else if (warp == SCALE_WARP) {
-        // ------------------------------------------------------------------ row scale gather (both CTAs)
-        // lane l holds rows l, l + 32, l + 64, l + 96 of this CTA's half: 16 bytes of each atom
-        uint32_t stage = 0, phase = 0;
+    } else if (warp >= SCALE_WARP) {
+        // ------------------------------------------------------------------ scales (both CTAs)
+        // (tn, kn) is the group of stages being loaded, one ahead of the one in use, across tiles too
+        const int lq = warp & 3;   // tensor-memory lane quarter, and the quarter of the rows this warp gathers
+        const uint32_t quarter = static_cast<uint32_t>(lq * 32) << 16;
+        const int mine = 128 * static_cast<int>(rank) + 32 * lq + lane;
+        uint32_t stage = 0, phase = 0, buf = 0;
         bool ok = true;
-        for (int w = cluster; w < W && ok; w += nclusters) {
-            const Tile t = decode_tile(w, tprefix, off, a.G, BM, a.NT, m_inner);
-            const int first = 128 * static_cast<int>(rank) + lane;
-            const long long row = static_cast<long long>(t.row0) + first;
-            uint2 cur[4], nxt[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                cur[i] = make_uint2(0u, 0u);
-                if (first + 32 * i < t.rows) cur[i] = lhs_scale_stage(a, row + 32 * i, 0);
-            }
-            for (int ks = 0; ks < a.KS; ++ks) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {   // the next stage's, in flight while this one is stored
-                    nxt[i] = make_uint2(0u, 0u);
-                    if (ks + 1 < a.KS && first + 32 * i < t.rows) nxt[i] = lhs_scale_stage(a, row + 32 * i, ks + 1);
+        uint2 nxt[MX4_GROUP];
+        int wn = cluster, kn = 0;
+        Tile tn{};
+        if (wn < W) {
+            tn = decode_tile(wn, tprefix, off, a.G, BM, a.NT, m_inner);
+            load_scale_group(a, static_cast<long long>(tn.row0) + mine, mine < tn.rows, 0, nxt);
+        }
+        // all four warps run every group to the end, so that they meet at each group's barrier even when
+        // one of them has stopped early (ok false): it then only skips the waits and stores
+        for (int w = cluster; w < W; w += nclusters) {
+            for (int k0 = 0; k0 < a.KS; k0 += MX4_GROUP) {
+                // this buffer was last read two groups ago, before the barrier of the group between
+                put_scale_group(sfa_buf + buf * MX4_GROUP_BYTES, 32 * lq + lane, nxt);
+                kn += MX4_GROUP;
+                if (kn >= a.KS) {
+                    kn = 0;
+                    wn += nclusters;
+                    if (wn < W) tn = decode_tile(wn, tprefix, off, a.G, BM, a.NT, m_inner);
                 }
-                if (!mbar_wait_warp(&empty[stage], phase ^ 1, guard)) {
-                    ok = false;
-                    break;
-                }
-                uint8_t* sf = smem + stage * STAGE_BYTES + A_BYTES + B_BYTES;
-                reinterpret_cast<uint4*>(sf)[lane] = make_uint4(cur[0].x, cur[1].x, cur[2].x, cur[3].x);
-                reinterpret_cast<uint4*>(sf + MX4_ATOM_BYTES)[lane] = make_uint4(cur[0].y, cur[1].y, cur[2].y, cur[3].y);
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&sfull[stage]), 0));
-#pragma unroll
-                for (int i = 0; i < 4; ++i) cur[i] = nxt[i];
-                if (++stage == STAGES) {
-                    stage = 0;
-                    phase ^= 1;
+                if (ok && wn < W) load_scale_group(a, static_cast<long long>(tn.row0) + mine, mine < tn.rows, kn, nxt);
+                named_barrier(1, 128);
+                const uint4* sa = reinterpret_cast<const uint4*>(sfa_buf + buf * MX4_GROUP_BYTES) + lane;
+                buf ^= 1;
+                for (int j = 0; j < min(MX4_GROUP, a.KS - k0) && ok; ++j) {
+                    // the MMAs that read this stage's scale columns are done; the weights' atoms are here
+                    ok = mbar_wait_warp(&empty[stage], phase ^ 1, guard) && mbar_wait_warp(&bfull[stage], phase, guard);
+                    if (!ok) break;
+                    tc_fence_after();
+                    // [column atom][K atom] of 32 x 16 bytes
+                    const uint4* sb = reinterpret_cast<const uint4*>(smem + stage * STAGE_BYTES + A_BYTES + B_BYTES) + lane;
+                    const uint32_t t = tmem_base + TMEM_SF_BASE + SF_COLS * stage + quarter;
+                    tmem_st_32x8(t, sa[64 * j], sb[0]);
+                    tmem_st_32x8(t + 8, sb[64], sa[64 * j + 32]);
+                    tmem_st_32x8(t + 16, sb[32], sb[96]);
+                    tmem_st_wait();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_tmem(mapa_shared(smem_u32(&sfull[stage]), 0));
+                    if (++stage == STAGES) {
+                        stage = 0;
+                        phase ^= 1;
+                    }
                 }
             }
         }
@@ -216,26 +240,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                 if (!mbar_wait(tempty, acc_phase ^ 1, guard)) break;
                 tc_fence_after();
                 for (int ks = 0; ks < a.KS; ++ks) {
-                    if (!mbar_wait(&full[stage], phase, guard) || !mbar_wait_cluster(&sfull[stage], phase, guard)) {
+                    if (!mbar_wait(&full[stage], phase, guard) || !mbar_wait(&sfull[stage], phase, guard)) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
                     const uint32_t sa = smem_u32(smem + stage * STAGE_BYTES);
                     const uint32_t sb = sa + A_BYTES;
-                    const uint32_t sfa = sb + B_BYTES, sfb = sfa + SFA_BYTES;
                     const uint32_t sf_t = tmem_base + TMEM_SF_BASE + SF_COLS * stage;
                     const int steps = min(4, (a.K - ks * MX4_STAGE_K + 63) / 64);   // MMAs of K = 64 with data
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk) {
                         if (kk >= steps) break;
                         const uint32_t a_t = sf_t + 12 * (kk >> 1), b_t = a_t + 4;
-                        if ((kk & 1) == 0) {
-                            const uint32_t atom = (kk >> 1) * MX4_ATOM_BYTES;
-                            tmem_cp_scales<2>(a_t, smem_desc_rows16(sfa + atom));
-                            tmem_cp_scales<2>(b_t, smem_desc_rows16(sfb + atom));
-                            tmem_cp_scales<2>(b_t + 4, smem_desc_rows16(sfb + 2 * MX4_ATOM_BYTES + atom));
-                        }
                         mma_mxf4<2>(tmem_base, smem_desc_sw128(sa + kk * 32, 16, 1024),
                                     smem_desc_sw128(sb + kk * 32, 16, 1024), idesc_mxf4(BM, BN, 2 * (kk & 1)), a_t, b_t,
                                     (ks | kk) != 0 ? 1u : 0u);
@@ -278,7 +295,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
             tmem_read_bf16_32x128(tbase, pk);
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(tempty), 0));
+            if (lane == 0) mbar_arrive_tmem(mapa_shared(smem_u32(tempty), 0));
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
                 const int col = n0 + c * 32;
