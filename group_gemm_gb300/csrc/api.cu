@@ -1454,9 +1454,9 @@ rdot_status rdot_forward_mxfp4(rdot_plan_t plan, const void* lhs, const uint8_t*
     a.KA = static_cast<int>((p.k + 127) / 128);
     a.KS = static_cast<int>((p.k + MX4_STAGE_K - 1) / MX4_STAGE_K);
     a.KB = static_cast<int>(p.k / 32);
-    // rows of lhs scales are read 8 or 4 bytes at a time where every row starts on such a boundary
+    // rows of lhs scales are read 16, 8 or 4 bytes at a time where every row starts on such a boundary
     const uintptr_t sp = reinterpret_cast<uintptr_t>(lhs_scale);
-    a.scale_vec = (a.KB % 8 == 0 && sp % 8 == 0) ? 8 : (a.KB % 4 == 0 && sp % 4 == 0) ? 4 : 1;
+    a.scale_vec = (a.KB % 16 == 0 && sp % 16 == 0) ? 16 : (a.KB % 8 == 0 && sp % 8 == 0) ? 8 : (a.KB % 4 == 0 && sp % 4 == 0) ? 4 : 1;
     a.m_inner = plan->m_inner;
     a.status = static_cast<int32_t*>(workspace);
     a.timeout_ns = plan->timeout_ns;

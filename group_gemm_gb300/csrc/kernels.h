@@ -220,7 +220,7 @@ struct Mx4Args {
     int KA;                       // 128-element scale atoms along K
     int KS;                       // K stages of 256 elements
     int KB;                       // scale blocks along K (K / 32)
-    int scale_vec;                // bytes a lhs scale row can be read by: 8, 4 or 1
+    int scale_vec;                // bytes a lhs scale row can be read by: 16, 8, 4 or 1
     int m_inner;
     int32_t* status;
     uint64_t timeout_ns;

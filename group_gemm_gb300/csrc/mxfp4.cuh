@@ -56,6 +56,42 @@ __device__ __forceinline__ void tmem_cp_scales(uint32_t taddr, uint64_t sdesc) {
         asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(sdesc) : "memory");
 }
 
+// mbar_wait (ptx.cuh) that looks at the clock only after MX4_TRIES waits: reading the global timer takes
+// longer than these rings' waits usually do, and mbar_wait reads it before its second look.
+constexpr int MX4_TRIES = 32;
+
+__device__ __forceinline__ bool mx4_wait(uint64_t* bar, uint32_t parity, const WaitGuard& g) {
+    for (int i = 0; i < MX4_TRIES; ++i)
+        if (mbar_try_wait(bar, parity)) return true;
+    return mbar_wait(bar, parity, g);
+}
+
+__device__ __forceinline__ bool mx4_wait_warp(uint64_t* bar, uint32_t parity, const WaitGuard& g) {
+    int ok = 0;
+    if ((threadIdx.x & 31) == 0) ok = mx4_wait(bar, parity, g) ? 1 : 0;
+    return __shfl_sync(0xffffffffu, ok, 0) != 0;
+}
+
+// A wait by every lane of a warp whose control flow stays uniform: the MMA warps run their loops with all
+// lanes and elect one only for the tcgen05 instructions, so that descriptors and addresses stay in uniform
+// registers. (In a lane-0 branch each MMA took about 100 clocks to issue, more than it takes to run with
+// N = 64; see mxfp4_tc2.cu.)
+__device__ __forceinline__ bool mx4_wait_uniform(uint64_t* bar, uint32_t parity, const WaitGuard& g) {
+    for (int i = 0; i < MX4_TRIES; ++i)
+        if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity, g)) != 0;
+}
+
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(p));
+    return p != 0;
+}
+
 // Eight 32-bit registers of each lane to eight tensor-memory columns of the warp's lane quarter.
 __device__ __forceinline__ void tmem_st_32x8(uint32_t taddr, uint4 a, uint4 b) {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(a.x),
@@ -86,15 +122,26 @@ __device__ __forceinline__ uint2 lhs_scale_stage(const Mx4Args& a, long long row
 
 // Scale gather of a token or row tile. The rows' scales are plain [M, K/32]: a tile starts at its
 // group's first row, so no fixed layout could hold them as atoms. A warp loads one row per lane, the
-// scales of MX4_GROUP consecutive K stages (one 32-byte sector) at a time and one group ahead of the
-// one in use, and puts them into shared memory as atoms, from which the warps that fill tensor memory
+// scales of MX4_GROUP consecutive K stages (64 bytes) at a time and one group ahead of the one in use
+// (groups of 4 stages did not hide the loads: 460 against 4XX us in mxfp4_tc2.cu), and puts them into shared memory as atoms, from which the warps that fill tensor memory
 // read 16 bytes a lane. (Loading four rows a lane in each of them instead cost 512 uncoalesced L1
 // lookups per stage and SM, as much as the stage's MMAs.)
-constexpr int MX4_GROUP = 4;
-constexpr int MX4_GROUP_BYTES = MX4_GROUP * 2 * MX4_ATOM_BYTES;   // atoms of a group: 4 KB
+constexpr int MX4_GROUP = 8;
+constexpr int MX4_GROUP_BYTES = MX4_GROUP * 2 * MX4_ATOM_BYTES;   // atoms of a group: 8 KB
 
 __device__ __forceinline__ void load_scale_group(const Mx4Args& a, long long row, bool live, int ks0,
                                                  uint2 (&v)[MX4_GROUP]) {
+    if (a.scale_vec == 16) {   // whole pairs of stages, 16 bytes each
+        const uint4* p = reinterpret_cast<const uint4*>(a.lhs_scale + row * a.KB) + (ks0 >> 1);
+#pragma unroll
+        for (int j = 0; j < MX4_GROUP; j += 2) {
+            uint4 u = make_uint4(0u, 0u, 0u, 0u);
+            if (live && ks0 + j < a.KS) u = __ldg(p + (j >> 1));
+            v[j] = make_uint2(u.x, u.y);
+            v[j + 1] = make_uint2(u.z, u.w);
+        }
+        return;
+    }
 #pragma unroll
     for (int j = 0; j < MX4_GROUP; ++j) {
         v[j] = make_uint2(0u, 0u);

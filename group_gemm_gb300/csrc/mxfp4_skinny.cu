@@ -140,7 +140,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 const int nx = (t.rows + 15) / 16;
                 const uint8_t* sfw = a.rhs_scale + (static_cast<long long>(t.g) * a.NB + t.nb) * a.KA * MX4_ATOM_BYTES;
                 for (int ks = 0; ks < a.KS; ++ks) {
-                    if (!mbar_wait(&empty[stage], phase ^ 1, guard)) {
+                    if (!mx4_wait(&empty[stage], phase ^ 1, guard)) {
                         ok = false;
                         break;
                     }
@@ -210,7 +210,7 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
                 for (int j = 0; j < MX4_GROUP; ++j) {
                     if (k0 + j >= a.KS) break;
-                    if (!mbar_wait_warp(&empty[stage], phase ^ 1, guard)) {
+                    if (!mx4_wait_warp(&empty[stage], phase ^ 1, guard)) {
                         ok = false;
                         break;
                     }
@@ -235,11 +235,11 @@ __global__ void __launch_bounds__(THREADS, 1)
             for (int u = u0; u < u1 && ok;) {
                 const SkinnyTile t = next_tile(u, u1, a, tprefix, off);
                 const int n = 16 * ((t.rows + 15) / 16);
-                if (!mbar_wait(&tempty[acc], acc_phase ^ 1, guard)) break;
+                if (!mx4_wait(&tempty[acc], acc_phase ^ 1, guard)) break;
                 tc_fence_after();
                 const uint32_t d_tmem = tmem_base + acc * TT;
                 for (int ks = 0; ks < a.KS; ++ks) {
-                    if (!mbar_wait(&full[stage], phase, guard) || !mbar_wait(&sfull[stage], phase, guard)) {
+                    if (!mx4_wait(&full[stage], phase, guard) || !mx4_wait(&sfull[stage], phase, guard)) {
                         ok = false;
                         break;
                     }
@@ -285,7 +285,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out);
         for (int u = u0; u < u1;) {
             const SkinnyTile t = next_tile(u, u1, a, tprefix, off);
-            if (!mbar_wait_warp(&tfull[acc], acc_phase, guard)) break;
+            if (!mx4_wait_warp(&tfull[acc], acc_phase, guard)) break;
             tc_fence_after();
             const int col = t.nb * 128 + q * 32 + lane;
             if (q >= t.q0 && q < t.q1) {

@@ -145,7 +145,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                 const int my_a = r ? a1 : A_BYTES, my_b = r ? b1 : B_BYTES;
                 const int sfb_row = t.g * a.NB + 2 * t.nt;   // two atom rows, 128 columns each
                 for (int ks = 0; ks < a.KS; ++ks) {
-                    if (!mbar_wait(&empty[stage], phase ^ 1, guard)) {
+                    if (!mx4_wait(&empty[stage], phase ^ 1, guard)) {
                         ok = false;
                         break;
                     }
@@ -211,7 +211,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                 buf ^= 1;
                 for (int j = 0; j < min(MX4_GROUP, a.KS - k0) && ok; ++j) {
                     // the MMAs that read this stage's scale columns are done; the weights' atoms are here
-                    ok = mbar_wait_warp(&empty[stage], phase ^ 1, guard) && mbar_wait_warp(&bfull[stage], phase, guard);
+                    ok = mx4_wait_warp(&empty[stage], phase ^ 1, guard) && mx4_wait_warp(&bfull[stage], phase, guard);
                     if (!ok) break;
                     tc_fence_after();
                     // [column atom][K atom] of 32 x 16 bytes
@@ -233,43 +233,48 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         }
     } else if (warp == 1) {
         // ------------------------------------------------------------------ MMA issuer (even CTA)
-        if (lane == 0 && leader) {
+        if (leader) {
+            const bool elected = elect_one();
             uint32_t stage = 0, phase = 0, acc_phase = 0;
             bool ok = true;
             for (int w = cluster; w < W && ok; w += nclusters) {
-                if (!mbar_wait(tempty, acc_phase ^ 1, guard)) break;
+                ok = mx4_wait_uniform(tempty, acc_phase ^ 1, guard);
+                if (!ok) break;
                 tc_fence_after();
                 for (int ks = 0; ks < a.KS; ++ks) {
-                    if (!mbar_wait(&full[stage], phase, guard) || !mbar_wait(&sfull[stage], phase, guard)) {
-                        ok = false;
-                        break;
-                    }
+                    ok = mx4_wait_uniform(&full[stage], phase, guard) && mx4_wait_uniform(&sfull[stage], phase, guard);
+                    if (!ok) break;
                     tc_fence_after();
                     const uint32_t sa = smem_u32(smem + stage * STAGE_BYTES);
-                    const uint32_t sb = sa + A_BYTES;
+                    const uint64_t adesc = smem_desc_sw128(sa, 16, 1024), bdesc = smem_desc_sw128(sa + A_BYTES, 16, 1024);
                     const uint32_t sf_t = tmem_base + TMEM_SF_BASE + SF_COLS * stage;
                     const int steps = min(4, (a.K - ks * MX4_STAGE_K + 63) / 64);   // MMAs of K = 64 with data
+                    if (elected) {
 #pragma unroll
-                    for (int kk = 0; kk < 4; ++kk) {
-                        if (kk >= steps) break;
-                        const uint32_t a_t = sf_t + 12 * (kk >> 1), b_t = a_t + 4;
-                        mma_mxf4<2>(tmem_base, smem_desc_sw128(sa + kk * 32, 16, 1024),
-                                    smem_desc_sw128(sb + kk * 32, 16, 1024), idesc_mxf4(BM, BN, 2 * (kk & 1)), a_t, b_t,
-                                    (ks | kk) != 0 ? 1u : 0u);
+                        for (int kk = 0; kk < 4; ++kk) {
+                            // +32 bytes (descriptor units of 16) per 64 elements inside the swizzled row
+                            const uint32_t a_t = sf_t + 12 * (kk >> 1);
+                            if (kk < steps)
+                                mma_mxf4<2>(tmem_base, adesc + 2 * kk, bdesc + 2 * kk, idesc_mxf4(BM, BN, 2 * (kk & 1)),
+                                            a_t, a_t + 4, (ks | kk) != 0 ? 1u : 0u);
+                        }
+                        mma_commit_pair_multicast(&empty[stage], 0x3);
+                        if (ks + 1 == a.KS) mma_commit_pair_multicast(tfull, 0x3);
                     }
-                    mma_commit_pair_multicast(&empty[stage], 0x3);
+                    __syncwarp();
                     if (++stage == STAGES) {
                         stage = 0;
                         phase ^= 1;
                     }
                 }
-                if (!ok) break;
-                mma_commit_pair_multicast(tfull, 0x3);
                 acc_phase ^= 1;
             }
-            mma_commit_pair(drain);
-            int dummy;
-            (void)mbar_wait(drain, 0, drain_guard(guard, &dummy));
+            // the commit tracks what its own thread issued: one lane is elected once, for all of it
+            if (elected) {
+                mma_commit_pair(drain);
+                int dummy;
+                (void)mbar_wait(drain, 0, drain_guard(guard, &dummy));
+            }
         }
         __syncwarp();
     } else {
@@ -281,7 +286,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         for (int w = cluster; w < W; w += nclusters) {
             const Tile t = decode_tile(w, tprefix, off, a.G, BM, a.NT, m_inner);
             const int n0 = t.nt * BN + half * (BN / 2);
-            const bool ready = mbar_wait_warp(tfull, acc_phase, guard);
+            const bool ready = mx4_wait_warp(tfull, acc_phase, guard);
             if (!ready) break;
             tc_fence_after();
             const uint32_t tbase = tmem_base + half * (BN / 2) + (static_cast<uint32_t>(q * 32) << 16);
