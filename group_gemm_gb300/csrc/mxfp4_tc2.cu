@@ -31,18 +31,21 @@ namespace rdot {
 namespace {
 
 constexpr int EPI_WARPS = 8;
-constexpr int SCALE_WARP = 2 + EPI_WARPS;   // the first of four
+constexpr int EPI_WARP = 4;                          // the first of eight; warps 0..3: codes, MMAs, weight scales, none
+constexpr int SCALE_WARP = EPI_WARP + EPI_WARPS;     // the first of four
 constexpr int THREADS = 32 * (SCALE_WARP + 4);
 constexpr int BM = 256;                // rows per cluster tile
 constexpr int BN = 256;
 constexpr int STAGES = 5;
 constexpr int A_BYTES = 128 * MX4_STAGE_BYTES;       // this CTA's 128 rows
 constexpr int B_BYTES = 128 * MX4_STAGE_BYTES;       // this CTA's 128 columns
-constexpr int SFB_BYTES = 4 * MX4_ATOM_BYTES;        // the scales of all 256 columns, 256 elements
-constexpr int STAGE_BYTES = A_BYTES + B_BYTES + SFB_BYTES;
+constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
 constexpr int RING_BYTES = STAGES * STAGE_BYTES;
+constexpr int SFB_STAGES = 10;                       // the weight scales' own ring runs further ahead
+constexpr int SFB_STAGE_BYTES = 4 * MX4_ATOM_BYTES;  // the scales of all 256 columns, 256 elements
+constexpr int SFB_BYTES = SFB_STAGES * SFB_STAGE_BYTES;
 constexpr int EPI_BYTES = EPI_WARPS * EpiStage<false>::BYTES;
-constexpr int BAR_BYTES = (4 * STAGES + 4) * 8;      // full, bfull, sfull, empty; tfull, tempty, drain
+constexpr int BAR_BYTES = (3 * STAGES + 2 * SFB_STAGES + 4) * 8;   // full, sfull, empty; bfull, bempty; tfull, tempty, drain
 constexpr int MISC_BYTES = 16;
 constexpr int SFA_BYTES = 2 * MX4_GROUP_BYTES;       // the rows' scale atoms, two groups of stages
 constexpr int XCH_BYTES = (sizeof(PairExchange<STAGES>) + 15) / 16 * 16;
@@ -54,7 +57,8 @@ static_assert(TMEM_SF_BASE + STAGES * SF_COLS <= TMEM_COLS, "tensor memory budge
 constexpr uint32_t EMPTY_ARRIVALS = 2 * EPI_WARPS;
 
 size_t smem_bytes(int G) {
-    return 1024 + RING_BYTES + SFA_BYTES + EPI_BYTES + BAR_BYTES + MISC_BYTES + XCH_BYTES + sizeof(int32_t) * 2 * (G + 1);
+    return 1024 + RING_BYTES + SFB_BYTES + SFA_BYTES + EPI_BYTES + BAR_BYTES + MISC_BYTES + XCH_BYTES +
+           sizeof(int32_t) * 2 * (G + 1);
 }
 
 // Arrive on a barrier of the even CTA for work whose only data is tensor memory (scales written, an
@@ -70,14 +74,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                      const __grid_constant__ CUtensorMap tmap_sfb, Mx4Args a) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    uint8_t* sfa_buf = smem + RING_BYTES;
+    uint8_t* sfb_ring = smem + RING_BYTES;
+    uint8_t* sfa_buf = sfb_ring + SFB_BYTES;
     uint32_t* epi_stage = reinterpret_cast<uint32_t*>(sfa_buf + SFA_BYTES);
     uint8_t* bars = sfa_buf + SFA_BYTES + EPI_BYTES;
     uint64_t* full = reinterpret_cast<uint64_t*>(bars);
-    uint64_t* bfull = full + STAGES;    // this CTA's weight scales of the stage are in shared memory
-    uint64_t* sfull = bfull + STAGES;   // even CTA: both CTAs' scales of the stage are in tensor memory
+    uint64_t* sfull = full + STAGES;    // even CTA: both CTAs' scales of the stage are in tensor memory
     uint64_t* empty = sfull + STAGES;
-    uint64_t* tfull = empty + STAGES;
+    uint64_t* bfull = empty + STAGES;         // this CTA's weight scales of a stage are in shared memory
+    uint64_t* bempty = bfull + SFB_STAGES;    // its scale warps have read them
+    uint64_t* tfull = bempty + SFB_STAGES;
     uint64_t* tempty = tfull + 1;
     uint64_t* drain = tempty + 1;
     uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(drain + 1);
@@ -96,9 +102,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; ++s) {
             mbar_init(&full[s], 1);
-            mbar_init(&bfull[s], 1);
             mbar_init(&sfull[s], 8);   // the four scale warps of each CTA
             mbar_init(&empty[s], 1);
+        }
+        for (int s = 0; s < SFB_STAGES; ++s) {
+            mbar_init(&bfull[s], 1);
+            mbar_init(&bempty[s], 4);
         }
         mbar_init(tfull, 1);
         mbar_init(tempty, EMPTY_ARRIVALS);
@@ -130,52 +139,73 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
 
     if (warp == 0) {
         // ------------------------------------------------------------------ TMA producer (both CTAs)
-        if (lane == 0) {
-            uint32_t stage = 0, phase = 0, issued_mask = 0, issued_phase = 0;
-            int pos = 0;   // load iterations issued (see pairdrain.cuh)
-            bool ok = true;
-            const int r = static_cast<int>(rank);
-            for (int w = cluster; w < W && ok; w += nclusters) {
-                const Tile t = decode_tile(w, tprefix, off, a.G, BM, a.NT, m_inner);
-                const int n0 = t.nt * BN;
-                // the odd CTA's A half unless wholly past the group, its B half unless wholly past N:
-                // what is not loaded only feeds rows or columns that are not stored
-                const int a1 = t.rows > 128 ? A_BYTES : 0;
-                const int b1 = (n0 + 128 < a.N) ? B_BYTES : 0;
-                const int my_a = r ? a1 : A_BYTES, my_b = r ? b1 : B_BYTES;
-                const int sfb_row = t.g * a.NB + 2 * t.nt;   // two atom rows, 128 columns each
-                for (int ks = 0; ks < a.KS; ++ks) {
-                    if (!mx4_wait(&empty[stage], phase ^ 1, guard)) {
-                        ok = false;
-                        break;
-                    }
-                    uint8_t* st = smem + stage * STAGE_BYTES;
+        const bool elected = elect_one();
+        uint32_t stage = 0, phase = 0;
+        int pos = 0;   // load iterations issued (see pairdrain.cuh)
+        bool ok = true;
+        const int r = static_cast<int>(rank);
+        for (int w = cluster; w < W && ok; w += nclusters) {
+            const Tile t = decode_tile(w, tprefix, off, a.G, BM, a.NT, m_inner);
+            const int n0 = t.nt * BN;
+            // the odd CTA's A half unless wholly past the group, its B half unless wholly past N: what is
+            // not loaded only feeds rows or columns that are not stored
+            const int a1 = t.rows > 128 ? A_BYTES : 0;
+            const int b1 = (n0 + 128 < a.N) ? B_BYTES : 0;
+            const int my_a = r ? a1 : A_BYTES, my_b = r ? b1 : B_BYTES;
+            for (int ks = 0; ks < a.KS; ++ks) {
+                ok = mx4_wait_uniform(&empty[stage], phase ^ 1, guard);
+                if (!ok) break;
+                uint8_t* st = smem + stage * STAGE_BYTES;
+                const uint32_t fb = mapa_shared(smem_u32(&full[stage]), 0);
+                if (elected) {
                     if (leader) mbar_arrive_expect_tx(&full[stage], A_BYTES + a1 + B_BYTES + b1);
-                    const uint32_t fb = mapa_shared(smem_u32(&full[stage]), 0);
                     if (my_a) tma_load_2d_pair(st, &tmap_a, fb, ks * MX4_STAGE_BYTES, t.row0 + 128 * r);
                     if (my_b) tma_load_3d_pair(st + A_BYTES, &tmap_b, fb, ks * MX4_STAGE_BYTES, n0 + 128 * r, t.g);
-                    // 2 x 256 words: the two column atoms' scales of this stage (zeros past the tensor)
-                    mbar_arrive_expect_tx(&bfull[stage], SFB_BYTES);
-                    tma_load_2d(st + A_BYTES + B_BYTES, &tmap_sfb, &bfull[stage], ks * (2 * MX4_ATOM_BYTES / 4), sfb_row);
-                    issued_mask |= 1u << stage;
-                    issued_phase = (issued_phase & ~(1u << stage)) | (phase << stage);
                     xch->share[stage] = a1 + b1;   // the odd CTA's bytes of this iteration
-                    ++pos;
-                    if (++stage == STAGES) {
-                        stage = 0;
-                        phase ^= 1;
-                    }
+                }
+                __syncwarp();
+                ++pos;
+                if (++stage == STAGES) {
+                    stage = 0;
+                    phase ^= 1;
                 }
             }
-            // every load either CTA issued lands before either CTA can leave: the scales, which complete
-            // on this CTA's own barriers, then the codes (pairdrain.cuh)
-            if (!ok) {
-                int dummy;
-                const WaitGuard dguard = drain_guard(guard, &dummy);
-                for (int s = 0; s < STAGES; ++s)
-                    if (issued_mask & (1u << s)) (void)mbar_wait(&bfull[s], (issued_phase >> s) & 1u, dguard);
+        }
+        // every load either CTA issued lands before either CTA can leave (pairdrain.cuh)
+        if (elected) pair_drain(xch, full, pos, leader, guard);
+        __syncwarp();
+    } else if (warp == 2) {
+        // ------------------------------------------------------------------ weight scale producer (both CTAs)
+        const bool elected = elect_one();
+        uint32_t stage = 0, phase = 0, issued_mask = 0, issued_phase = 0;
+        bool ok = true;
+        for (int w = cluster; w < W && ok; w += nclusters) {
+            const Tile t = decode_tile(w, tprefix, off, a.G, BM, a.NT, m_inner);
+            const int row = t.g * a.NB + 2 * t.nt;   // two rows of the atoms' map: 128 columns each
+            for (int ks = 0; ks < a.KS; ++ks) {
+                ok = mx4_wait_uniform(&bempty[stage], phase ^ 1, guard);
+                if (!ok) break;
+                if (elected) {
+                    // 2 x 256 words: the two column atoms' scales of this stage (zeros past the tensor)
+                    mbar_arrive_expect_tx(&bfull[stage], SFB_STAGE_BYTES);
+                    tma_load_2d(sfb_ring + stage * SFB_STAGE_BYTES, &tmap_sfb, &bfull[stage],
+                                ks * (2 * MX4_ATOM_BYTES / 4), row);
+                }
+                __syncwarp();
+                issued_mask |= 1u << stage;
+                issued_phase = (issued_phase & ~(1u << stage)) | (phase << stage);
+                if (++stage == SFB_STAGES) {
+                    stage = 0;
+                    phase ^= 1;
+                }
             }
-            pair_drain(xch, full, pos, leader, guard);
+        }
+        if (!ok && elected) {
+            // stopping early: let every load still in flight land before the CTA exits
+            int dummy;
+            const WaitGuard dguard = drain_guard(guard, &dummy);
+            for (int s = 0; s < SFB_STAGES; ++s)
+                if (issued_mask & (1u << s)) (void)mbar_wait(&bfull[s], (issued_phase >> s) & 1u, dguard);
         }
         __syncwarp();
     } else if (warp >= SCALE_WARP) {
@@ -184,7 +214,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         const int lq = warp & 3;   // tensor-memory lane quarter, and the quarter of the rows this warp gathers
         const uint32_t quarter = static_cast<uint32_t>(lq * 32) << 16;
         const int mine = 128 * static_cast<int>(rank) + 32 * lq + lane;
-        uint32_t stage = 0, phase = 0, buf = 0;
+        uint32_t stage = 0, phase = 0, bstage = 0, bphase = 0, buf = 0;
         bool ok = true;
         uint2 nxt[MX4_GROUP];
         int wn = cluster, kn = 0;
@@ -210,12 +240,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                 const uint4* sa = reinterpret_cast<const uint4*>(sfa_buf + buf * MX4_GROUP_BYTES) + lane;
                 buf ^= 1;
                 for (int j = 0; j < min(MX4_GROUP, a.KS - k0) && ok; ++j) {
-                    // the MMAs that read this stage's scale columns are done; the weights' atoms are here
-                    ok = mx4_wait_warp(&empty[stage], phase ^ 1, guard) && mx4_wait_warp(&bfull[stage], phase, guard);
+                    // the weights' atoms are here, and the MMAs that read this stage's scale columns are done
+                    ok = mx4_wait_warp(&bfull[bstage], bphase, guard) && mx4_wait_warp(&empty[stage], phase ^ 1, guard);
                     if (!ok) break;
                     tc_fence_after();
                     // [column atom][K atom] of 32 x 16 bytes
-                    const uint4* sb = reinterpret_cast<const uint4*>(smem + stage * STAGE_BYTES + A_BYTES + B_BYTES) + lane;
+                    const uint4* sb = reinterpret_cast<const uint4*>(sfb_ring + bstage * SFB_STAGE_BYTES) + lane;
                     const uint32_t t = tmem_base + TMEM_SF_BASE + SF_COLS * stage + quarter;
                     tmem_st_32x8(t, sa[64 * j], sb[0]);
                     tmem_st_32x8(t + 8, sb[64], sa[64 * j + 32]);
@@ -223,7 +253,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                     tmem_st_wait();
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive_tmem(mapa_shared(smem_u32(&sfull[stage]), 0));
+                    if (lane == 0) {
+                        mbar_arrive(&bempty[bstage]);
+                        mbar_arrive_tmem(mapa_shared(smem_u32(&sfull[stage]), 0));
+                    }
+                    if (++bstage == SFB_STAGES) {
+                        bstage = 0;
+                        bphase ^= 1;
+                    }
                     if (++stage == STAGES) {
                         stage = 0;
                         phase ^= 1;
@@ -277,11 +314,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
             }
         }
         __syncwarp();
-    } else {
+    } else if (warp >= EPI_WARP) {
         // ------------------------------------------------------------------ epilogue (both CTAs)
         const int q = warp & 3;
-        const int half = (warp - 2) / 4;
-        uint32_t* stage_buf = epi_stage + (warp - 2) * EpiStage<false>::WORDS;
+        const int half = (warp - EPI_WARP) / 4;
+        uint32_t* stage_buf = epi_stage + (warp - EPI_WARP) * EpiStage<false>::WORDS;
         uint32_t acc_phase = 0;
         for (int w = cluster; w < W; w += nclusters) {
             const Tile t = decode_tile(w, tprefix, off, a.G, BM, a.NT, m_inner);
@@ -318,7 +355,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                 const long long per = (nv + gridDim.x - 1) / gridDim.x;
                 const long long s = per * blockIdx.x;
                 const long long e = min(nv, s + per);
-                for (long long i = s + (threadIdx.x - 64); i < e; i += 32 * EPI_WARPS) base[i] = make_uint4(0, 0, 0, 0);
+                for (long long i = s + (threadIdx.x - 32 * EPI_WARP); i < e; i += 32 * EPI_WARPS) base[i] = make_uint4(0, 0, 0, 0);
             }
         }
     }
