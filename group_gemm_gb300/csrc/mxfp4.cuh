@@ -121,11 +121,9 @@ __device__ __forceinline__ uint2 lhs_scale_stage(const Mx4Args& a, long long row
 }
 
 // Scale gather of a token or row tile. The rows' scales are plain [M, K/32]: a tile starts at its
-// group's first row, so no fixed layout could hold them as atoms. A warp loads one row per lane, the
-// scales of MX4_GROUP consecutive K stages (64 bytes) at a time and one group ahead of the one in use
-// (groups of 4 stages did not hide the loads: 460 against 4XX us in mxfp4_tc2.cu), and puts them into shared memory as atoms, from which the warps that fill tensor memory
-// read 16 bytes a lane. (Loading four rows a lane in each of them instead cost 512 uncoalesced L1
-// lookups per stage and SM, as much as the stage's MMAs.)
+// group's first row, so no fixed layout could hold them as atoms. A warp loads a row per lane at a time,
+// the scales of MX4_GROUP consecutive K stages (64 bytes), one group ahead of the one in use, and puts
+// them into shared memory as atoms, from which the warps that fill tensor memory read 16 bytes a lane.
 constexpr int MX4_GROUP = 8;
 constexpr int MX4_GROUP_BYTES = MX4_GROUP * 2 * MX4_ATOM_BYTES;   // atoms of a group: 8 KB
 
@@ -157,11 +155,6 @@ __device__ __forceinline__ void put_scale_group(uint8_t* atoms, int r, const uin
         *reinterpret_cast<uint32_t*>(p + 2 * j * MX4_ATOM_BYTES) = v[j].x;
         *reinterpret_cast<uint32_t*>(p + (2 * j + 1) * MX4_ATOM_BYTES) = v[j].y;
     }
-}
-
-// Barrier of `threads` threads on hardware barrier `id` (1 .. 15; __syncthreads is 0).
-__device__ __forceinline__ void named_barrier(int id, int threads) {
-    asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
 
 }  // namespace rdot

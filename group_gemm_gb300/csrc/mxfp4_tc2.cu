@@ -11,11 +11,16 @@
 // Scales reach tensor memory through registers, not through tcgen05.cp: the six copies a stage
 // would need run in order with the MMAs on the tensor pipe and cost 145 of 531 us at 16384 rows x 4096
 // -> 14336 (8 experts). Four scale warps per CTA, one for each lane quarter, write the stage's 24
-// columns with tcgen05.st: the rows' scales, gathered from global memory a group of stages ahead (each
-// warp a quarter of the rows) and shared as atoms; the weights' atoms (laid out once, by the
-// quantiser) brought by TMA with the codes, completing on a barrier of their own CTA. The even CTA
-// issues M = 256, N = 256, K = 64 MMAs. Eight epilogue warps per CTA read the accumulator out as bf16
-// and hand it back before they store.
+// columns with tcgen05.st: the rows' scales, gathered by another warp from global memory a group of
+// stages ahead and put down as atoms; the weights' atoms (laid out once, by the quantiser), brought by
+// TMA in a ring of their own. The even CTA
+// issues M = 256, N = 256, K = 64 MMAs.
+//
+// Two accumulators share their middle: tensor memory holds 512 columns, the scales of five stages take
+// 120, and a tile 256, so even tiles accumulate in columns [0, 256) and odd ones in [128, 384). The eight
+// epilogue warps of a CTA read a tile's shared half out first, 64 columns each, and hand it back; the
+// next tile then starts while they read the other half and store. (With one accumulator the MMAs waited
+// about 2000 clocks a tile for the read-out.)
 #include <cuda_bf16.h>
 
 #include "epilogue.cuh"
@@ -31,7 +36,7 @@ namespace rdot {
 namespace {
 
 constexpr int EPI_WARPS = 8;
-constexpr int EPI_WARP = 4;                          // the first of eight; warps 0..3: codes, MMAs, weight scales, none
+constexpr int EPI_WARP = 4;                          // the first of eight; warps 0..3: codes, MMAs, weight scales, row scales
 constexpr int SCALE_WARP = EPI_WARP + EPI_WARPS;     // the first of four
 constexpr int THREADS = 32 * (SCALE_WARP + 4);
 constexpr int BM = 256;                // rows per cluster tile
@@ -45,12 +50,13 @@ constexpr int SFB_STAGES = 10;                       // the weight scales' own r
 constexpr int SFB_STAGE_BYTES = 4 * MX4_ATOM_BYTES;  // the scales of all 256 columns, 256 elements
 constexpr int SFB_BYTES = SFB_STAGES * SFB_STAGE_BYTES;
 constexpr int EPI_BYTES = EPI_WARPS * EpiStage<false>::BYTES;
-constexpr int BAR_BYTES = (3 * STAGES + 2 * SFB_STAGES + 4) * 8;   // full, sfull, empty; bfull, bempty; tfull, tempty, drain
+constexpr int BAR_BYTES = (3 * STAGES + 2 * SFB_STAGES + 8) / 2 * 16;   // full, sfull, empty; bfull, bempty; afull[2],
+                                                                       // aempty[2], tfull, tempty, drain
 constexpr int MISC_BYTES = 16;
 constexpr int SFA_BYTES = 2 * MX4_GROUP_BYTES;       // the rows' scale atoms, two groups of stages
 constexpr int XCH_BYTES = (sizeof(PairExchange<STAGES>) + 15) / 16 * 16;
 constexpr int TMEM_COLS = 512;
-constexpr int TMEM_SF_BASE = BN;                     // after the accumulator
+constexpr int TMEM_SF_BASE = BN + BN / 2;            // after the two overlapping accumulators
 constexpr int SF_COLS = 2 * (4 + 8);                 // per stage: two atoms of A and two of B (256 columns)
 static_assert(STAGE_BYTES % 1024 == 0, "swizzle atoms stay 1 KB aligned");
 static_assert(TMEM_SF_BASE + STAGES * SF_COLS <= TMEM_COLS, "tensor memory budget");
@@ -69,6 +75,20 @@ __device__ __forceinline__ void mbar_arrive_tmem(uint32_t cluster_addr) {
     asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 
+// 32 rows x 64 accumulator columns of this warp's lane quarter as packed bf16: pk[c][j] holds columns
+// 32c + 2j, 32c + 2j + 1 of row `lane`. Both loads are in flight together.
+__device__ __forceinline__ void tmem_read_bf16_32x64(uint32_t taddr, uint32_t (&pk)[2][16]) {
+    uint32_t v0[32], v1[32];
+    tmem_ld_32x32b_x32(taddr, v0);
+    tmem_ld_32x32b_x32(taddr + 32, v1);
+    tmem_ld_wait();
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+        pk[0][j] = pack_bf16x2(__uint_as_float(v0[2 * j]), __uint_as_float(v0[2 * j + 1]));
+        pk[1][j] = pack_bf16x2(__uint_as_float(v1[2 * j]), __uint_as_float(v1[2 * j + 1]));
+    }
+}
+
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     mxfp4_tc2_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ CUtensorMap tmap_b,
                      const __grid_constant__ CUtensorMap tmap_sfb, Mx4Args a) {
@@ -83,7 +103,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     uint64_t* empty = sfull + STAGES;
     uint64_t* bfull = empty + STAGES;         // this CTA's weight scales of a stage are in shared memory
     uint64_t* bempty = bfull + SFB_STAGES;    // its scale warps have read them
-    uint64_t* tfull = bempty + SFB_STAGES;
+    uint64_t* afull = bempty + SFB_STAGES;    // this CTA's row scales of a group of stages, two buffers
+    uint64_t* aempty = afull + 2;
+    uint64_t* tfull = aempty + 2;
     uint64_t* tempty = tfull + 1;
     uint64_t* drain = tempty + 1;
     uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(drain + 1);
@@ -108,6 +130,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         for (int s = 0; s < SFB_STAGES; ++s) {
             mbar_init(&bfull[s], 1);
             mbar_init(&bempty[s], 4);
+        }
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(&afull[s], 1);
+            mbar_init(&aempty[s], 4);
         }
         mbar_init(tfull, 1);
         mbar_init(tempty, EMPTY_ARRIVALS);
@@ -208,63 +234,85 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                 if (issued_mask & (1u << s)) (void)mbar_wait(&bfull[s], (issued_phase >> s) & 1u, dguard);
         }
         __syncwarp();
-    } else if (warp >= SCALE_WARP) {
-        // ------------------------------------------------------------------ scales (both CTAs)
-        // (tn, kn) is the group of stages being loaded, one ahead of the one in use, across tiles too
-        const int lq = warp & 3;   // tensor-memory lane quarter, and the quarter of the rows this warp gathers
-        const uint32_t quarter = static_cast<uint32_t>(lq * 32) << 16;
-        const int mine = 128 * static_cast<int>(rank) + 32 * lq + lane;
-        uint32_t stage = 0, phase = 0, bstage = 0, bphase = 0, buf = 0;
+    } else if (warp == 3) {
+        // ------------------------------------------------------------------ row scale gather (both CTAs)
+        // lane l loads rows l, l + 32, l + 64, l + 96 of this CTA's half. (tn, kn) is the group of stages
+        // being loaded, one ahead of the one being stored, across tiles too
+        const int first = 128 * static_cast<int>(rank) + lane;
+        uint32_t buf = 0, phase = 0;
         bool ok = true;
-        uint2 nxt[MX4_GROUP];
+        uint2 nxt[4][MX4_GROUP];
         int wn = cluster, kn = 0;
         Tile tn{};
+        const auto load = [&] {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                load_scale_group(a, static_cast<long long>(tn.row0) + first + 32 * i, first + 32 * i < tn.rows, kn, nxt[i]);
+        };
         if (wn < W) {
             tn = decode_tile(wn, tprefix, off, a.G, BM, a.NT, m_inner);
-            load_scale_group(a, static_cast<long long>(tn.row0) + mine, mine < tn.rows, 0, nxt);
+            load();
         }
-        // all four warps run every group to the end, so that they meet at each group's barrier even when
-        // one of them has stopped early (ok false): it then only skips the waits and stores
-        for (int w = cluster; w < W; w += nclusters) {
-            for (int k0 = 0; k0 < a.KS; k0 += MX4_GROUP) {
-                // this buffer was last read two groups ago, before the barrier of the group between
-                put_scale_group(sfa_buf + buf * MX4_GROUP_BYTES, 32 * lq + lane, nxt);
-                kn += MX4_GROUP;
-                if (kn >= a.KS) {
-                    kn = 0;
-                    wn += nclusters;
-                    if (wn < W) tn = decode_tile(wn, tprefix, off, a.G, BM, a.NT, m_inner);
+        while (wn < W) {
+            ok = mx4_wait_uniform(&aempty[buf], phase ^ 1, guard);
+            if (!ok) break;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) put_scale_group(sfa_buf + buf * MX4_GROUP_BYTES, lane + 32 * i, nxt[i]);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&afull[buf]);
+            buf ^= 1;
+            phase ^= buf == 0 ? 1 : 0;
+            kn += MX4_GROUP;
+            if (kn >= a.KS) {
+                kn = 0;
+                wn += nclusters;
+                if (wn < W) tn = decode_tile(wn, tprefix, off, a.G, BM, a.NT, m_inner);
+            }
+            if (wn < W) load();
+        }
+    } else if (warp >= SCALE_WARP) {
+        // ------------------------------------------------------------------ scales (both CTAs)
+        const uint32_t quarter = static_cast<uint32_t>((warp & 3) * 32) << 16;   // this warp's tensor-memory lanes
+        uint32_t stage = 0, phase = 0, bstage = 0, bphase = 0, buf = 0, aphase = 0;
+        bool ok = true;
+        for (int w = cluster; w < W && ok; w += nclusters) {
+            for (int ks = 0; ks < a.KS; ++ks) {
+                const int j = ks % MX4_GROUP;
+                if (j == 0) ok = mx4_wait_uniform(&afull[buf], aphase, guard);
+                ok = ok && mx4_wait_uniform(&bfull[bstage], bphase, guard);
+                if (!ok) break;
+                // rows: [K atom]; weights: [column atom][K atom] of 32 x 16 bytes
+                const uint4* sa = reinterpret_cast<const uint4*>(sfa_buf + buf * MX4_GROUP_BYTES) + 64 * j + lane;
+                const uint4* sb = reinterpret_cast<const uint4*>(sfb_ring + bstage * SFB_STAGE_BYTES) + lane;
+                const uint4 a0 = sa[0], a1 = sa[32], b00 = sb[0], b01 = sb[32], b10 = sb[64], b11 = sb[96];
+                ok = mx4_wait_uniform(&empty[stage], phase ^ 1, guard);   // the MMAs that read these columns are done
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t t = tmem_base + TMEM_SF_BASE + SF_COLS * stage + quarter;
+                tmem_st_32x8(t, a0, b00);
+                tmem_st_32x8(t + 8, b10, a1);
+                tmem_st_32x8(t + 16, b01, b11);
+                const bool last = j == MX4_GROUP - 1 || ks + 1 == a.KS;   // of this buffer of row scales
+                __syncwarp();
+                if (lane == 0) {   // every lane's values are in registers, taken by the stores above
+                    mbar_arrive(&bempty[bstage]);
+                    if (last) mbar_arrive(&aempty[buf]);
                 }
-                if (ok && wn < W) load_scale_group(a, static_cast<long long>(tn.row0) + mine, mine < tn.rows, kn, nxt);
-                named_barrier(1, 128);
-                const uint4* sa = reinterpret_cast<const uint4*>(sfa_buf + buf * MX4_GROUP_BYTES) + lane;
-                buf ^= 1;
-                for (int j = 0; j < min(MX4_GROUP, a.KS - k0) && ok; ++j) {
-                    // the weights' atoms are here, and the MMAs that read this stage's scale columns are done
-                    ok = mx4_wait_warp(&bfull[bstage], bphase, guard) && mx4_wait_warp(&empty[stage], phase ^ 1, guard);
-                    if (!ok) break;
-                    tc_fence_after();
-                    // [column atom][K atom] of 32 x 16 bytes
-                    const uint4* sb = reinterpret_cast<const uint4*>(sfb_ring + bstage * SFB_STAGE_BYTES) + lane;
-                    const uint32_t t = tmem_base + TMEM_SF_BASE + SF_COLS * stage + quarter;
-                    tmem_st_32x8(t, sa[64 * j], sb[0]);
-                    tmem_st_32x8(t + 8, sb[64], sa[64 * j + 32]);
-                    tmem_st_32x8(t + 16, sb[32], sb[96]);
-                    tmem_st_wait();
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) {
-                        mbar_arrive(&bempty[bstage]);
-                        mbar_arrive_tmem(mapa_shared(smem_u32(&sfull[stage]), 0));
-                    }
-                    if (++bstage == SFB_STAGES) {
-                        bstage = 0;
-                        bphase ^= 1;
-                    }
-                    if (++stage == STAGES) {
-                        stage = 0;
-                        phase ^= 1;
-                    }
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_tmem(mapa_shared(smem_u32(&sfull[stage]), 0));
+                if (last) {
+                    buf ^= 1;
+                    aphase ^= buf == 0 ? 1 : 0;
+                }
+                if (++bstage == SFB_STAGES) {
+                    bstage = 0;
+                    bphase ^= 1;
+                }
+                if (++stage == STAGES) {
+                    stage = 0;
+                    phase ^= 1;
                 }
             }
         }
@@ -278,6 +326,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                 ok = mx4_wait_uniform(tempty, acc_phase ^ 1, guard);
                 if (!ok) break;
                 tc_fence_after();
+                const uint32_t d_tmem = tmem_base + (acc_phase ? BN / 2 : 0);   // tiles alternate
                 for (int ks = 0; ks < a.KS; ++ks) {
                     ok = mx4_wait_uniform(&full[stage], phase, guard) && mx4_wait_uniform(&sfull[stage], phase, guard);
                     if (!ok) break;
@@ -292,7 +341,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                             // +32 bytes (descriptor units of 16) per 64 elements inside the swizzled row
                             const uint32_t a_t = sf_t + 12 * (kk >> 1);
                             if (kk < steps)
-                                mma_mxf4<2>(tmem_base, adesc + 2 * kk, bdesc + 2 * kk, idesc_mxf4(BM, BN, 2 * (kk & 1)),
+                                mma_mxf4<2>(d_tmem, adesc + 2 * kk, bdesc + 2 * kk, idesc_mxf4(BM, BN, 2 * (kk & 1)),
                                             a_t, a_t + 4, (ks | kk) != 0 ? 1u : 0u);
                         }
                         mma_commit_pair_multicast(&empty[stage], 0x3);
@@ -322,27 +371,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         uint32_t acc_phase = 0;
         for (int w = cluster; w < W; w += nclusters) {
             const Tile t = decode_tile(w, tprefix, off, a.G, BM, a.NT, m_inner);
-            const int n0 = t.nt * BN + half * (BN / 2);
             const bool ready = mx4_wait_warp(tfull, acc_phase, guard);
             if (!ready) break;
             tc_fence_after();
-            const uint32_t tbase = tmem_base + half * (BN / 2) + (static_cast<uint32_t>(q * 32) << 16);
             const int first = 128 * static_cast<int>(rank) + q * 32;
             const int rows_valid = t.rows - first;
             __nv_bfloat16* out_rows =
                 static_cast<__nv_bfloat16*>(a.out) + (static_cast<long long>(t.row0) + first) * a.N;
-            // read this warp's 32 x 128 block out as bf16, hand the accumulator back, then store
-            // while the pair's next tile runs
-            uint32_t pk[4][16];
-            tmem_read_bf16_32x128(tbase, pk);
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_tmem(mapa_shared(smem_u32(tempty), 0));
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                const int col = n0 + c * 32;
-                if (rows_valid > 0 && col < a.N)
-                    store_packed_bf16_32x32(pk[c], stage_buf, out_rows + col, a.N, rows_valid, a.N - col);
+            for (int part = 0; part < 2; ++part) {
+                // part 0: the half the accumulators share (columns 128.. of an even tile, 0.. of an odd one),
+                // tensor-memory columns [128, 256); part 1: the tile's own, [0, 128) or [256, 384)
+                const int tcol = (part == 0 ? BN / 2 : acc_phase ? BN : 0) + 64 * half;
+                const int col0 = t.nt * BN + ((part == 0) != (acc_phase != 0) ? BN / 2 : 0) + 64 * half;
+                uint32_t pk[2][16];
+                tmem_read_bf16_32x64(tmem_base + tcol + (static_cast<uint32_t>(q * 32) << 16), pk);
+                tc_fence_before();
+                if (part == 0) {
+                    // this warp has also read all of the tile before: the next tile may start
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_tmem(mapa_shared(smem_u32(tempty), 0));
+                }
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    const int col = col0 + c * 32;
+                    if (rows_valid > 0 && col < a.N)
+                        store_packed_bf16_32x32(pk[c], stage_buf, out_rows + col, a.N, rows_valid, a.N - col);
+                }
             }
             acc_phase ^= 1;
         }
