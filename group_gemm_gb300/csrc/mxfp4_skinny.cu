@@ -131,21 +131,20 @@ __global__ void __launch_bounds__(THREADS, 1)
 
     if (warp == 0) {
         // ------------------------------------------------------------------ TMA producer
-        if (lane == 0) {
-            const uint64_t x_policy = l2_policy_evict_last();   // a token tile is read by every column tile
-            uint32_t stage = 0, phase = 0, issued_mask = 0, issued_phase = 0;
-            bool ok = true;
-            for (int u = u0; u < u1 && ok;) {
-                const SkinnyTile t = next_tile(u, u1, a, tprefix, off);
-                const int nx = (t.rows + 15) / 16;
-                const uint8_t* sfw = a.rhs_scale + (static_cast<long long>(t.g) * a.NB + t.nb) * a.KA * MX4_ATOM_BYTES;
-                for (int ks = 0; ks < a.KS; ++ks) {
-                    if (!mx4_wait(&empty[stage], phase ^ 1, guard)) {
-                        ok = false;
-                        break;
-                    }
-                    uint8_t* st = smem + stage * STAGE_BYTES;
-                    const int atoms = min(2, a.KA - 2 * ks);
+        const bool elected = elect_one();
+        const uint64_t x_policy = l2_policy_evict_last();   // a token tile is read by every column tile
+        uint32_t stage = 0, phase = 0, issued_mask = 0, issued_phase = 0;
+        bool ok = true;
+        for (int u = u0; u < u1 && ok;) {
+            const SkinnyTile t = next_tile(u, u1, a, tprefix, off);
+            const int nx = (t.rows + 15) / 16;
+            const uint8_t* sfw = a.rhs_scale + (static_cast<long long>(t.g) * a.NB + t.nb) * a.KA * MX4_ATOM_BYTES;
+            for (int ks = 0; ks < a.KS; ++ks) {
+                ok = mx4_wait_uniform(&empty[stage], phase ^ 1, guard);
+                if (!ok) break;
+                uint8_t* st = smem + stage * STAGE_BYTES;
+                const int atoms = min(2, a.KA - 2 * ks);
+                if (elected) {
                     mbar_arrive_expect_tx(&full[stage],
                                           (t.q1 - t.q0) * Q_BYTES + nx * X_BOX + atoms * MX4_ATOM_BYTES);
                     // rows past N and bytes past K arrive as zeros
@@ -157,21 +156,22 @@ __global__ void __launch_bounds__(THREADS, 1)
                                          t.row0 + 16 * j, x_policy);
                     bulk_load(st + W_BYTES + X_BYTES, sfw + static_cast<long long>(ks) * SF_BYTES,
                               atoms * MX4_ATOM_BYTES, &full[stage]);
-                    issued_mask |= 1u << stage;
-                    issued_phase = (issued_phase & ~(1u << stage)) | (phase << stage);
-                    if (++stage == STAGES) {
-                        stage = 0;
-                        phase ^= 1;
-                    }
+                }
+                __syncwarp();
+                issued_mask |= 1u << stage;
+                issued_phase = (issued_phase & ~(1u << stage)) | (phase << stage);
+                if (++stage == STAGES) {
+                    stage = 0;
+                    phase ^= 1;
                 }
             }
-            if (!ok) {
-                // stopping early: let every load still in flight land before the CTA exits
-                int dummy;
-                const WaitGuard dguard = drain_guard(guard, &dummy);
-                for (int s = 0; s < STAGES; ++s)
-                    if (issued_mask & (1u << s)) (void)mbar_wait(&full[s], (issued_phase >> s) & 1u, dguard);
-            }
+        }
+        if (!ok && elected) {
+            // stopping early: let every load still in flight land before the CTA exits
+            int dummy;
+            const WaitGuard dguard = drain_guard(guard, &dummy);
+            for (int s = 0; s < STAGES; ++s)
+                if (issued_mask & (1u << s)) (void)mbar_wait(&full[s], (issued_phase >> s) & 1u, dguard);
         }
         __syncwarp();
     } else if (warp == 6) {
@@ -210,10 +210,8 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
                 for (int j = 0; j < MX4_GROUP; ++j) {
                     if (k0 + j >= a.KS) break;
-                    if (!mx4_wait_warp(&empty[stage], phase ^ 1, guard)) {
-                        ok = false;
-                        break;
-                    }
+                    ok = mx4_wait_uniform(&empty[stage], phase ^ 1, guard);
+                    if (!ok) break;
                     uint8_t* sf = smem + stage * STAGE_BYTES + W_BYTES + X_BYTES + SF_BYTES;
                     reinterpret_cast<uint4*>(sf)[lane] = make_uint4(c0[j].x, c1[j].x, 0u, 0u);
                     reinterpret_cast<uint4*>(sf + MX4_ATOM_BYTES)[lane] = make_uint4(c0[j].y, c1[j].y, 0u, 0u);
@@ -229,49 +227,53 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
     } else if (warp == 1) {
         // ------------------------------------------------------------------ MMA issuer
-        if (lane == 0) {
-            uint32_t stage = 0, phase = 0, acc = 0, acc_phase = 0;
-            bool ok = true;
-            for (int u = u0; u < u1 && ok;) {
-                const SkinnyTile t = next_tile(u, u1, a, tprefix, off);
-                const int n = 16 * ((t.rows + 15) / 16);
-                if (!mx4_wait(&tempty[acc], acc_phase ^ 1, guard)) break;
+        const bool elected = elect_one();
+        uint32_t stage = 0, phase = 0, acc = 0, acc_phase = 0;
+        bool ok = true;
+        for (int u = u0; u < u1 && ok;) {
+            const SkinnyTile t = next_tile(u, u1, a, tprefix, off);
+            const int n = 16 * ((t.rows + 15) / 16);
+            ok = mx4_wait_uniform(&tempty[acc], acc_phase ^ 1, guard);
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t d_tmem = tmem_base + acc * TT;
+            const uint32_t idesc0 = idesc_mxf4(128, n, 0), idesc1 = idesc_mxf4(128, n, 2);
+            for (int ks = 0; ks < a.KS; ++ks) {
+                ok = mx4_wait_uniform(&full[stage], phase, guard) && mx4_wait_uniform(&sfull[stage], phase, guard);
+                if (!ok) break;
                 tc_fence_after();
-                const uint32_t d_tmem = tmem_base + acc * TT;
-                for (int ks = 0; ks < a.KS; ++ks) {
-                    if (!mx4_wait(&full[stage], phase, guard) || !mx4_wait(&sfull[stage], phase, guard)) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
-                    const uint32_t sw = smem_u32(smem + stage * STAGE_BYTES);
-                    const uint32_t sx = sw + W_BYTES;
-                    const uint32_t sf = sx + X_BYTES;
-                    const uint32_t sf_t = tmem_base + TMEM_SF_BASE + SF_COLS * stage;
-                    const int steps = min(4, (a.K - ks * MX4_STAGE_K + 63) / 64);   // MMAs of K = 64 with data
+                const uint32_t sw = smem_u32(smem + stage * STAGE_BYTES);
+                const uint64_t wdesc = smem_desc_sw128(sw, 16, 1024), xdesc = smem_desc_sw128(sw + W_BYTES, 16, 1024);
+                const uint64_t sfdesc = smem_desc_rows16(sw + W_BYTES + X_BYTES);
+                const uint32_t sf_t = tmem_base + TMEM_SF_BASE + SF_COLS * stage;
+                const int steps = min(4, (a.K - ks * MX4_STAGE_K + 63) / 64);   // MMAs of K = 64 with data
+                if (elected) {
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk) {
                         if (kk >= steps) break;
+                        // descriptor addresses count 16 bytes: an atom is 32, 64 elements of a row 2
                         const uint32_t w_t = sf_t + 8 * (kk >> 1), x_t = w_t + 4;
                         if ((kk & 1) == 0) {
-                            tmem_cp_scales<1>(w_t, smem_desc_rows16(sf + (kk >> 1) * MX4_ATOM_BYTES));
-                            tmem_cp_scales<1>(x_t, smem_desc_rows16(sf + SF_BYTES + (kk >> 1) * MX4_ATOM_BYTES));
+                            tmem_cp_scales<1>(w_t, sfdesc + (kk >> 1) * 32);
+                            tmem_cp_scales<1>(x_t, sfdesc + (SF_BYTES / 16) + (kk >> 1) * 32);
                         }
-                        mma_mxf4<1>(d_tmem, smem_desc_sw128(sw + kk * 32, 16, 1024), smem_desc_sw128(sx + kk * 32, 16, 1024),
-                                    idesc_mxf4(128, n, 2 * (kk & 1)), w_t, x_t, (ks | kk) != 0 ? 1u : 0u);
+                        mma_mxf4<1>(d_tmem, wdesc + 2 * kk, xdesc + 2 * kk, (kk & 1) ? idesc1 : idesc0, w_t, x_t,
+                                    (ks | kk) != 0 ? 1u : 0u);
                     }
                     mma_commit(&empty[stage]);
-                    if (++stage == STAGES) {
-                        stage = 0;
-                        phase ^= 1;
-                    }
+                    if (ks + 1 == a.KS) mma_commit(&tfull[acc]);
                 }
-                if (!ok) break;
-                mma_commit(&tfull[acc]);
-                acc ^= 1;
-                if (acc == 0) acc_phase ^= 1;
+                __syncwarp();
+                if (++stage == STAGES) {
+                    stage = 0;
+                    phase ^= 1;
+                }
             }
-            // all MMAs issued by this thread complete before teardown frees TMEM
+            acc ^= 1;
+            if (acc == 0) acc_phase ^= 1;
+        }
+        // all MMAs issued by this thread complete before teardown frees TMEM
+        if (elected) {
             mma_commit(drain);
             int dummy;
             const WaitGuard dguard = drain_guard(guard, &dummy);
