@@ -407,8 +407,8 @@ rdot_status rdot_plan(const rdot_problem* problem, int device, rdot_plan_t* plan
         pl->skinny = want_mx4_skinny(p);
         pl->pair = !pl->skinny;
         pl->tile_m = pl->skinny ? MX4_SKINNY_ROWS : TC2_BM;
-        pl->tile_n = pl->skinny ? 32 : 256;   // the swapped kernel's work is counted in 32-column quarters
-        if (pl->skinny) pl->m_inner = 0;
+        pl->tile_n = pl->skinny ? 128 : 256;
+        if (pl->skinny) pl->m_inner = 1;   // the token tiles of a group read one weight slab together
         const long long nt = (p.n + pl->tile_n - 1) / pl->tile_n;
         // tiles, and the rows of the weight scales' tensor map, are numbered in 32 bits
         if (((p.m + pl->tile_m - 1) / pl->tile_m + p.groups) > 0x7fffffffLL / nt ||
@@ -425,7 +425,8 @@ rdot_status rdot_plan(const rdot_problem* problem, int device, rdot_plan_t* plan
             }
             pl->grid = 2 * static_cast<int>(std::max<long long>(1, std::min<long long>(bound, clusters)));
         } else {
-            pl->grid = static_cast<int>(std::max<long long>(1, std::min<long long>(bound, pl->sm_count)));
+            // one CTA per SM, unless even quarters of the items are fewer
+            pl->grid = static_cast<int>(std::max<long long>(1, std::min<long long>(4 * bound, pl->sm_count)));
         }
     } else if (p.mode == RDOT_MODE_GRAD_WEIGHT_MXFP8) {
         if (prop.major != 10) {
@@ -1462,12 +1463,12 @@ rdot_status rdot_forward_mxfp4(rdot_plan_t plan, const void* lhs, const uint8_t*
     a.timeout_ns = plan->timeout_ns;
     // code rows of K/2 bytes, boxes of 128 bytes (256 elements) x the kernel's rows or columns
     const uint64_t kb = static_cast<uint64_t>(p.k / 2);
-    CUtensorMap map_a, map_b;
+    CUtensorMap map_a, map_b[3];   // rhs: 128 columns a box; the swapped kernel also 64 and 32
     rdot_status st = encode_2d(&map_a, CU_TENSOR_MAP_DATA_TYPE_UINT8, lhs, kb, p.m, kb, MX4_STAGE_BYTES,
                                plan->skinny ? 16 : 128);
-    if (st == RDOT_OK)
-        st = encode_3d(&map_b, CU_TENSOR_MAP_DATA_TYPE_UINT8, rhs, kb, p.n, p.groups, kb, p.n * kb, MX4_STAGE_BYTES,
-                       plan->skinny ? 32 : 128, 1);
+    for (int i = 0; i < (plan->skinny ? 3 : 1) && st == RDOT_OK; ++i)
+        st = encode_3d(&map_b[i], CU_TENSOR_MAP_DATA_TYPE_UINT8, rhs, kb, p.n, p.groups, kb, p.n * kb, MX4_STAGE_BYTES,
+                       128 >> i, 1);
     if (st != RDOT_OK) return st;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     cudaError_t e;
@@ -1479,7 +1480,7 @@ rdot_status rdot_forward_mxfp4(rdot_plan_t plan, const void* lhs, const uint8_t*
                        static_cast<uint64_t>(a.KA) * (MX4_ATOM_BYTES / 4), static_cast<uint64_t>(p.groups) * a.NB,
                        static_cast<uint64_t>(a.KA) * MX4_ATOM_BYTES, 2 * MX4_ATOM_BYTES / 4, 2, CU_TENSOR_MAP_SWIZZLE_NONE);
         if (st != RDOT_OK) return st;
-        e = launch_mxfp4_pair(map_a, map_b, map_sfb, a, plan->grid, s);
+        e = launch_mxfp4_pair(map_a, map_b[0], map_sfb, a, plan->grid, s);
     }
     return e == cudaSuccess ? RDOT_OK : cuda_fail(e, "mxfp4 launch");
 }

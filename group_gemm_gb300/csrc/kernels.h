@@ -215,7 +215,7 @@ struct Mx4Args {
     const uint8_t* rhs_scale;     // device [G, NB, KA, 512]
     void* out;                    // device bf16 [M, N]
     int M, K, N, G;
-    int NT;                       // column tiles: 256 wide (pairs), 32 wide (the swapped kernel)
+    int NT;                       // 256-column tiles (pairs)
     int NB;                       // 128-column scale atoms across N
     int KA;                       // 128-element scale atoms along K
     int KS;                       // K stages of 256 elements
@@ -233,9 +233,9 @@ cudaError_t launch_mxfp4_pair(const CUtensorMap& tmap_a, const CUtensorMap& tmap
                               const Mx4Args& a, int grid, cudaStream_t stream);
 int mxfp4_pair_max_clusters(int G);
 // MXFP4 forward for a few rows per group (mxfp4_skinny.cu): tmap_x: lhs codes, box (128, 16); tmap_w: rhs
-// codes, box (128, 32, 1); a.NT counts 32-column quarters.
+// codes, boxes (128, 128, 1), (128, 64, 1) and (128, 32, 1).
 constexpr int MX4_SKINNY_ROWS = 64;   // token rows per tile
-cudaError_t launch_mxfp4_skinny(const CUtensorMap& tmap_x, const CUtensorMap& tmap_w, const Mx4Args& a, int grid,
+cudaError_t launch_mxfp4_skinny(const CUtensorMap& tmap_x, const CUtensorMap (&tmap_w)[3], const Mx4Args& a, int grid,
                                 cudaStream_t stream);
 // MXFP4 quantisation (mxfp4_quant.cu) of fp32 or bf16 elements: rows as one array of 32-element blocks, and
 // weights [groups, K, N] to codes [groups, N, K/2] and scale atoms. values (bf16, x's layout) may be null.

@@ -2,17 +2,17 @@
 //
 // out[i, :] = A[i, :] B[g(i)] with A, B in MXFP4 (mxfp4.cuh), fp32 accumulation, bf16 out, computed as
 // out_g^T = B_g A_g^T: 128 weight columns on the MMA's M, up to 64 token rows on its N. What bounds it
-// is streaming the routed experts' codes and scales (17/32 byte per weight) from HBM, so the work is
-// cut by weight bytes: the column quarters (32 columns, 16 KB of codes at K = 1024) of all token tiles
-// are numbered in group order and split evenly over the CTAs, one contiguous range each. A CTA walks
-// its range in tiles of up to four quarters that lie in one 128-column atom; a tile of fewer loads only
-// its quarters' rows, at their natural place in the stage, and the MMA's other rows are not read out.
-// So the last round costs 32-column steps instead of whole 128-column items.
+// is streaming the routed experts' codes and scales (17/32 byte per weight) from HBM; with few experts,
+// how evenly the SMs share them and what a CTA's start and end cost. A work item is a 128-column atom
+// of a group for one token tile. Every CTA takes the same number of whole items; the items that are
+// left over are cut into halves or quarters (64 or 32 columns) where that many parts still fit the
+// CTAs, so the last round costs half or a quarter of an item. A part loads only its columns' rows, at
+// their natural place in the stage, and the MMA's other rows are not read out.
 //
-// Warp 0 streams codes and weight scales (TMA, a ring of STAGES stages of 256 K elements), warp 6
-// gathers the token rows' scale bytes into the atom layout (their row offsets depend on the group
-// sizes, so no fixed layout serves), warp 1 copies scales to tensor memory and issues the MMAs, warps
-// 2..5 read out one 32-column quarter each.
+// Warp 0 streams the codes (one TMA box a stage: with 32-row boxes alone issuing took longer than the
+// bytes), warp 7 the token codes and weight scales, warp 6 gathers the token rows' scale bytes into the
+// atom layout (their row offsets depend on the group sizes, so no fixed layout serves), warp 1 copies
+// scales to tensor memory and issues the MMAs, warps 2..5 read out one 32-column quarter each.
 #include <cuda_bf16.h>
 
 #include "kernels.h"
@@ -25,7 +25,7 @@ namespace rdot {
 
 namespace {
 
-constexpr int THREADS = 224;
+constexpr int THREADS = 256;
 constexpr int TT = MX4_SKINNY_ROWS;             // token rows per tile (64)
 constexpr int STAGES = 8;
 constexpr int Q_BYTES = 32 * MX4_STAGE_BYTES;   // one quarter's codes of a stage: 4 KB
@@ -60,24 +60,43 @@ struct SkinnyTile {
     int g, row0, rows, nb, q0, q1;
 };
 
-// The tile at unit u of a range that ends at `end`; u advances past it. Units: (group, token tile,
-// 32-column quarter), the quarter fastest; a.NT quarters cover N.
-__device__ __forceinline__ SkinnyTile next_tile(int& u, int end, const Mx4Args& a, const int32_t* tprefix,
-                                                const int32_t* off) {
-    const Tile t = decode_tile(u, tprefix, off, a.G, TT, a.NT, false);
+// The CTA's share of `items`: `whole` whole items (blockIdx.x + i gridDim.x), then, if `part` >= 0, quarters
+// [q0, q0 + width) of item `part`.
+struct SkinnyShare {
+    int whole, part, q0, width;
+};
+
+__device__ __forceinline__ SkinnyShare skinny_share(int items) {
+    const int grid = static_cast<int>(gridDim.x), b = static_cast<int>(blockIdx.x);
+    SkinnyShare s;
+    s.whole = items / grid;
+    const int left = items - s.whole * grid;          // < grid
+    s.width = 4 * left <= grid ? 1 : 2 * left <= grid ? 2 : 4;
+    const int parts = 4 / s.width;
+    s.part = b < left * parts ? s.whole * grid + b / parts : -1;
+    s.q0 = s.width * (b % parts);
+    return s;
+}
+
+// Tile i of the share, 0 .. whole (the last one only if part >= 0; it may lie past N: then q1 <= q0).
+__device__ __forceinline__ SkinnyTile skinny_tile(int i, const SkinnyShare& sh, const Mx4Args& a, const int32_t* tprefix,
+                                                  const int32_t* off) {
+    const bool whole = i < sh.whole;
+    const int item = whole ? static_cast<int>(blockIdx.x) + i * static_cast<int>(gridDim.x) : sh.part;
+    const Tile t = decode_tile(item, tprefix, off, a.G, TT, a.NB, true);
     SkinnyTile s;
     s.g = t.g;
     s.row0 = t.row0;
     s.rows = t.rows;
-    s.nb = t.nt >> 2;
-    s.q0 = t.nt & 3;
-    s.q1 = min(min(4, s.q0 + (end - u)), a.NT - 4 * s.nb);
-    u += s.q1 - s.q0;
+    s.nb = t.nt;
+    s.q0 = whole ? 0 : sh.q0;
+    s.q1 = min(s.q0 + (whole ? 4 : sh.width), (a.N - 128 * t.nt + 31) / 32);
     return s;
 }
 
 __global__ void __launch_bounds__(THREADS, 1)
-    mxfp4_skinny_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant__ CUtensorMap tmap_w,
+    mxfp4_skinny_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant__ CUtensorMap tmap_w128,
+                        const __grid_constant__ CUtensorMap tmap_w64, const __grid_constant__ CUtensorMap tmap_w32,
                         Mx4Args a) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -96,7 +115,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     const int lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; ++s) {
-            mbar_init(&full[s], 1);
+            mbar_init(&full[s], 2);   // warps 0 and 7
             mbar_init(&sfull[s], 1);
             mbar_init(&empty[s], 1);
         }
@@ -108,7 +127,9 @@ __global__ void __launch_bounds__(THREADS, 1)
         *abort_flag = 0;
         fence_mbar_init();
         tma_prefetch_desc(&tmap_x);
-        tma_prefetch_desc(&tmap_w);
+        tma_prefetch_desc(&tmap_w128);
+        tma_prefetch_desc(&tmap_w64);
+        tma_prefetch_desc(&tmap_w32);
     }
     if (warp == 1) {
         tmem_alloc(tmem_holder, TMEM_COLS);
@@ -116,7 +137,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
     grid_dependency_enter();   // group sizes and the token codes come from earlier kernels
     if (warp == 2) {
-        const int bad = group_scan_warp(a.group_sizes, a.G, a.M, TT, a.NT, off, tprefix);
+        const int bad = group_scan_warp(a.group_sizes, a.G, a.M, TT, a.NB, off, tprefix);
         if (bad && lane == 0 && blockIdx.x == 0 && a.status) atomicOr(a.status, bad);
     }
     tc_fence_before();
@@ -124,33 +145,63 @@ __global__ void __launch_bounds__(THREADS, 1)
     tc_fence_after();
 
     const uint32_t tmem_base = *tmem_holder;
-    const long long U = tprefix[a.G];
-    const int u0 = static_cast<int>(U * blockIdx.x / gridDim.x);
-    const int u1 = static_cast<int>(U * (blockIdx.x + 1) / gridDim.x);
+    const SkinnyShare sh = skinny_share(tprefix[a.G]);
+    const int tiles = sh.whole + (sh.part >= 0 ? 1 : 0);
     const WaitGuard guard{abort_flag, a.status, a.timeout_ns};
 
     if (warp == 0) {
-        // ------------------------------------------------------------------ TMA producer
+        // ------------------------------------------------------------------ weight codes
+        const bool elected = elect_one();
+        uint32_t stage = 0, phase = 0, issued_mask = 0, issued_phase = 0;
+        bool ok = true;
+        for (int i = 0; i < tiles && ok; ++i) {
+            const SkinnyTile t = skinny_tile(i, sh, a, tprefix, off);
+            const CUtensorMap* map = i < sh.whole || sh.width == 4 ? &tmap_w128 : sh.width == 2 ? &tmap_w64 : &tmap_w32;
+            const int rows = i < sh.whole ? 128 : 32 * sh.width;
+            for (int ks = 0; ks < a.KS && t.q0 < t.q1; ++ks) {
+                ok = mx4_wait_uniform(&empty[stage], phase ^ 1, guard);
+                if (!ok) break;
+                if (elected) {
+                    mbar_arrive_expect_tx(&full[stage], rows * MX4_STAGE_BYTES);
+                    // rows past N and bytes past K arrive as zeros
+                    tma_load_3d(smem + stage * STAGE_BYTES + t.q0 * Q_BYTES, map, &full[stage], ks * MX4_STAGE_BYTES,
+                                t.nb * 128 + 32 * t.q0, t.g);
+                }
+                __syncwarp();
+                issued_mask |= 1u << stage;
+                issued_phase = (issued_phase & ~(1u << stage)) | (phase << stage);
+                if (++stage == STAGES) {
+                    stage = 0;
+                    phase ^= 1;
+                }
+            }
+        }
+        if (!ok && elected) {
+            // stopping early: let every load still in flight land before the CTA exits (a stage whose other
+            // half was never issued runs into the drain's limit, far beyond a load's time)
+            int dummy;
+            const WaitGuard dguard = drain_guard(guard, &dummy);
+            for (int s = 0; s < STAGES; ++s)
+                if (issued_mask & (1u << s)) (void)mbar_wait(&full[s], (issued_phase >> s) & 1u, dguard);
+        }
+        __syncwarp();
+    } else if (warp == 7) {
+        // ------------------------------------------------------------------ token codes, weight scales
         const bool elected = elect_one();
         const uint64_t x_policy = l2_policy_evict_last();   // a token tile is read by every column tile
         uint32_t stage = 0, phase = 0, issued_mask = 0, issued_phase = 0;
         bool ok = true;
-        for (int u = u0; u < u1 && ok;) {
-            const SkinnyTile t = next_tile(u, u1, a, tprefix, off);
+        for (int i = 0; i < tiles && ok; ++i) {
+            const SkinnyTile t = skinny_tile(i, sh, a, tprefix, off);
             const int nx = (t.rows + 15) / 16;
             const uint8_t* sfw = a.rhs_scale + (static_cast<long long>(t.g) * a.NB + t.nb) * a.KA * MX4_ATOM_BYTES;
-            for (int ks = 0; ks < a.KS; ++ks) {
+            for (int ks = 0; ks < a.KS && t.q0 < t.q1; ++ks) {
                 ok = mx4_wait_uniform(&empty[stage], phase ^ 1, guard);
                 if (!ok) break;
                 uint8_t* st = smem + stage * STAGE_BYTES;
                 const int atoms = min(2, a.KA - 2 * ks);
                 if (elected) {
-                    mbar_arrive_expect_tx(&full[stage],
-                                          (t.q1 - t.q0) * Q_BYTES + nx * X_BOX + atoms * MX4_ATOM_BYTES);
-                    // rows past N and bytes past K arrive as zeros
-                    for (int q = t.q0; q < t.q1; ++q)
-                        tma_load_3d(st + q * Q_BYTES, &tmap_w, &full[stage], ks * MX4_STAGE_BYTES,
-                                    t.nb * 128 + 32 * q, t.g);
+                    mbar_arrive_expect_tx(&full[stage], nx * X_BOX + atoms * MX4_ATOM_BYTES);
                     for (int j = 0; j < nx; ++j)
                         tma_load_2d_hint(st + W_BYTES + j * X_BOX, &tmap_x, &full[stage], ks * MX4_STAGE_BYTES,
                                          t.row0 + 16 * j, x_policy);
@@ -166,8 +217,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 }
             }
         }
-        if (!ok && elected) {
-            // stopping early: let every load still in flight land before the CTA exits
+        if (!ok && elected) {   // as warp 0
             int dummy;
             const WaitGuard dguard = drain_guard(guard, &dummy);
             for (int s = 0; s < STAGES; ++s)
@@ -176,25 +226,24 @@ __global__ void __launch_bounds__(THREADS, 1)
         __syncwarp();
     } else if (warp == 6) {
         // ------------------------------------------------------------------ token scale gather
-        // lane l holds rows l and l + 32 of the token tile: 16 bytes of each atom. (tn, kn) is the group
+        // lane l holds rows l and l + 32 of the token tile: 16 bytes of each atom. (in, kn) is the group
         // of stages being loaded, one ahead of the one being stored, across tiles too
         uint32_t stage = 0, phase = 0;
         bool ok = true;
         uint2 c0[MX4_GROUP], c1[MX4_GROUP], n0[MX4_GROUP], n1[MX4_GROUP];
-        int un = u0, kn = 0;
-        bool more = un < u1;
+        int in = 0, kn = 0;
         SkinnyTile tn{};
         const auto load = [&] {
             load_scale_group(a, static_cast<long long>(tn.row0) + lane, lane < tn.rows, kn, n0);
             load_scale_group(a, static_cast<long long>(tn.row0) + lane + 32, lane + 32 < tn.rows, kn, n1);
         };
-        if (more) {
-            tn = next_tile(un, u1, a, tprefix, off);
+        if (in < tiles) {
+            tn = skinny_tile(in, sh, a, tprefix, off);
             load();
         }
-        for (int u = u0; u < u1 && ok;) {
-            (void)next_tile(u, u1, a, tprefix, off);
-            for (int k0 = 0; k0 < a.KS && ok; k0 += MX4_GROUP) {
+        for (int i = 0; i < tiles && ok; ++i) {
+            const bool live = tn.q0 < tn.q1;   // tn is tile i here
+            for (int k0 = 0; k0 < a.KS && ok && live; k0 += MX4_GROUP) {
 #pragma unroll
                 for (int j = 0; j < MX4_GROUP; ++j) {
                     c0[j] = n0[j];
@@ -203,10 +252,9 @@ __global__ void __launch_bounds__(THREADS, 1)
                 kn += MX4_GROUP;
                 if (kn >= a.KS) {
                     kn = 0;
-                    more = un < u1;
-                    if (more) tn = next_tile(un, u1, a, tprefix, off);
+                    if (++in < tiles) tn = skinny_tile(in, sh, a, tprefix, off);
                 }
-                if (more) load();
+                if (in < tiles) load();
 #pragma unroll
                 for (int j = 0; j < MX4_GROUP; ++j) {
                     if (k0 + j >= a.KS) break;
@@ -230,8 +278,9 @@ __global__ void __launch_bounds__(THREADS, 1)
         const bool elected = elect_one();
         uint32_t stage = 0, phase = 0, acc = 0, acc_phase = 0;
         bool ok = true;
-        for (int u = u0; u < u1 && ok;) {
-            const SkinnyTile t = next_tile(u, u1, a, tprefix, off);
+        for (int i = 0; i < tiles; ++i) {
+            const SkinnyTile t = skinny_tile(i, sh, a, tprefix, off);
+            if (t.q0 >= t.q1) break;   // only ever the last tile
             const int n = 16 * ((t.rows + 15) / 16);
             ok = mx4_wait_uniform(&tempty[acc], acc_phase ^ 1, guard);
             if (!ok) break;
@@ -269,6 +318,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                     phase ^= 1;
                 }
             }
+            if (!ok) break;
             acc ^= 1;
             if (acc == 0) acc_phase ^= 1;
         }
@@ -285,8 +335,9 @@ __global__ void __launch_bounds__(THREADS, 1)
         const int q = warp & 3;   // TMEM lane quarter: columns 32 q + lane of the tile's atom
         uint32_t acc = 0, acc_phase = 0;
         __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out);
-        for (int u = u0; u < u1;) {
-            const SkinnyTile t = next_tile(u, u1, a, tprefix, off);
+        for (int i = 0; i < tiles; ++i) {
+            const SkinnyTile t = skinny_tile(i, sh, a, tprefix, off);
+            if (t.q0 >= t.q1) break;
             if (!mx4_wait_warp(&tfull[acc], acc_phase, guard)) break;
             tc_fence_after();
             const int col = t.nb * 128 + q * 32 + lane;
@@ -335,13 +386,13 @@ __global__ void __launch_bounds__(THREADS, 1)
 
 }  // namespace
 
-cudaError_t launch_mxfp4_skinny(const CUtensorMap& tmap_x, const CUtensorMap& tmap_w, const Mx4Args& a, int grid,
+cudaError_t launch_mxfp4_skinny(const CUtensorMap& tmap_x, const CUtensorMap (&tmap_w)[3], const Mx4Args& a, int grid,
                                 cudaStream_t stream) {
     const size_t shm = smem_bytes(a.G);
     cudaError_t e = cudaFuncSetAttribute(mxfp4_skinny_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          static_cast<int>(shm));
     if (e != cudaSuccess) return e;
-    return launch_pdl(mxfp4_skinny_kernel, dim3(grid), dim3(THREADS), shm, stream, tmap_x, tmap_w, a);
+    return launch_pdl(mxfp4_skinny_kernel, dim3(grid), dim3(THREADS), shm, stream, tmap_x, tmap_w[0], tmap_w[1], tmap_w[2], a);
 }
 
 }  // namespace rdot
