@@ -95,6 +95,8 @@ def build(force: bool = False, verbose: bool = False) -> str:
 def load():
     """Loads librdot.so (raises if it has not been built)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -157,14 +159,19 @@ def _check(status: int, what: str):
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _stream(stream, device):
-    import torch
+    """The cudaStream_t of a torch stream, a raw handle, or (None) the device's current stream. The last
+    is asked for as a raw handle: building a torch.cuda.Stream costs more than the library's own call."""
     if stream is None:
+        import torch
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        if raw is not None and device.type == "cuda" and device.index is not None:
+            return raw(device.index)
         stream = torch.cuda.current_stream(device)
-    return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
 # ------------------------------------------------------------------------------ C-ABI names

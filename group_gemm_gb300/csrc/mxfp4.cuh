@@ -16,6 +16,7 @@
 
 #include "kernels.h"
 #include "ptx.cuh"
+#include "sched.cuh"
 
 namespace rdot {
 
@@ -54,6 +55,41 @@ __device__ __forceinline__ void tmem_cp_scales(uint32_t taddr, uint64_t sdesc) {
         tmem_cp_32x128b_warpx4(taddr, sdesc);
     else
         asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(sdesc) : "memory");
+}
+
+// group_scan_warp (sched.cuh) with each size loaded once, for up to 32 groups a lane's: its three passes
+// over the sizes are three L2 round trips at the start of every CTA, 1 us of a one-token call.
+__device__ __forceinline__ int mx4_group_scan(const int32_t* __restrict__ group_sizes, int G, int M, int BM, int NT,
+                                              int32_t* off, int32_t* tile_prefix) {
+    if (G > 32) return group_scan_warp(group_sizes, G, M, BM, NT, off, tile_prefix);
+    const int lane = threadIdx.x & 31;
+    const int s = lane < G ? __ldg(group_sizes + lane) : 0;
+    const int bad = __any_sync(0xffffffffu, s < 0);
+    long long end = max(s, 0);
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const long long v = __shfl_up_sync(0xffffffffu, end, d);
+        if (lane >= d) end += v;
+    }
+    const long long start = min(end - max(s, 0), static_cast<long long>(M));
+    const bool over = __any_sync(0xffffffffu, end > M);
+    end = min(end, static_cast<long long>(M));
+    const int tiles = static_cast<int>((end - start + BM - 1) / BM) * NT;
+    int tend = tiles;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, tend, d);
+        if (lane >= d) tend += v;
+    }
+    if (lane < G) {
+        off[lane] = static_cast<int32_t>(start);
+        tile_prefix[lane] = tend - tiles;
+    }
+    if (lane == G - 1) {
+        off[G] = static_cast<int32_t>(end);
+        tile_prefix[G] = tend;
+    }
+    return bad || over ? RDOT_STATUS_BIT_GROUP_SIZES : 0;
 }
 
 // mbar_wait (ptx.cuh) that looks at the clock only after MX4_TRIES waits: reading the global timer takes

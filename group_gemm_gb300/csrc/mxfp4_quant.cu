@@ -58,6 +58,18 @@ __device__ __forceinline__ float unpack_bf16(uint32_t w, int hi) {
 
 // Rows: the blocks of all rows are consecutive, so the tensor is one array of 32-element blocks. Four
 // lanes hold a block, 8 elements each.
+constexpr int QR_UNROLL = 4;   // vectors of 8 elements in flight per lane
+
+template <bool BF16>
+__device__ __forceinline__ void load_vec8(const uint4* __restrict__ x, long long i, uint4 (&u)[2]) {
+    if (BF16) {
+        u[0] = __ldg(x + i);
+    } else {
+        u[0] = __ldg(x + 2 * i);
+        u[1] = __ldg(x + 2 * i + 1);
+    }
+}
+
 template <bool BF16, bool VALUES>
 __global__ void __launch_bounds__(256) quantize_rows_kernel(const uint4* __restrict__ x, long long vecs,
                                                             uint32_t* __restrict__ codes,
@@ -65,40 +77,40 @@ __global__ void __launch_bounds__(256) quantize_rows_kernel(const uint4* __restr
                                                             uint4* __restrict__ values) {
     grid_dependency_enter();
     const long long step = static_cast<long long>(gridDim.x) * blockDim.x;
-    // vecs is a multiple of 4: the four lanes of a block run together
-    for (long long i = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x; i < vecs; i += step) {
-        float v[8];
-        if (BF16) {
-            const uint4 u = __ldg(x + i);
-            const uint32_t q[4] = {u.x, u.y, u.z, u.w};
+    const uint32_t group = 0xfu << (threadIdx.x & 28);   // the four lanes of a block; vecs is a multiple of 4
+    for (long long i0 = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x; i0 < vecs; i0 += QR_UNROLL * step) {
+        uint4 u[QR_UNROLL][2];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] = unpack_bf16(q[j >> 1], j & 1);
-        } else {
-            const uint4 u0 = __ldg(x + 2 * i), u1 = __ldg(x + 2 * i + 1);
-            const uint32_t q[8] = {u0.x, u0.y, u0.z, u0.w, u1.x, u1.y, u1.z, u1.w};
+        for (int r = 0; r < QR_UNROLL; ++r)
+            if (i0 + r * step < vecs) load_vec8<BF16>(x, i0 + r * step, u[r]);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] = __uint_as_float(q[j]);
-        }
-        uint32_t amax = 0;
+        for (int r = 0; r < QR_UNROLL; ++r) {
+            const long long i = i0 + r * step;
+            if (i >= vecs) break;
+            const uint32_t q[8] = {u[r][0].x, u[r][0].y, u[r][0].z, u[r][0].w, u[r][1].x, u[r][1].y, u[r][1].z, u[r][1].w};
+            float v[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) amax = max(amax, __float_as_uint(v[j]) & 0x7fffffffu);
-        const uint32_t group = 0xfu << (threadIdx.x & 28);
-        amax = max(amax, __shfl_xor_sync(group, amax, 1));
-        amax = max(amax, __shfl_xor_sync(group, amax, 2));
-        const uint32_t s = scale_byte(amax);
-        const bool nan = s == 255u;
-        const float inv = nan ? 0.f : inverse_scale(s);
+            for (int j = 0; j < 8; ++j) v[j] = BF16 ? unpack_bf16(q[j >> 1], j & 1) : __uint_as_float(q[j]);
+            uint32_t amax = 0;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] *= inv;
-        const uint32_t c = nan ? 0u : e2m1x8(v);
-        codes[i] = c;
-        if ((threadIdx.x & 3) == 0) scales[i >> 2] = static_cast<uint8_t>(s);
-        if (VALUES) {
-            const float sv = nan ? __uint_as_float(0x7fffffffu) : scale_value(s);
+            for (int j = 0; j < 8; ++j) amax = max(amax, __float_as_uint(v[j]) & 0x7fffffffu);
+            amax = max(amax, __shfl_xor_sync(group, amax, 1));
+            amax = max(amax, __shfl_xor_sync(group, amax, 2));
+            const uint32_t s = scale_byte(amax);
+            const bool nan = s == 255u;
+            const float inv = nan ? 0.f : inverse_scale(s);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] = e2m1_value(c >> (4 * j)) * sv;
-            values[i] = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
-                                   pack_bf16x2(v[6], v[7]));
+            for (int j = 0; j < 8; ++j) v[j] *= inv;
+            const uint32_t c = nan ? 0u : e2m1x8(v);
+            codes[i] = c;
+            if ((threadIdx.x & 3) == 0) scales[i >> 2] = static_cast<uint8_t>(s);
+            if (VALUES) {
+                const float sv = nan ? __uint_as_float(0x7fffffffu) : scale_value(s);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v[j] = e2m1_value(c >> (4 * j)) * sv;
+                values[i] = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                                       pack_bf16x2(v[6], v[7]));
+            }
         }
     }
 }
@@ -112,7 +124,7 @@ constexpr int QW_BLOCKS = 8;    // scale blocks (32 rows each) per thread block
 constexpr int QW_PITCH = 144;   // shared bytes of a column's codes (128) plus 16 against bank conflicts
 
 template <bool BF16, bool VALUES>
-__global__ void __launch_bounds__(256) quantize_weight_kernel(const void* __restrict__ w, int K, int N, int NT, int KC,
+__global__ void __launch_bounds__(256, 2) quantize_weight_kernel(const void* __restrict__ w, int K, int N, int NT, int KC,
                                                               uint8_t* __restrict__ codes,
                                                               uint8_t* __restrict__ scales,
                                                               uint32_t* __restrict__ values) {
@@ -212,7 +224,7 @@ cudaError_t launch_quantize_rows(const void* x, bool bf16, long long elements, u
                                  void* values, int sm_count, cudaStream_t stream) {
     const long long vecs = elements / 8;
     const long long want = (vecs + 255) / 256;
-    const int grid = static_cast<int>(want < 16LL * sm_count ? want : 16LL * sm_count);
+    const int grid = static_cast<int>(want < 8LL * sm_count ? want : 8LL * sm_count);
     auto kern = bf16 ? (values ? quantize_rows_kernel<true, true> : quantize_rows_kernel<true, false>)
                      : (values ? quantize_rows_kernel<false, true> : quantize_rows_kernel<false, false>);
     return launch_pdl(kern, dim3(grid), dim3(256), 0, stream, static_cast<const uint4*>(x), vecs,

@@ -26,24 +26,30 @@ namespace rdot {
 namespace {
 
 constexpr int THREADS = 256;
-constexpr int TT = MX4_SKINNY_ROWS;             // token rows per tile (64)
-constexpr int STAGES = 8;
 constexpr int Q_BYTES = 32 * MX4_STAGE_BYTES;   // one quarter's codes of a stage: 4 KB
 constexpr int W_BYTES = 4 * Q_BYTES;
 constexpr int X_BOX = 16 * MX4_STAGE_BYTES;     // 16 token rows: 2 KB
-constexpr int X_BYTES = TT * MX4_STAGE_BYTES;
 constexpr int SF_BYTES = 2 * MX4_ATOM_BYTES;    // a stage's two scale atoms
-constexpr int STAGE_BYTES = W_BYTES + X_BYTES + 2 * SF_BYTES;
-constexpr int RING_BYTES = STAGES * STAGE_BYTES;
-constexpr int BAR_BYTES = (3 * STAGES + 5) * 8;   // full, sfull, empty; tfull[2], tempty[2], drain
 constexpr int MISC_BYTES = 16;
-constexpr int TMEM_SF_BASE = 2 * TT;              // after the two accumulators
-constexpr int SF_COLS = 16;                       // per stage: two weight atoms, two token atoms
+constexpr int SF_COLS = 16;                     // per stage: two weight atoms, two token atoms
 constexpr int TMEM_COLS = 256;
-static_assert(STAGE_BYTES % 1024 == 0, "swizzle atoms stay 1 KB aligned");
-static_assert(TMEM_SF_BASE + STAGES * SF_COLS <= TMEM_COLS, "tensor memory budget");
 
-size_t smem_bytes(int G) { return 1024 + RING_BYTES + BAR_BYTES + MISC_BYTES + sizeof(int32_t) * 2 * (G + 1); }
+// TT token rows per tile: 64, or 16 where no tile can have more (at most 16 rows in all), which leaves
+// room for two more stages: one token streams its weights in 16.5 us with 8, X with 10.
+template <int TT>
+struct Ring {
+    static constexpr int STAGES = TT == 16 ? 10 : 8;
+    static constexpr int X_BYTES = TT * MX4_STAGE_BYTES;
+    static constexpr int STAGE_BYTES = W_BYTES + X_BYTES + 2 * SF_BYTES;
+    static constexpr int RING_BYTES = STAGES * STAGE_BYTES;
+    static constexpr int BAR_BYTES = (3 * STAGES + 6) / 2 * 16;   // full, sfull, empty; tfull[2], tempty[2], drain
+    static constexpr int TMEM_SF_BASE = 2 * TT;                   // after the two accumulators
+    static_assert(STAGE_BYTES % 1024 == 0, "swizzle atoms stay 1 KB aligned");
+    static_assert(TMEM_SF_BASE + STAGES * SF_COLS <= TMEM_COLS, "tensor memory budget");
+    static size_t smem_bytes(int G) {
+        return 1024 + RING_BYTES + BAR_BYTES + MISC_BYTES + sizeof(int32_t) * 2 * (G + 1);
+    }
+};
 
 __device__ __forceinline__ void tmem_ld_32x16(uint32_t taddr, uint32_t (&r)[16]) {
     asm volatile(
@@ -79,6 +85,7 @@ __device__ __forceinline__ SkinnyShare skinny_share(int items) {
 }
 
 // Tile i of the share, 0 .. whole (the last one only if part >= 0; it may lie past N: then q1 <= q0).
+template <int TT>
 __device__ __forceinline__ SkinnyTile skinny_tile(int i, const SkinnyShare& sh, const Mx4Args& a, const int32_t* tprefix,
                                                   const int32_t* off) {
     const bool whole = i < sh.whole;
@@ -94,10 +101,14 @@ __device__ __forceinline__ SkinnyTile skinny_tile(int i, const SkinnyShare& sh, 
     return s;
 }
 
+template <int TT>
 __global__ void __launch_bounds__(THREADS, 1)
     mxfp4_skinny_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant__ CUtensorMap tmap_w128,
                         const __grid_constant__ CUtensorMap tmap_w64, const __grid_constant__ CUtensorMap tmap_w32,
                         Mx4Args a) {
+    using R = Ring<TT>;
+    constexpr int STAGES = R::STAGES, STAGE_BYTES = R::STAGE_BYTES, X_BYTES = R::X_BYTES, RING_BYTES = R::RING_BYTES;
+    constexpr int BAR_BYTES = R::BAR_BYTES, TMEM_SF_BASE = R::TMEM_SF_BASE;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + RING_BYTES);
@@ -137,7 +148,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
     grid_dependency_enter();   // group sizes and the token codes come from earlier kernels
     if (warp == 2) {
-        const int bad = group_scan_warp(a.group_sizes, a.G, a.M, TT, a.NB, off, tprefix);
+        const int bad = mx4_group_scan(a.group_sizes, a.G, a.M, TT, a.NB, off, tprefix);
         if (bad && lane == 0 && blockIdx.x == 0 && a.status) atomicOr(a.status, bad);
     }
     tc_fence_before();
@@ -155,7 +166,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         uint32_t stage = 0, phase = 0, issued_mask = 0, issued_phase = 0;
         bool ok = true;
         for (int i = 0; i < tiles && ok; ++i) {
-            const SkinnyTile t = skinny_tile(i, sh, a, tprefix, off);
+            const SkinnyTile t = skinny_tile<TT>(i, sh, a, tprefix, off);
             const CUtensorMap* map = i < sh.whole || sh.width == 4 ? &tmap_w128 : sh.width == 2 ? &tmap_w64 : &tmap_w32;
             const int rows = i < sh.whole ? 128 : 32 * sh.width;
             for (int ks = 0; ks < a.KS && t.q0 < t.q1; ++ks) {
@@ -192,7 +203,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         uint32_t stage = 0, phase = 0, issued_mask = 0, issued_phase = 0;
         bool ok = true;
         for (int i = 0; i < tiles && ok; ++i) {
-            const SkinnyTile t = skinny_tile(i, sh, a, tprefix, off);
+            const SkinnyTile t = skinny_tile<TT>(i, sh, a, tprefix, off);
             const int nx = (t.rows + 15) / 16;
             const uint8_t* sfw = a.rhs_scale + (static_cast<long long>(t.g) * a.NB + t.nb) * a.KA * MX4_ATOM_BYTES;
             for (int ks = 0; ks < a.KS && t.q0 < t.q1; ++ks) {
@@ -238,7 +249,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             load_scale_group(a, static_cast<long long>(tn.row0) + lane + 32, lane + 32 < tn.rows, kn, n1);
         };
         if (in < tiles) {
-            tn = skinny_tile(in, sh, a, tprefix, off);
+            tn = skinny_tile<TT>(in, sh, a, tprefix, off);
             load();
         }
         for (int i = 0; i < tiles && ok; ++i) {
@@ -252,7 +263,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 kn += MX4_GROUP;
                 if (kn >= a.KS) {
                     kn = 0;
-                    if (++in < tiles) tn = skinny_tile(in, sh, a, tprefix, off);
+                    if (++in < tiles) tn = skinny_tile<TT>(in, sh, a, tprefix, off);
                 }
                 if (in < tiles) load();
 #pragma unroll
@@ -279,7 +290,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         uint32_t stage = 0, phase = 0, acc = 0, acc_phase = 0;
         bool ok = true;
         for (int i = 0; i < tiles; ++i) {
-            const SkinnyTile t = skinny_tile(i, sh, a, tprefix, off);
+            const SkinnyTile t = skinny_tile<TT>(i, sh, a, tprefix, off);
             if (t.q0 >= t.q1) break;   // only ever the last tile
             const int n = 16 * ((t.rows + 15) / 16);
             ok = mx4_wait_uniform(&tempty[acc], acc_phase ^ 1, guard);
@@ -336,7 +347,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         uint32_t acc = 0, acc_phase = 0;
         __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out);
         for (int i = 0; i < tiles; ++i) {
-            const SkinnyTile t = skinny_tile(i, sh, a, tprefix, off);
+            const SkinnyTile t = skinny_tile<TT>(i, sh, a, tprefix, off);
             if (t.q0 >= t.q1) break;
             if (!mx4_wait_warp(&tfull[acc], acc_phase, guard)) break;
             tc_fence_after();
@@ -386,13 +397,14 @@ __global__ void __launch_bounds__(THREADS, 1)
 
 }  // namespace
 
-cudaError_t launch_mxfp4_skinny(const CUtensorMap& tmap_x, const CUtensorMap (&tmap_w)[3], const Mx4Args& a, int grid,
-                                cudaStream_t stream) {
-    const size_t shm = smem_bytes(a.G);
-    cudaError_t e = cudaFuncSetAttribute(mxfp4_skinny_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         static_cast<int>(shm));
+cudaError_t launch_mxfp4_skinny(const CUtensorMap& tmap_x, const CUtensorMap (&tmap_w)[3], const Mx4Args& a, int tt,
+                                int grid, cudaStream_t stream) {
+    if (tt != 16 && tt != 64) return cudaErrorInvalidValue;
+    const size_t shm = tt == 16 ? Ring<16>::smem_bytes(a.G) : Ring<64>::smem_bytes(a.G);
+    auto kern = tt == 16 ? mxfp4_skinny_kernel<16> : mxfp4_skinny_kernel<64>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(shm));
     if (e != cudaSuccess) return e;
-    return launch_pdl(mxfp4_skinny_kernel, dim3(grid), dim3(THREADS), shm, stream, tmap_x, tmap_w[0], tmap_w[1], tmap_w[2], a);
+    return launch_pdl(kern, dim3(grid), dim3(THREADS), shm, stream, tmap_x, tmap_w[0], tmap_w[1], tmap_w[2], a);
 }
 
 }  // namespace rdot

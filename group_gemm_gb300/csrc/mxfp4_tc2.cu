@@ -151,7 +151,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     }
     grid_dependency_enter();   // group sizes and operands may come from the previous kernel
     if (warp == 2) {
-        const int bad = group_scan_warp(a.group_sizes, a.G, a.M, BM, a.NT, off, tprefix);
+        const int bad = mx4_group_scan(a.group_sizes, a.G, a.M, BM, a.NT, off, tprefix);
         if (bad && lane == 0 && blockIdx.x == 0 && a.status) atomicOr(a.status, bad);
     }
     tc_fence_before();
