@@ -167,8 +167,9 @@ __device__ __forceinline__ void store_elem(void* p, long long i, float v) {
 //   values        dl[e_j] = g_j
 //   softmax       dl[e]   = [e = e_j] w_j g_j - p_e s,  p = softmax over all E logits (recomputed)
 //   softmax_topk  dl[e_j] = w_j (g_j - s)
-// and zero for the other experts. Lane j holds copy j's expert and its term.
-template <bool BF16>
+// and zero for the other experts. Lane j holds copy j's expert and its term; lane l the logits of
+// experts l, l + 32, ..., IPL of them, read once.
+template <int IPL, bool BF16>
 __global__ void __launch_bounds__(256) router_topk_grad_kernel(const void* __restrict__ logits,
                                                                const int32_t* __restrict__ ids,
                                                                const float* __restrict__ w,
@@ -179,35 +180,55 @@ __global__ void __launch_bounds__(256) router_topk_grad_kernel(const void* __res
     const long long warp = (static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
     const long long nwarps = (static_cast<long long>(gridDim.x) * blockDim.x) >> 5;
     for (long long t = warp; t < tokens; t += nwarps) {
+        float v[IPL];
+        if (mode == RDOT_ROUTER_SOFTMAX) {
+#pragma unroll
+            for (int i = 0; i < IPL; ++i)
+                v[i] = lane + 32 * i < E ? load_elem<BF16>(logits, t * E + lane + 32 * i) : -INFINITY;
+        }
         const int id = lane < k ? __ldg(ids + t * k + lane) : -1;
         const float wj = lane < k ? __ldg(w + t * k + lane) : 0.f;
         const float gj = lane < k ? __ldg(dw + t * k + lane) : 0.f;
         const float s = mode == RDOT_ROUTER_VALUES ? 0.f : warp_sum(wj * gj);
         const float term = mode == RDOT_ROUTER_VALUES ? gj : mode == RDOT_ROUTER_SOFTMAX ? wj * gj : wj * (gj - s);
-        float m = 0.f, inv_sum = 0.f;
         if (mode == RDOT_ROUTER_SOFTMAX) {
-            m = -INFINITY;
-            for (int e = lane; e < E; e += 32) m = fmaxf(m, load_elem<BF16>(logits, t * E + e));
-            __syncwarp();
+            float m = v[0];
+#pragma unroll
+            for (int i = 1; i < IPL; ++i) m = fmaxf(m, v[i]);
 #pragma unroll
             for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
             float sum = 0.f;
-            for (int e = lane; e < E; e += 32) sum += expf(load_elem<BF16>(logits, t * E + e) - m);
-            __syncwarp();
-            inv_sum = 1.f / warp_sum(sum);
-        }
-        for (int e0 = 0; e0 < E; e0 += 32) {
-            const int e = e0 + lane;
-            float v = 0.f;
-            if (mode == RDOT_ROUTER_SOFTMAX && e < E) v = -(expf(load_elem<BF16>(logits, t * E + e) - m) * inv_sum) * s;
-            for (int j = 0; j < k; ++j) {
-                const int ej = __shfl_sync(0xffffffffu, id, j);
-                const float tj = __shfl_sync(0xffffffffu, term, j);
-                if (ej == e) v += tj;
+#pragma unroll
+            for (int i = 0; i < IPL; ++i) {
+                v[i] = lane + 32 * i < E ? expf(v[i] - m) : 0.f;
+                sum += v[i];
             }
-            if (e < E) store_elem<BF16>(dlogits, t * E + e, v);
+            const float scale = -s / warp_sum(sum);
+#pragma unroll
+            for (int i = 0; i < IPL; ++i) v[i] *= scale;
+        } else {
+#pragma unroll
+            for (int i = 0; i < IPL; ++i) v[i] = 0.f;
         }
+        for (int j = 0; j < k; ++j) {
+            const int ej = __shfl_sync(0xffffffffu, id, j);
+            const float tj = __shfl_sync(0xffffffffu, term, j);
+#pragma unroll
+            for (int i = 0; i < IPL; ++i)
+                if (ej == lane + 32 * i) v[i] += tj;
+        }
+#pragma unroll
+        for (int i = 0; i < IPL; ++i)
+            if (lane + 32 * i < E) store_elem<BF16>(dlogits, t * E + lane + 32 * i, v[i]);
     }
+}
+
+template <int IPL>
+cudaError_t launch_topk_grad_ipl(const void* logits, bool bf16, const int32_t* ids, const float* weights,
+                                 const float* dweights, long long tokens, int E, int k, int mode, void* dlogits, int grid,
+                                 cudaStream_t stream) {
+    auto kern = bf16 ? router_topk_grad_kernel<IPL, true> : router_topk_grad_kernel<IPL, false>;
+    return launch_pdl(kern, dim3(grid), dim3(256), 0, stream, logits, ids, weights, dweights, tokens, E, k, mode, dlogits);
 }
 
 int warps_grid(long long warps, int sm_count) {
@@ -239,9 +260,14 @@ cudaError_t launch_moe_permute_grad(const void* dx_sorted, bool bf16, const int3
 cudaError_t launch_router_topk_grad(const void* logits, bool bf16, const int32_t* ids, const float* weights,
                                     const float* dweights, long long tokens, int E, int k, int mode, void* dlogits,
                                     int sm_count, cudaStream_t stream) {
-    auto kern = bf16 ? router_topk_grad_kernel<true> : router_topk_grad_kernel<false>;
-    return launch_pdl(kern, dim3(warps_grid(tokens, sm_count)), dim3(256), 0, stream, logits, ids, weights, dweights,
-                      tokens, E, k, mode, dlogits);
+    const int grid = warps_grid(tokens, sm_count);
+    const auto launch = E <= 32    ? launch_topk_grad_ipl<1>
+                        : E <= 64  ? launch_topk_grad_ipl<2>
+                        : E <= 128 ? launch_topk_grad_ipl<4>
+                        : E <= 256 ? launch_topk_grad_ipl<8>
+                        : E <= 512 ? launch_topk_grad_ipl<16>
+                                   : launch_topk_grad_ipl<32>;
+    return launch(logits, bf16, ids, weights, dweights, tokens, E, k, mode, dlogits, grid, stream);
 }
 
 }  // namespace rdot
