@@ -7,8 +7,8 @@
 // A K stage is 128 code bytes (256 elements) of a row, one 128-byte swizzle row: four MMAs of K = 64
 // (tcgen05.mma kind::mxf4, scale_vec::2X: two scales per row and MMA). The scales of 128 rows x 4
 // consecutive scale blocks (128 elements) form a 512-byte atom, byte 16 (r % 32) + 4 (r / 32) + kblock;
-// tcgen05.cp .32x128b.warpx4 copies it into 4 tensor-memory columns, replicated over the four lane
-// quarters, and the MMA reads the scales of rows 32q .. 32q+31 from column q. One atom serves two
+// it occupies 4 tensor-memory columns, replicated over the four lane quarters (lane l of each holds
+// bytes 16 l .. 16 l + 15), and the MMA reads the scales of rows 32q .. 32q+31 from column q. One atom serves two
 // MMAs: scale-factor id 0 picks the word's bytes 0-1, id 2 its bytes 2-3.
 #pragma once
 
@@ -47,14 +47,6 @@ __device__ __forceinline__ void mma_mxf4(uint32_t d_tmem, uint64_t a_desc, uint6
                 d_tmem),
             "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sfa_tmem), "r"(sfb_tmem), "r"(accumulate)
             : "memory");
-}
-
-template <int CTAS>
-__device__ __forceinline__ void tmem_cp_scales(uint32_t taddr, uint64_t sdesc) {
-    if constexpr (CTAS == 1)
-        tmem_cp_32x128b_warpx4(taddr, sdesc);
-    else
-        asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(sdesc) : "memory");
 }
 
 // group_scan_warp (sched.cuh) with each size loaded once, for up to 32 groups a lane's: its three passes

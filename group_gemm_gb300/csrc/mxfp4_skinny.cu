@@ -10,9 +10,11 @@
 // their natural place in the stage, and the MMA's other rows are not read out.
 //
 // Warp 0 streams the codes (one TMA box a stage: with 32-row boxes alone issuing took longer than the
-// bytes), warp 7 the token codes and weight scales, warp 6 gathers the token rows' scale bytes into the
-// atom layout (their row offsets depend on the group sizes, so no fixed layout serves), warp 1 copies
-// scales to tensor memory and issues the MMAs, warps 2..5 read out one 32-column quarter each.
+// bytes), warp 7 the token codes and weight scales, warp 6 gathers the token rows' scale bytes into
+// atoms a group of stages ahead. Warps 8..11 wait for all of a stage's data, write its scales to their
+// tensor-memory lane quarter and tell warp 1, which issues the MMAs and waits for nothing else: copies
+// by tcgen05.cp would run in order with the MMAs, as long as them. Warps 2..5 read out one 32-column
+// quarter each.
 #include <cuda_bf16.h>
 
 #include "kernels.h"
@@ -25,29 +27,32 @@ namespace rdot {
 
 namespace {
 
-constexpr int THREADS = 256;
+constexpr int THREADS = 384;
+constexpr int SCALE_WARP = 8;   // the first of four
 constexpr int Q_BYTES = 32 * MX4_STAGE_BYTES;   // one quarter's codes of a stage: 4 KB
 constexpr int W_BYTES = 4 * Q_BYTES;
 constexpr int X_BOX = 16 * MX4_STAGE_BYTES;     // 16 token rows: 2 KB
 constexpr int SF_BYTES = 2 * MX4_ATOM_BYTES;    // a stage's two scale atoms
+constexpr int SFX_BYTES = 2 * MX4_GROUP_BYTES;  // the token rows' scale atoms, two groups of stages
 constexpr int MISC_BYTES = 16;
 constexpr int SF_COLS = 16;                     // per stage: two weight atoms, two token atoms
 constexpr int TMEM_COLS = 256;
 
 // TT token rows per tile: 64, or 16 where no tile can have more (at most 16 rows in all), which leaves
-// room for two more stages: one token streams its weights in 16.5 us with 8, X with 10.
+// room for two more stages: 
 template <int TT>
 struct Ring {
     static constexpr int STAGES = TT == 16 ? 10 : 8;
     static constexpr int X_BYTES = TT * MX4_STAGE_BYTES;
-    static constexpr int STAGE_BYTES = W_BYTES + X_BYTES + 2 * SF_BYTES;
+    static constexpr int STAGE_BYTES = W_BYTES + X_BYTES + SF_BYTES;
     static constexpr int RING_BYTES = STAGES * STAGE_BYTES;
-    static constexpr int BAR_BYTES = (3 * STAGES + 6) / 2 * 16;   // full, sfull, empty; tfull[2], tempty[2], drain
+    // full, xfull, sfull, empty; afull[2], aempty[2], tfull[2], tempty[2], drain
+    static constexpr int BAR_BYTES = (4 * STAGES + 10) / 2 * 16;
     static constexpr int TMEM_SF_BASE = 2 * TT;                   // after the two accumulators
     static_assert(STAGE_BYTES % 1024 == 0, "swizzle atoms stay 1 KB aligned");
     static_assert(TMEM_SF_BASE + STAGES * SF_COLS <= TMEM_COLS, "tensor memory budget");
     static size_t smem_bytes(int G) {
-        return 1024 + RING_BYTES + BAR_BYTES + MISC_BYTES + sizeof(int32_t) * 2 * (G + 1);
+        return 1024 + RING_BYTES + SFX_BYTES + BAR_BYTES + MISC_BYTES + sizeof(int32_t) * 2 * (G + 1);
     }
 };
 
@@ -111,26 +116,34 @@ __global__ void __launch_bounds__(THREADS, 1)
     constexpr int BAR_BYTES = R::BAR_BYTES, TMEM_SF_BASE = R::TMEM_SF_BASE;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    uint64_t* full = reinterpret_cast<uint64_t*>(smem + RING_BYTES);
-    uint64_t* sfull = full + STAGES;
+    uint8_t* sfx_buf = smem + RING_BYTES;
+    uint8_t* bars = sfx_buf + SFX_BYTES;
+    uint64_t* full = reinterpret_cast<uint64_t*>(bars);   // a stage's weight codes have landed
+    uint64_t* xfull = full + STAGES;                      // its token codes and weight scales
+    uint64_t* sfull = xfull + STAGES;                     // all of these, and its scales are in tensor memory
     uint64_t* empty = sfull + STAGES;
-    uint64_t* tfull = empty + STAGES;
+    uint64_t* afull = empty + STAGES;                     // the token rows' scales of a group of stages
+    uint64_t* aempty = afull + 2;
+    uint64_t* tfull = aempty + 2;
     uint64_t* tempty = tfull + 2;
     uint64_t* drain = tempty + 2;
     uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(drain + 1);
     int* abort_flag = reinterpret_cast<int*>(tmem_holder + 1);
-    int32_t* off = reinterpret_cast<int32_t*>(smem + RING_BYTES + BAR_BYTES + MISC_BYTES);
+    int32_t* off = reinterpret_cast<int32_t*>(bars + BAR_BYTES + MISC_BYTES);
     int32_t* tprefix = off + a.G + 1;
 
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; ++s) {
-            mbar_init(&full[s], 2);   // warps 0 and 7
-            mbar_init(&sfull[s], 1);
+            mbar_init(&full[s], 1);
+            mbar_init(&xfull[s], 1);
+            mbar_init(&sfull[s], 4);   // the scale warps
             mbar_init(&empty[s], 1);
         }
         for (int i = 0; i < 2; ++i) {
+            mbar_init(&afull[i], 1);
+            mbar_init(&aempty[i], 4);
             mbar_init(&tfull[i], 1);
             mbar_init(&tempty[i], 128);
         }
@@ -188,8 +201,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             }
         }
         if (!ok && elected) {
-            // stopping early: let every load still in flight land before the CTA exits (a stage whose other
-            // half was never issued runs into the drain's limit, far beyond a load's time)
+            // stopping early: let every load still in flight land before the CTA exits
             int dummy;
             const WaitGuard dguard = drain_guard(guard, &dummy);
             for (int s = 0; s < STAGES; ++s)
@@ -212,12 +224,12 @@ __global__ void __launch_bounds__(THREADS, 1)
                 uint8_t* st = smem + stage * STAGE_BYTES;
                 const int atoms = min(2, a.KA - 2 * ks);
                 if (elected) {
-                    mbar_arrive_expect_tx(&full[stage], nx * X_BOX + atoms * MX4_ATOM_BYTES);
+                    mbar_arrive_expect_tx(&xfull[stage], nx * X_BOX + atoms * MX4_ATOM_BYTES);
                     for (int j = 0; j < nx; ++j)
-                        tma_load_2d_hint(st + W_BYTES + j * X_BOX, &tmap_x, &full[stage], ks * MX4_STAGE_BYTES,
+                        tma_load_2d_hint(st + W_BYTES + j * X_BOX, &tmap_x, &xfull[stage], ks * MX4_STAGE_BYTES,
                                          t.row0 + 16 * j, x_policy);
                     bulk_load(st + W_BYTES + X_BYTES, sfw + static_cast<long long>(ks) * SF_BYTES,
-                              atoms * MX4_ATOM_BYTES, &full[stage]);
+                              atoms * MX4_ATOM_BYTES, &xfull[stage]);
                 }
                 __syncwarp();
                 issued_mask |= 1u << stage;
@@ -232,55 +244,76 @@ __global__ void __launch_bounds__(THREADS, 1)
             int dummy;
             const WaitGuard dguard = drain_guard(guard, &dummy);
             for (int s = 0; s < STAGES; ++s)
-                if (issued_mask & (1u << s)) (void)mbar_wait(&full[s], (issued_phase >> s) & 1u, dguard);
+                if (issued_mask & (1u << s)) (void)mbar_wait(&xfull[s], (issued_phase >> s) & 1u, dguard);
         }
         __syncwarp();
     } else if (warp == 6) {
         // ------------------------------------------------------------------ token scale gather
-        // lane l holds rows l and l + 32 of the token tile: 16 bytes of each atom. (in, kn) is the group
-        // of stages being loaded, one ahead of the one being stored, across tiles too
-        uint32_t stage = 0, phase = 0;
-        bool ok = true;
-        uint2 c0[MX4_GROUP], c1[MX4_GROUP], n0[MX4_GROUP], n1[MX4_GROUP];
+        // lane l loads rows l and l + 32 of the token tile. (in, kn) is the group of stages being loaded, one
+        // ahead of the one being stored, across tiles too
+        uint32_t buf = 0, phase = 0;
+        uint2 n0[MX4_GROUP], n1[MX4_GROUP];
         int in = 0, kn = 0;
         SkinnyTile tn{};
         const auto load = [&] {
             load_scale_group(a, static_cast<long long>(tn.row0) + lane, lane < tn.rows, kn, n0);
-            load_scale_group(a, static_cast<long long>(tn.row0) + lane + 32, lane + 32 < tn.rows, kn, n1);
+            if (TT > 32) load_scale_group(a, static_cast<long long>(tn.row0) + lane + 32, lane + 32 < tn.rows, kn, n1);
         };
-        if (in < tiles) {
-            tn = skinny_tile<TT>(in, sh, a, tprefix, off);
+        if (tiles > 0) {
+            tn = skinny_tile<TT>(0, sh, a, tprefix, off);
             load();
         }
+        while (in < tiles && tn.q0 < tn.q1) {
+            if (!mx4_wait_uniform(&aempty[buf], phase ^ 1, guard)) break;
+            put_scale_group(sfx_buf + buf * MX4_GROUP_BYTES, lane, n0);
+            if (TT > 32) put_scale_group(sfx_buf + buf * MX4_GROUP_BYTES, lane + 32, n1);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&afull[buf]);
+            buf ^= 1;
+            phase ^= buf == 0 ? 1 : 0;
+            kn += MX4_GROUP;
+            if (kn >= a.KS) {
+                kn = 0;
+                if (++in < tiles) tn = skinny_tile<TT>(in, sh, a, tprefix, off);
+            }
+            if (in < tiles) load();
+        }
+    } else if (warp >= SCALE_WARP) {
+        // ------------------------------------------------------------------ scales
+        const uint32_t quarter = static_cast<uint32_t>((warp & 3) * 32) << 16;   // this warp's tensor-memory lanes
+        uint32_t stage = 0, phase = 0, buf = 0, aphase = 0;
+        bool ok = true;
         for (int i = 0; i < tiles && ok; ++i) {
-            const bool live = tn.q0 < tn.q1;   // tn is tile i here
-            for (int k0 = 0; k0 < a.KS && ok && live; k0 += MX4_GROUP) {
-#pragma unroll
-                for (int j = 0; j < MX4_GROUP; ++j) {
-                    c0[j] = n0[j];
-                    c1[j] = n1[j];
+            const SkinnyTile t = skinny_tile<TT>(i, sh, a, tprefix, off);
+            for (int ks = 0; ks < a.KS && t.q0 < t.q1; ++ks) {
+                const int j = ks % MX4_GROUP;
+                if (j == 0) ok = mx4_wait_uniform(&afull[buf], aphase, guard);
+                // this stage's loads were issued after the MMAs that read its scale columns had completed
+                ok = ok && mx4_wait_uniform(&xfull[stage], phase, guard);
+                if (!ok) break;
+                tc_fence_after();
+                const uint4* sx = reinterpret_cast<const uint4*>(sfx_buf + buf * MX4_GROUP_BYTES) + 64 * j + lane;
+                const uint4* sw = reinterpret_cast<const uint4*>(smem + stage * STAGE_BYTES + W_BYTES + X_BYTES) + lane;
+                const uint4 x0 = sx[0], x1 = sx[32], w0 = sw[0], w1 = sw[32];
+                const uint32_t t0 = tmem_base + TMEM_SF_BASE + SF_COLS * stage + quarter;
+                tmem_st_32x8(t0, w0, x0);
+                tmem_st_32x8(t0 + 8, w1, x1);
+                const bool last = j == MX4_GROUP - 1 || ks + 1 == a.KS;   // of this buffer of token scales
+                __syncwarp();
+                if (lane == 0 && last) mbar_arrive(&aempty[buf]);   // every lane's values are in registers
+                ok = mx4_wait_uniform(&full[stage], phase, guard);
+                if (!ok) break;
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sfull[stage]);
+                if (last) {
+                    buf ^= 1;
+                    aphase ^= buf == 0 ? 1 : 0;
                 }
-                kn += MX4_GROUP;
-                if (kn >= a.KS) {
-                    kn = 0;
-                    if (++in < tiles) tn = skinny_tile<TT>(in, sh, a, tprefix, off);
-                }
-                if (in < tiles) load();
-#pragma unroll
-                for (int j = 0; j < MX4_GROUP; ++j) {
-                    if (k0 + j >= a.KS) break;
-                    ok = mx4_wait_uniform(&empty[stage], phase ^ 1, guard);
-                    if (!ok) break;
-                    uint8_t* sf = smem + stage * STAGE_BYTES + W_BYTES + X_BYTES + SF_BYTES;
-                    reinterpret_cast<uint4*>(sf)[lane] = make_uint4(c0[j].x, c1[j].x, 0u, 0u);
-                    reinterpret_cast<uint4*>(sf + MX4_ATOM_BYTES)[lane] = make_uint4(c0[j].y, c1[j].y, 0u, 0u);
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&sfull[stage]);
-                    if (++stage == STAGES) {
-                        stage = 0;
-                        phase ^= 1;
-                    }
+                if (++stage == STAGES) {
+                    stage = 0;
+                    phase ^= 1;
                 }
             }
         }
@@ -299,25 +332,20 @@ __global__ void __launch_bounds__(THREADS, 1)
             const uint32_t d_tmem = tmem_base + acc * TT;
             const uint32_t idesc0 = idesc_mxf4(128, n, 0), idesc1 = idesc_mxf4(128, n, 2);
             for (int ks = 0; ks < a.KS; ++ks) {
-                ok = mx4_wait_uniform(&full[stage], phase, guard) && mx4_wait_uniform(&sfull[stage], phase, guard);
+                ok = mx4_wait_uniform(&sfull[stage], phase, guard);
                 if (!ok) break;
                 tc_fence_after();
                 const uint32_t sw = smem_u32(smem + stage * STAGE_BYTES);
                 const uint64_t wdesc = smem_desc_sw128(sw, 16, 1024), xdesc = smem_desc_sw128(sw + W_BYTES, 16, 1024);
-                const uint64_t sfdesc = smem_desc_rows16(sw + W_BYTES + X_BYTES);
                 const uint32_t sf_t = tmem_base + TMEM_SF_BASE + SF_COLS * stage;
                 const int steps = min(4, (a.K - ks * MX4_STAGE_K + 63) / 64);   // MMAs of K = 64 with data
                 if (elected) {
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk) {
                         if (kk >= steps) break;
-                        // descriptor addresses count 16 bytes: an atom is 32, 64 elements of a row 2
-                        const uint32_t w_t = sf_t + 8 * (kk >> 1), x_t = w_t + 4;
-                        if ((kk & 1) == 0) {
-                            tmem_cp_scales<1>(w_t, sfdesc + (kk >> 1) * 32);
-                            tmem_cp_scales<1>(x_t, sfdesc + (SF_BYTES / 16) + (kk >> 1) * 32);
-                        }
-                        mma_mxf4<1>(d_tmem, wdesc + 2 * kk, xdesc + 2 * kk, (kk & 1) ? idesc1 : idesc0, w_t, x_t,
+                        // +32 bytes (descriptor units of 16) per 64 elements inside the swizzled row
+                        const uint32_t w_t = sf_t + 8 * (kk >> 1);
+                        mma_mxf4<1>(d_tmem, wdesc + 2 * kk, xdesc + 2 * kk, (kk & 1) ? idesc1 : idesc0, w_t, w_t + 4,
                                     (ks | kk) != 0 ? 1u : 0u);
                     }
                     mma_commit(&empty[stage]);
@@ -341,7 +369,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             (void)mbar_wait(drain, 0, dguard);
         }
         __syncwarp();
-    } else {
+    } else if (warp < 6) {
         // ------------------------------------------------------------------ epilogue
         const int q = warp & 3;   // TMEM lane quarter: columns 32 q + lane of the tile's atom
         uint32_t acc = 0, acc_phase = 0;
