@@ -9,7 +9,7 @@
 // from -128 to 127 fit it (its subnormals reach 2^-133).
 //
 // Both kernels are HBM-bound streams: each element is read once. Rows: 16384 x 4096 bf16 with values in
-// 47.4 us (6.4 TB/s).
+// 47.1 us (6.5 TB/s), codes alone in 28.6 us.
 #include <cuda_bf16.h>
 
 #include "kernels.h"
@@ -252,7 +252,7 @@ cudaError_t launch_quantize_rows(const void* x, bool bf16, long long elements, u
                                  void* values, int sm_count, cudaStream_t stream) {
     const long long vecs = elements / 8;
     const long long want = (vecs + 255) / 256;
-    const int grid = static_cast<int>(want < 8LL * sm_count ? want : 8LL * sm_count);
+    const int grid = static_cast<int>(want < 16LL * sm_count ? want : 16LL * sm_count);
     const auto launch = [&](auto kern) {
         return launch_pdl(kern, dim3(grid), dim3(256), 0, stream, static_cast<const uint4*>(x), vecs,
                           reinterpret_cast<uint32_t*>(codes), scales, static_cast<uint4*>(values));
