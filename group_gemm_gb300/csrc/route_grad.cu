@@ -53,8 +53,12 @@ __device__ __forceinline__ float warp_sum(float v) {
     return v;
 }
 
-// One warp per copy f = t*k + j: reads dout[t] and y[inv[f]], writes dy[inv[f]] and dw[f]; then zeroes
-// row f of dy if no copy is placed there. Index values outside [0, T*k) count as none.
+// WARPS warps per copy f = t*k + j: reads dout[t] and y[inv[f]], writes dy[inv[f]] and dw[f]; then zeroes
+// row f of dy if no copy is placed there. Index values outside [0, T*k) count as none. One warp a copy
+// streams best when the copies fill the GPU (8192 tokens top-2, rows of 4096: 51.0 us, 6.6 TB/s); a whole
+// block a copy when they do not (61 tokens top-8, rows of 7168: 3.4 against
+// 7.4 us).
+template <int WARPS>
 __global__ void __launch_bounds__(256) unpermute_grad_kernel(const uint4* __restrict__ dout,
                                                              const uint4* __restrict__ y,
                                                              const int32_t* __restrict__ order,
@@ -62,11 +66,15 @@ __global__ void __launch_bounds__(256) unpermute_grad_kernel(const uint4* __rest
                                                              const float* __restrict__ w, long long total, int k,
                                                              int vec_per_row, uint4* __restrict__ dy,
                                                              float* __restrict__ dw) {
+    static_assert(WARPS == 1 || WARPS == 8, "a warp or a block per copy");
+    __shared__ float part[8];
     grid_dependency_enter();
+    constexpr int STEP = 32 * WARPS;   // threads of a copy
     const int lane = threadIdx.x & 31;
-    const long long warp = (static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
-    const long long nwarps = (static_cast<long long>(gridDim.x) * blockDim.x) >> 5;
-    for (long long f = warp; f < total; f += nwarps) {
+    const int sub = threadIdx.x % STEP;
+    const long long first = (static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x) / STEP;
+    const long long stride = static_cast<long long>(gridDim.x) * blockDim.x / STEP;
+    for (long long f = first; f < total; f += stride) {
         const int32_t p = __ldg(inv + f);
         const bool kept = p >= 0 && p < total;
         float dot = 0.f;
@@ -75,17 +83,17 @@ __global__ void __launch_bounds__(256) unpermute_grad_kernel(const uint4* __rest
             const uint4* d = dout + (f / k) * vec_per_row;
             const uint4* src = y + static_cast<long long>(p) * vec_per_row;
             uint4* dst = dy + static_cast<long long>(p) * vec_per_row;
-            for (int i0 = lane; i0 < vec_per_row; i0 += 32 * VEC_UNROLL) {
+            for (int i0 = sub; i0 < vec_per_row; i0 += STEP * VEC_UNROLL) {
                 uint4 a[VEC_UNROLL], b[VEC_UNROLL];
 #pragma unroll
                 for (int u = 0; u < VEC_UNROLL; ++u)
-                    if (i0 + 32 * u < vec_per_row) {
-                        a[u] = __ldg(d + i0 + 32 * u);
-                        b[u] = __ldg(src + i0 + 32 * u);
+                    if (i0 + STEP * u < vec_per_row) {
+                        a[u] = __ldg(d + i0 + STEP * u);
+                        b[u] = __ldg(src + i0 + STEP * u);
                     }
 #pragma unroll
                 for (int u = 0; u < VEC_UNROLL; ++u) {
-                    if (i0 + 32 * u >= vec_per_row) continue;
+                    if (i0 + STEP * u >= vec_per_row) continue;
                     float x[8], v[8];
                     Vec<true>::unpack(a[u], x);
                     Vec<true>::unpack(b[u], v);
@@ -94,16 +102,24 @@ __global__ void __launch_bounds__(256) unpermute_grad_kernel(const uint4* __rest
                         dot += x[c] * v[c];
                         x[c] *= wf;
                     }
-                    dst[i0 + 32 * u] = Vec<true>::pack(x);
+                    dst[i0 + STEP * u] = Vec<true>::pack(x);
                 }
             }
             __syncwarp();
             dot = warp_sum(dot);
         }
-        if (lane == 0) dw[f] = dot;
+        if constexpr (WARPS > 1) {   // f is the same for the whole block
+            if (lane == 0) part[threadIdx.x >> 5] = dot;
+            __syncthreads();
+            dot = 0.f;
+#pragma unroll
+            for (int i = 0; i < WARPS; ++i) dot += part[i];
+            __syncthreads();
+        }
+        if (sub == 0) dw[f] = dot;
         const int32_t o = __ldg(order + f);
         if (o < 0 || o >= total)
-            for (int i = lane; i < vec_per_row; i += 32) dy[f * vec_per_row + i] = make_uint4(0, 0, 0, 0);
+            for (int i = sub; i < vec_per_row; i += STEP) dy[f * vec_per_row + i] = make_uint4(0, 0, 0, 0);
     }
 }
 
@@ -242,9 +258,16 @@ cudaError_t launch_moe_unpermute_grad(const void* dout, const void* y_sorted, co
                                       const float* weights, long long tokens, int k, long long n, void* dy_sorted,
                                       float* dweights, int sm_count, cudaStream_t stream) {
     const long long total = tokens * k;
-    return launch_pdl(unpermute_grad_kernel, dim3(warps_grid(total, sm_count)), dim3(256), 0, stream,
-                      static_cast<const uint4*>(dout), static_cast<const uint4*>(y_sorted), order, inv, weights, total, k,
-                      static_cast<int>(n / 8), static_cast<uint4*>(dy_sorted), dweights);
+    // a block per copy while the copies are few for the length of their rows (measured on both sides:
+    // rows of 7168, 2048 copies 12.8 against 14.9 us; of 4096, 122 copies 2.2 / 4.2, 2048 copies 10.4 / 9.3; of
+    // 1024, 3200 copies 6.9 / 3.1)
+    const bool block = total * 64 < n / 8 * sm_count;
+    const long long blocks = block ? total : (total + 7) / 8;
+    const int grid = static_cast<int>(blocks < 8LL * sm_count ? blocks : 8LL * sm_count);
+    auto kern = block ? unpermute_grad_kernel<8> : unpermute_grad_kernel<1>;
+    return launch_pdl(kern, dim3(grid), dim3(256), 0, stream, static_cast<const uint4*>(dout),
+                      static_cast<const uint4*>(y_sorted), order, inv, weights, total, k, static_cast<int>(n / 8),
+                      static_cast<uint4*>(dy_sorted), dweights);
 }
 
 cudaError_t launch_moe_permute_grad(const void* dx_sorted, bool bf16, const int32_t* inv, long long tokens, int k,

@@ -28,7 +28,8 @@ def main():
     ap = argparse.ArgumentParser()
     ap.add_argument("--kernel", choices=["fwd", "dgrad", "wgrad", "padded", "mxfp8", "mxdgrad", "mxwgrad", "gated",
                                          "permute",
-                                         "unpermute", "topk"], default="fwd")
+                                         "unpermute", "topk", "mxfp4", "mx4rows", "mx4weight", "unpermute_grad",
+                                         "permute_grad", "topk_grad"], default="fwd")
     ap.add_argument("--workload", default="mixtral_bf16")
     ap.add_argument("--tokens", type=int, default=2048)
     ap.add_argument("--iters", type=int, default=3)
@@ -97,6 +98,45 @@ def main():
         def run():
             gg.rdot_forward_gated(plan.handle, lhs, w0, w1, gs_d, out, plan.workspace, stream)
         flops = 4.0 * m * k * n
+    elif args.kernel in ("mxfp4", "mx4rows", "mx4weight"):
+        # the MXFP4 product of quantised rows and weights, or either quantiser (with the values)
+        x = ri.device_normal((m, k), 1, 1.0, dev, torch.bfloat16)
+        w = ri.device_normal((g, k, n), 2, 0.02, dev, torch.float32)
+        xq, xs, xv = gg.quantize_mxfp4(x, values=True)
+        wq, ws, wv = gg.quantize_mxfp4_weight(w, values=True)
+        out = torch.empty((m, n), dtype=torch.bfloat16, device=dev)
+        plan = gg.Plan(m, k, n, g, "forward_mxfp4", "e2m1", "bf16", flags=args.flags)
+        if args.kernel == "mxfp4":
+            del w, wv
+
+            def run():
+                gg.rdot_forward_mxfp4(plan.handle, xq, xs, wq, ws, gs_d, out, plan.workspace, stream)
+        elif args.kernel == "mx4rows":
+            def run():
+                gg.rdot_quantize_mxfp4(x, xq, xs, xv, stream)
+        else:
+            def run():
+                gg.rdot_quantize_mxfp4_weight(w, wq, ws, wv, stream)
+        flops = 2.0 * m * k * n if args.kernel == "mxfp4" else 0.0
+    elif args.kernel in ("unpermute_grad", "permute_grad", "topk_grad"):
+        # the gradients of the routing kernels below, rows of width K
+        t = args.tokens
+        logits = ri.device_normal((t, g), 4, 1.0, dev, torch.float32)
+        ids, wts = gg.router_topk(logits, topk, "softmax")
+        x = ri.device_normal((t, k), 5, 1.0, dev, torch.bfloat16)
+        xs, gsz, order, inv = gg.moe_permute(ids, x, g)
+        dy, dx, dl = torch.empty_like(xs), torch.empty_like(x), torch.empty_like(logits)
+        dw = torch.empty_like(wts)
+        plan = None
+
+        def run():
+            if args.kernel == "unpermute_grad":
+                gg.rdot_moe_unpermute_grad(x, xs, order, inv, wts, dy, dw, stream)
+            elif args.kernel == "permute_grad":
+                gg.rdot_moe_permute_grad(xs, inv, dx, stream)
+            else:
+                gg.rdot_router_topk_grad(logits, ids, wts, wts, gg.RDOT_ROUTER_SOFTMAX, dl, stream)
+        flops = 0.0
     elif args.kernel in ("permute", "unpermute", "topk"):
         # the routing kernels on `tokens` tokens routed top-k over the workload's experts: the
         # permute of rows of width K, the weighted un-permute of rows of width K, the router top-k
