@@ -1556,6 +1556,6 @@ const char* rdot_status_string(rdot_status status) {
 
 const char* rdot_last_cuda_error(void) { return g_last_cuda_error.c_str(); }
 
-int rdot_version(void) { return 103; }
+int rdot_version(void) { return 104; }
 
 }  // extern "C"

@@ -149,6 +149,8 @@ CASES = [
     (1000, 768, 776, [0, 313, 1, 0, 257, 300, 129]),
     (700, 1152, 264, [100, 0, 300, 200]),              # rows past the sum; 36 scale bytes a row
     (40, 7168, 512, [7, 0, 0, 1, 30]),
+    (260, 256, 136, [i % 9 if i % 3 else 0 for i in range(65)]),      # more groups than a warp has lanes
+    (1500, 64, 72, [1 + i % 2 if i % 4 else 0 for i in range(1024)]),   # the most groups a plan takes
 ]
 
 

@@ -57,7 +57,7 @@ def unpermute_ref(dout, y, order, inv, w):
 CASES = [          # tokens, topk, experts, n, share of dropped copies
     (1, 1, 1, 8, 0.0), (1, 2, 8, 64, 0.0), (1, 8, 256, 7168, 0.2), (3, 2, 8, 264, 0.0), (33, 4, 5, 1032, 0.3),
     (257, 8, 128, 4096, 0.1), (700, 1, 3, 24, 0.0), (64, 40, 7, 136, 0.1), (50, 3, 4, 512, 1.0),
-    (5000, 2, 8, 128, 0.05),
+    (5000, 2, 8, 128, 0.05), (701, 1, 3, 24, 0.1), (1001, 3, 64, 512, 0.1), (333, 5, 9, 2048, 0.0),
 ]
 
 
@@ -137,6 +137,24 @@ def test_router_topk_grad_of_special_logits():
         dl = gg.router_topk_grad(logits, ids, w, torch.tensor([[1.0, -2.0]] * 3, device=DEV), mode)
         assert torch.all(dl[0, 2:] == 0) and torch.isfinite(dl[0]).all() and torch.isfinite(dl[2]).all()
         assert torch.isnan(dl[1]).all() if mode == "softmax" else torch.isfinite(dl[1]).all()
+
+
+def test_router_topk_grad_counts_bad_and_repeated_ids():
+    """An id outside the experts counts as none (its weight still enters the softmax's sum); copies of one
+    expert, which the router never makes, add up."""
+    for experts in (8, 40, 300):
+        logits = torch.randn((3, experts), generator=torch.Generator(device=DEV).manual_seed(9), device=DEV)
+        ids = torch.tensor([[1, -1, 5], [7, 7, 7], [experts, 0, 6]], dtype=torch.int32, device=DEV)
+        w = torch.tensor([[0.5, 0.25, 0.25]] * 3, device=DEV)
+        g = torch.tensor([[1.0, 2.0, -3.0]] * 3, device=DEV)
+        for mode in ("values", "softmax_topk"):
+            term = g if mode == "values" else w * (g - (w * g).sum(1, keepdim=True))
+            want = torch.zeros((3, experts), device=DEV)
+            for t in range(3):
+                for j in range(3):
+                    if 0 <= ids[t, j] < experts:
+                        want[t, ids[t, j]] += term[t, j]
+            assert torch.equal(gg.router_topk_grad(logits, ids, w, g, mode), want)
 
 
 def test_gradients_agree_with_differences_of_the_forward():
