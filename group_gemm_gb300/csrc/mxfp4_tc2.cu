@@ -23,7 +23,6 @@
 // about 2000 clocks a tile for the read-out.)
 #include <cuda_bf16.h>
 
-#include "epilogue.cuh"
 #include "kernels.h"
 #include "mxfp4.cuh"
 #include "pairdrain.cuh"
@@ -49,7 +48,7 @@ constexpr int RING_BYTES = STAGES * STAGE_BYTES;
 constexpr int SFB_STAGES = 10;                       // the weight scales' own ring runs further ahead
 constexpr int SFB_STAGE_BYTES = 4 * MX4_ATOM_BYTES;  // the scales of all 256 columns, 256 elements
 constexpr int SFB_BYTES = SFB_STAGES * SFB_STAGE_BYTES;
-constexpr int EPI_BYTES = EPI_WARPS * EpiStage<false>::BYTES;
+constexpr int EPI_BYTES = EPI_WARPS * 32 * 64;      // a 32 x 32 bf16 block per epilogue warp
 constexpr int BAR_BYTES = (3 * STAGES + 2 * SFB_STAGES + 8) / 2 * 16;   // full, sfull, empty; bfull, bempty; afull[2],
                                                                        // aempty[2], tfull, tempty, drain
 constexpr int MISC_BYTES = 16;
@@ -89,6 +88,27 @@ __device__ __forceinline__ void tmem_read_bf16_32x64(uint32_t taddr, uint32_t (&
     }
 }
 
+// Stores a 32 x 32 block already packed as bf16 (p[j]: columns 2j, 2j + 1 of row `lane`): turned through
+// 2 KB of shared memory in 16-byte units (unit u of row r at u ^ (r / 2) % 4, conflict-free both ways), so that
+// four lanes store 64 consecutive bytes of a row. Word-wise, as store_packed_bf16_32x32 turns its block, the
+// epilogue took 4700 clocks a tile, more than the MMAs of a contraction below 2048.
+__device__ __forceinline__ void store_block_bf16_v16(const uint32_t (&p)[16], uint4* stage, __nv_bfloat16* out,
+                                                     long long ld, int rows_valid, int cols_valid) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+        stage[4 * lane + (u ^ ((lane >> 1) & 3))] = make_uint4(p[4 * u], p[4 * u + 1], p[4 * u + 2], p[4 * u + 3]);
+    __syncwarp();
+    const int rr = lane >> 2, u = lane & 3;
+#pragma unroll
+    for (int it = 0; it < 4; ++it) {
+        const int row = it * 8 + rr;
+        const uint4 v = stage[4 * row + (u ^ ((row >> 1) & 3))];
+        if (row < rows_valid && 8 * u < cols_valid) *reinterpret_cast<uint4*>(out + row * ld + 8 * u) = v;
+    }
+    __syncwarp();
+}
+
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     mxfp4_tc2_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ CUtensorMap tmap_b,
                      const __grid_constant__ CUtensorMap tmap_sfb, Mx4Args a) {
@@ -96,7 +116,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t* sfb_ring = smem + RING_BYTES;
     uint8_t* sfa_buf = sfb_ring + SFB_BYTES;
-    uint32_t* epi_stage = reinterpret_cast<uint32_t*>(sfa_buf + SFA_BYTES);
+    uint4* epi_stage = reinterpret_cast<uint4*>(sfa_buf + SFA_BYTES);
     uint8_t* bars = sfa_buf + SFA_BYTES + EPI_BYTES;
     uint64_t* full = reinterpret_cast<uint64_t*>(bars);
     uint64_t* sfull = full + STAGES;    // even CTA: both CTAs' scales of the stage are in tensor memory
@@ -367,7 +387,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         // ------------------------------------------------------------------ epilogue (both CTAs)
         const int q = warp & 3;
         const int half = (warp - EPI_WARP) / 4;
-        uint32_t* stage_buf = epi_stage + (warp - EPI_WARP) * EpiStage<false>::WORDS;
+        uint4* stage_buf = epi_stage + (warp - EPI_WARP) * (32 * 64 / 16);
         uint32_t acc_phase = 0;
         for (int w = cluster; w < W; w += nclusters) {
             const Tile t = decode_tile(w, tprefix, off, a.G, BM, a.NT, m_inner);
@@ -396,7 +416,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                 for (int c = 0; c < 2; ++c) {
                     const int col = col0 + c * 32;
                     if (rows_valid > 0 && col < a.N)
-                        store_packed_bf16_32x32(pk[c], stage_buf, out_rows + col, a.N, rows_valid, a.N - col);
+                        store_block_bf16_v16(pk[c], stage_buf, out_rows + col, a.N, rows_valid, a.N - col);
                 }
             }
             acc_phase ^= 1;
