@@ -190,15 +190,17 @@ bool want_mx_skinny(const rdot_problem& p) {
 }
 
 // The MXFP4 forward takes its swapped kernel (mxfp4_skinny.cu) while the rows, spread evenly over
-// min(M, G) groups, come to at most kMx4SkinnyRows a group: then it streams weights and the 128 token
-// rows of a pair tile would be mostly empty.
-constexpr long long kMx4SkinnyRows = 32;
-
-bool want_mx4_skinny(const rdot_problem& p) {
+// min(M, G) groups, come to at most 32 a group, where it streams weights and a pair tile would be mostly
+// empty (8 experts, 4096 -> 14336: 32 rows 43.5 against 47.8 us, 64 rows 44.9 / 49.7, 128 rows 71.2 / 51.4;
+// with skewed routing of 64 rows a group 57.6 / 49.0); and up to 128 rows a group while there are fewer
+// pair tiles than pairs of SMs (4 groups of 128 rows, 2048 -> 2048: 7.3 against 10.0 us; one group, 8192 ->
+// 8192: 128 rows 14.5 / 18.4, 256 rows 23.8 / 17.8).
+bool want_mx4_skinny(const rdot_problem& p, int sm_count) {
     if (p.flags & RDOT_FLAG_SKINNY) return true;
     if (p.flags & (RDOT_FLAG_NO_SKINNY | RDOT_FLAG_CTA_PAIR)) return false;
     const long long routed = std::max<long long>(1, std::min<long long>(p.m, p.groups));
-    return (p.m + routed - 1) / routed <= kMx4SkinnyRows;
+    const long long rows = (p.m + routed - 1) / routed;
+    return rows <= 32 || (rows <= 128 && routed * ((p.n + 255) / 256) <= sm_count / 2);
 }
 
 // Token rows per tile of that kernel: 16 (a sixth stage of weights in flight) when, with the
@@ -404,7 +406,7 @@ rdot_status rdot_plan(const rdot_problem* problem, int device, rdot_plan_t* plan
             return RDOT_ERR_UNSUPPORTED;
         }
         pl->kind = 8;
-        pl->skinny = want_mx4_skinny(p);
+        pl->skinny = want_mx4_skinny(p, pl->sm_count);
         pl->pair = !pl->skinny;
         pl->tile_m = !pl->skinny ? TC2_BM : p.m <= 16 ? 16 : 64;   // token rows of the swapped kernel's tiles
         pl->tile_n = pl->skinny ? 128 : 256;

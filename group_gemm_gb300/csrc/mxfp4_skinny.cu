@@ -111,9 +111,9 @@ __global__ void __launch_bounds__(THREADS, 1)
     mxfp4_skinny_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant__ CUtensorMap tmap_w128,
                         const __grid_constant__ CUtensorMap tmap_w64, const __grid_constant__ CUtensorMap tmap_w32,
                         Mx4Args a) {
-    using R = Ring<TT>;
-    constexpr int STAGES = R::STAGES, STAGE_BYTES = R::STAGE_BYTES, X_BYTES = R::X_BYTES, RING_BYTES = R::RING_BYTES;
-    constexpr int BAR_BYTES = R::BAR_BYTES, TMEM_SF_BASE = R::TMEM_SF_BASE;
+    using L = Ring<TT>;
+    constexpr int STAGES = L::STAGES, STAGE_BYTES = L::STAGE_BYTES, X_BYTES = L::X_BYTES, RING_BYTES = L::RING_BYTES;
+    constexpr int BAR_BYTES = L::BAR_BYTES, TMEM_SF_BASE = L::TMEM_SF_BASE;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t* sfx_buf = smem + RING_BYTES;
@@ -249,24 +249,23 @@ __global__ void __launch_bounds__(THREADS, 1)
         __syncwarp();
     } else if (warp == 6) {
         // ------------------------------------------------------------------ token scale gather
-        // lane l loads rows l and l + 32 of the token tile. (in, kn) is the group of stages being loaded, one
+        // lane l loads row l, or rows l and l + 32, of the token tile. (in, kn) is the group of stages being loaded, one
         // ahead of the one being stored, across tiles too
         uint32_t buf = 0, phase = 0;
-        uint2 n0[MX4_GROUP], n1[MX4_GROUP];
+        constexpr int R = TT > 32 ? 2 : 1;   // rows a lane
+        uint2 nxt[R][MX4_GROUP];
         int in = 0, kn = 0;
         SkinnyTile tn{};
-        const auto load = [&] {
-            load_scale_group(a, static_cast<long long>(tn.row0) + lane, lane < tn.rows, kn, n0);
-            if (TT > 32) load_scale_group(a, static_cast<long long>(tn.row0) + lane + 32, lane + 32 < tn.rows, kn, n1);
-        };
+        const auto load = [&] { load_scale_group(a, tn.row0, tn.rows, lane, kn, nxt); };
         if (tiles > 0) {
             tn = skinny_tile<TT>(0, sh, a, tprefix, off);
             load();
         }
         while (in < tiles && tn.q0 < tn.q1) {
             if (!mx4_wait_uniform(&aempty[buf], phase ^ 1, guard)) break;
-            put_scale_group(sfx_buf + buf * MX4_GROUP_BYTES, lane, n0);
-            if (TT > 32) put_scale_group(sfx_buf + buf * MX4_GROUP_BYTES, lane + 32, n1);
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+                put_scale_group(sfx_buf + buf * MX4_GROUP_BYTES, lane + 32 * r, nxt[r], a.KS - kn);
             __syncwarp();
             if (lane == 0) mbar_arrive(&afull[buf]);
             buf ^= 1;

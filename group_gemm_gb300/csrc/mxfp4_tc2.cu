@@ -264,11 +264,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         uint2 nxt[4][MX4_GROUP];
         int wn = cluster, kn = 0;
         Tile tn{};
-        const auto load = [&] {
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                load_scale_group(a, static_cast<long long>(tn.row0) + first + 32 * i, first + 32 * i < tn.rows, kn, nxt[i]);
-        };
+        const auto load = [&] { load_scale_group(a, tn.row0, tn.rows, first, kn, nxt); };
         if (wn < W) {
             tn = decode_tile(wn, tprefix, off, a.G, BM, a.NT, m_inner);
             load();
@@ -277,7 +273,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
             ok = mx4_wait_uniform(&aempty[buf], phase ^ 1, guard);
             if (!ok) break;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) put_scale_group(sfa_buf + buf * MX4_GROUP_BYTES, lane + 32 * i, nxt[i]);
+            for (int i = 0; i < 4; ++i) put_scale_group(sfa_buf + buf * MX4_GROUP_BYTES, lane + 32 * i, nxt[i], a.KS - kn);
             __syncwarp();
             if (lane == 0) mbar_arrive(&afull[buf]);
             buf ^= 1;

@@ -225,7 +225,7 @@ def test_scales_at_any_byte_offset():
 def test_quantised_product_of_real_values_and_default_kernels():
     """quantize -> product through the high-level calls, against the 64-bit product of the quantised
     values; a few rows a group take the swapped kernel, more the pairs."""
-    for m, groups, tile in ((6, 4, (16, 128)), (90, 4, (64, 128)), (900, 4, (256, 256))):
+    for m, groups, tile in ((6, 4, (16, 128)), (90, 4, (64, 128)), (500, 4, (64, 128)), (900, 4, (256, 256))):
         k, n = 1024, 512
         g = gen(m)
         x = torch.randn((m, k), generator=g, device=DEV).to(torch.bfloat16)
