@@ -408,7 +408,7 @@ rdot_status rdot_plan(const rdot_problem* problem, int device, rdot_plan_t* plan
         pl->kind = 8;
         pl->skinny = want_mx4_skinny(p, pl->sm_count);
         pl->pair = !pl->skinny;
-        pl->tile_m = !pl->skinny ? TC2_BM : p.m <= 16 ? 16 : 64;   // token rows of the swapped kernel's tiles
+        pl->tile_m = pl->skinny ? MX4_SKINNY_ROWS : TC2_BM;
         pl->tile_n = pl->skinny ? 128 : 256;
         if (pl->skinny) pl->m_inner = 1;   // the token tiles of a group read one weight slab together
         const long long nt = (p.n + pl->tile_n - 1) / pl->tile_n;
@@ -1475,7 +1475,7 @@ rdot_status rdot_forward_mxfp4(rdot_plan_t plan, const void* lhs, const uint8_t*
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     cudaError_t e;
     if (plan->skinny) {
-        e = launch_mxfp4_skinny(map_a, map_b, a, plan->tile_m, plan->grid, s);
+        e = launch_mxfp4_skinny(map_a, map_b, a, plan->grid, s);
     } else {
         CUtensorMap map_sfb;
         st = encode_2d(&map_sfb, CU_TENSOR_MAP_DATA_TYPE_UINT32, rhs_scale,

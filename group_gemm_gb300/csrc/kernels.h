@@ -234,9 +234,9 @@ cudaError_t launch_mxfp4_pair(const CUtensorMap& tmap_a, const CUtensorMap& tmap
 int mxfp4_pair_max_clusters(int G);
 // MXFP4 forward for a few rows per group (mxfp4_skinny.cu): tmap_x: lhs codes, box (128, 16); tmap_w: rhs
 // codes, boxes (128, 128, 1), (128, 64, 1) and (128, 32, 1).
-// tt: token rows per tile, 16 (only for M <= 16) or 64.
-cudaError_t launch_mxfp4_skinny(const CUtensorMap& tmap_x, const CUtensorMap (&tmap_w)[3], const Mx4Args& a, int tt,
-                                int grid, cudaStream_t stream);
+constexpr int MX4_SKINNY_ROWS = 64;   // token rows per tile
+cudaError_t launch_mxfp4_skinny(const CUtensorMap& tmap_x, const CUtensorMap (&tmap_w)[3], const Mx4Args& a, int grid,
+                                cudaStream_t stream);
 // MXFP4 quantisation (mxfp4_quant.cu) of fp32 or bf16 elements: rows as one array of 32-element blocks, and
 // weights [groups, K, N] to codes [groups, N, K/2] and scale atoms. values (bf16, x's layout) may be null.
 cudaError_t launch_quantize_rows(const void* x, bool bf16, long long elements, uint8_t* codes, uint8_t* scales,

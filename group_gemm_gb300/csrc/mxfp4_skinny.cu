@@ -15,6 +15,11 @@
 // tensor-memory lane quarter and tell warp 1, which issues the MMAs and waits for nothing else: copies
 // by tcgen05.cp would run in order with the MMAs, as long as them. Warps 2..5 read out one 32-column
 // quarter each.
+//
+// Measured: one token top-2 of 8, 4096 -> 14336: 15.1 us, of which a launch with one stage takes 4.9 (62 MB at
+// 6.1 TB/s in the rest; row tiles on pairs 25 us); 64 tokens top-8 of 256 (143 experts routed), 7168 -> 4096:
+// 314.5 us, 7.1 TB/s of codes and scales. The ring's depth does not matter above five stages for one token;
+// 64 tokens take 2 % longer with five than with eight.
 #include <cuda_bf16.h>
 
 #include "kernels.h"
@@ -38,23 +43,20 @@ constexpr int MISC_BYTES = 16;
 constexpr int SF_COLS = 16;                     // per stage: two weight atoms, two token atoms
 constexpr int TMEM_COLS = 256;
 
-// TT token rows per tile: 64, or 16 where no tile can have more (at most 16 rows in all), which leaves
-// room for two more stages: 
-template <int TT>
-struct Ring {
-    static constexpr int STAGES = TT == 16 ? 10 : 8;
-    static constexpr int X_BYTES = TT * MX4_STAGE_BYTES;
-    static constexpr int STAGE_BYTES = W_BYTES + X_BYTES + SF_BYTES;
-    static constexpr int RING_BYTES = STAGES * STAGE_BYTES;
-    // full, xfull, sfull, empty; afull[2], aempty[2], tfull[2], tempty[2], drain
-    static constexpr int BAR_BYTES = (4 * STAGES + 10) / 2 * 16;
-    static constexpr int TMEM_SF_BASE = 2 * TT;                   // after the two accumulators
-    static_assert(STAGE_BYTES % 1024 == 0, "swizzle atoms stay 1 KB aligned");
-    static_assert(TMEM_SF_BASE + STAGES * SF_COLS <= TMEM_COLS, "tensor memory budget");
-    static size_t smem_bytes(int G) {
-        return 1024 + RING_BYTES + SFX_BYTES + BAR_BYTES + MISC_BYTES + sizeof(int32_t) * 2 * (G + 1);
-    }
-};
+constexpr int TT = MX4_SKINNY_ROWS;             // token rows per tile (64)
+constexpr int STAGES = 8;
+constexpr int X_BYTES = TT * MX4_STAGE_BYTES;
+constexpr int STAGE_BYTES = W_BYTES + X_BYTES + SF_BYTES;
+constexpr int RING_BYTES = STAGES * STAGE_BYTES;
+// full, xfull, sfull, empty; afull[2], aempty[2], tfull[2], tempty[2], drain
+constexpr int BAR_BYTES = (4 * STAGES + 10) / 2 * 16;
+constexpr int TMEM_SF_BASE = 2 * TT;            // after the two accumulators
+static_assert(STAGE_BYTES % 1024 == 0, "swizzle atoms stay 1 KB aligned");
+static_assert(TMEM_SF_BASE + STAGES * SF_COLS <= TMEM_COLS, "tensor memory budget");
+
+size_t smem_bytes(int G) {
+    return 1024 + RING_BYTES + SFX_BYTES + BAR_BYTES + MISC_BYTES + sizeof(int32_t) * 2 * (G + 1);
+}
 
 __device__ __forceinline__ void tmem_ld_32x16(uint32_t taddr, uint32_t (&r)[16]) {
     asm volatile(
@@ -90,7 +92,6 @@ __device__ __forceinline__ SkinnyShare skinny_share(int items) {
 }
 
 // Tile i of the share, 0 .. whole (the last one only if part >= 0; it may lie past N: then q1 <= q0).
-template <int TT>
 __device__ __forceinline__ SkinnyTile skinny_tile(int i, const SkinnyShare& sh, const Mx4Args& a, const int32_t* tprefix,
                                                   const int32_t* off) {
     const bool whole = i < sh.whole;
@@ -106,14 +107,10 @@ __device__ __forceinline__ SkinnyTile skinny_tile(int i, const SkinnyShare& sh, 
     return s;
 }
 
-template <int TT>
 __global__ void __launch_bounds__(THREADS, 1)
     mxfp4_skinny_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant__ CUtensorMap tmap_w128,
                         const __grid_constant__ CUtensorMap tmap_w64, const __grid_constant__ CUtensorMap tmap_w32,
                         Mx4Args a) {
-    using L = Ring<TT>;
-    constexpr int STAGES = L::STAGES, STAGE_BYTES = L::STAGE_BYTES, X_BYTES = L::X_BYTES, RING_BYTES = L::RING_BYTES;
-    constexpr int BAR_BYTES = L::BAR_BYTES, TMEM_SF_BASE = L::TMEM_SF_BASE;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t* sfx_buf = smem + RING_BYTES;
@@ -179,7 +176,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         uint32_t stage = 0, phase = 0, issued_mask = 0, issued_phase = 0;
         bool ok = true;
         for (int i = 0; i < tiles && ok; ++i) {
-            const SkinnyTile t = skinny_tile<TT>(i, sh, a, tprefix, off);
+            const SkinnyTile t = skinny_tile(i, sh, a, tprefix, off);
             const CUtensorMap* map = i < sh.whole || sh.width == 4 ? &tmap_w128 : sh.width == 2 ? &tmap_w64 : &tmap_w32;
             const int rows = i < sh.whole ? 128 : 32 * sh.width;
             for (int ks = 0; ks < a.KS && t.q0 < t.q1; ++ks) {
@@ -215,7 +212,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         uint32_t stage = 0, phase = 0, issued_mask = 0, issued_phase = 0;
         bool ok = true;
         for (int i = 0; i < tiles && ok; ++i) {
-            const SkinnyTile t = skinny_tile<TT>(i, sh, a, tprefix, off);
+            const SkinnyTile t = skinny_tile(i, sh, a, tprefix, off);
             const int nx = (t.rows + 15) / 16;
             const uint8_t* sfw = a.rhs_scale + (static_cast<long long>(t.g) * a.NB + t.nb) * a.KA * MX4_ATOM_BYTES;
             for (int ks = 0; ks < a.KS && t.q0 < t.q1; ++ks) {
@@ -249,22 +246,21 @@ __global__ void __launch_bounds__(THREADS, 1)
         __syncwarp();
     } else if (warp == 6) {
         // ------------------------------------------------------------------ token scale gather
-        // lane l loads row l, or rows l and l + 32, of the token tile. (in, kn) is the group of stages being loaded, one
+        // lane l loads rows l and l + 32 of the token tile. (in, kn) is the group of stages being loaded, one
         // ahead of the one being stored, across tiles too
         uint32_t buf = 0, phase = 0;
-        constexpr int R = TT > 32 ? 2 : 1;   // rows a lane
-        uint2 nxt[R][MX4_GROUP];
+        uint2 nxt[2][MX4_GROUP];
         int in = 0, kn = 0;
         SkinnyTile tn{};
         const auto load = [&] { load_scale_group(a, tn.row0, tn.rows, lane, kn, nxt); };
         if (tiles > 0) {
-            tn = skinny_tile<TT>(0, sh, a, tprefix, off);
+            tn = skinny_tile(0, sh, a, tprefix, off);
             load();
         }
         while (in < tiles && tn.q0 < tn.q1) {
             if (!mx4_wait_uniform(&aempty[buf], phase ^ 1, guard)) break;
 #pragma unroll
-            for (int r = 0; r < R; ++r)
+            for (int r = 0; r < 2; ++r)
                 put_scale_group(sfx_buf + buf * MX4_GROUP_BYTES, lane + 32 * r, nxt[r], a.KS - kn);
             __syncwarp();
             if (lane == 0) mbar_arrive(&afull[buf]);
@@ -273,7 +269,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             kn += MX4_GROUP;
             if (kn >= a.KS) {
                 kn = 0;
-                if (++in < tiles) tn = skinny_tile<TT>(in, sh, a, tprefix, off);
+                if (++in < tiles) tn = skinny_tile(in, sh, a, tprefix, off);
             }
             if (in < tiles) load();
         }
@@ -283,7 +279,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         uint32_t stage = 0, phase = 0, buf = 0, aphase = 0;
         bool ok = true;
         for (int i = 0; i < tiles && ok; ++i) {
-            const SkinnyTile t = skinny_tile<TT>(i, sh, a, tprefix, off);
+            const SkinnyTile t = skinny_tile(i, sh, a, tprefix, off);
             for (int ks = 0; ks < a.KS && t.q0 < t.q1; ++ks) {
                 const int j = ks % MX4_GROUP;
                 if (j == 0) ok = mx4_wait_uniform(&afull[buf], aphase, guard);
@@ -322,7 +318,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         uint32_t stage = 0, phase = 0, acc = 0, acc_phase = 0;
         bool ok = true;
         for (int i = 0; i < tiles; ++i) {
-            const SkinnyTile t = skinny_tile<TT>(i, sh, a, tprefix, off);
+            const SkinnyTile t = skinny_tile(i, sh, a, tprefix, off);
             if (t.q0 >= t.q1) break;   // only ever the last tile
             const int n = 16 * ((t.rows + 15) / 16);
             ok = mx4_wait_uniform(&tempty[acc], acc_phase ^ 1, guard);
@@ -374,7 +370,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         uint32_t acc = 0, acc_phase = 0;
         __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out);
         for (int i = 0; i < tiles; ++i) {
-            const SkinnyTile t = skinny_tile<TT>(i, sh, a, tprefix, off);
+            const SkinnyTile t = skinny_tile(i, sh, a, tprefix, off);
             if (t.q0 >= t.q1) break;
             if (!mx4_wait_warp(&tfull[acc], acc_phase, guard)) break;
             tc_fence_after();
@@ -424,14 +420,14 @@ __global__ void __launch_bounds__(THREADS, 1)
 
 }  // namespace
 
-cudaError_t launch_mxfp4_skinny(const CUtensorMap& tmap_x, const CUtensorMap (&tmap_w)[3], const Mx4Args& a, int tt,
-                                int grid, cudaStream_t stream) {
-    if (tt != 16 && tt != 64) return cudaErrorInvalidValue;
-    const size_t shm = tt == 16 ? Ring<16>::smem_bytes(a.G) : Ring<64>::smem_bytes(a.G);
-    auto kern = tt == 16 ? mxfp4_skinny_kernel<16> : mxfp4_skinny_kernel<64>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(shm));
+cudaError_t launch_mxfp4_skinny(const CUtensorMap& tmap_x, const CUtensorMap (&tmap_w)[3], const Mx4Args& a, int grid,
+                                cudaStream_t stream) {
+    const size_t shm = smem_bytes(a.G);
+    cudaError_t e = cudaFuncSetAttribute(mxfp4_skinny_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         static_cast<int>(shm));
     if (e != cudaSuccess) return e;
-    return launch_pdl(kern, dim3(grid), dim3(THREADS), shm, stream, tmap_x, tmap_w[0], tmap_w[1], tmap_w[2], a);
+    return launch_pdl(mxfp4_skinny_kernel, dim3(grid), dim3(THREADS), shm, stream, tmap_x, tmap_w[0], tmap_w[1],
+                      tmap_w[2], a);
 }
 
 }  // namespace rdot

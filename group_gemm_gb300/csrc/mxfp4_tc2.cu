@@ -8,19 +8,24 @@
 // the tensor cores consume a stage in 512 clocks, so a lone 128 x 256 tile would ask 100 bytes per
 // clock and SM of L2, a pair tile 68.
 //
-// Scales reach tensor memory through registers, not through tcgen05.cp: the six copies a stage
-// would need run in order with the MMAs on the tensor pipe and cost 145 of 531 us at 16384 rows x 4096
-// -> 14336 (8 experts). Four scale warps per CTA, one for each lane quarter, write the stage's 24
-// columns with tcgen05.st: the rows' scales, gathered by another warp from global memory a group of
-// stages ahead and put down as atoms; the weights' atoms (laid out once, by the quantiser), brought by
-// TMA in a ring of their own. The even CTA
-// issues M = 256, N = 256, K = 64 MMAs.
+// Scales reach tensor memory through registers, not through tcgen05.cp: the six copies a stage would need
+// run in order with the MMAs on the tensor pipe (145 of 531 us in an earlier form of this kernel, at the
+// shapes below). Four scale warps per CTA, one for each lane quarter, write the stage's 24 columns with
+// tcgen05.st: the rows' scales, gathered by another warp from global memory a group of stages ahead and
+// put down as atoms; the weights' atoms (laid out once, by the quantiser), brought by TMA in a ring of
+// their own. The even CTA issues M = 256, N = 256, K = 64 MMAs.
 //
 // Two accumulators share their middle: tensor memory holds 512 columns, the scales of five stages take
 // 120, and a tile 256, so even tiles accumulate in columns [0, 256) and odd ones in [128, 384). The eight
 // epilogue warps of a CTA read a tile's shared half out first, 64 columns each, and hand it back; the
 // next tile then starts while they read the other half and store. (With one accumulator the MMAs waited
-// about 2000 clocks a tile for the read-out.)
+// about 2000 clocks a tile for the read-out, so about 1250.)
+//
+// Measured at 16384 rows x 4096 -> 14336, 8 experts: 300-310 us (6.2-6.4 PFLOP/s, by GPU) in a burst; 330-340 us
+// sustained, where the power cap holds the clock at 1.7 GHz. At 4096 rows the tensor pipe is active 62 % of
+// the clocks and L2 45 % busy (ncu); per stage the MMA warp spends about 500 clocks issuing (512 is the MMAs'
+// own time) and 220 in its two waits. Short contractions are bound by the epilogue (65536 rows x 512 -> 4096:
+// 120 us, 4.5 TB/s of output).
 #include <cuda_bf16.h>
 
 #include "kernels.h"
@@ -69,7 +74,7 @@ size_t smem_bytes(int G) {
 // Arrive on a barrier of the even CTA for work whose only data is tensor memory (scales written, an
 // accumulator read): tcgen05.wait and tcgen05.fence order that data, so the arrive itself need not
 // release this thread's other writes to the cluster. A release at cluster scope took about as long as a
-// stage's MMAs, and one per stage set the kernel's pace (678 against 448 us at the shapes above).
+// stage's MMAs, and one per stage set the kernel's pace (678 against 460 us at the shapes above).
 __device__ __forceinline__ void mbar_arrive_tmem(uint32_t cluster_addr) {
     asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }

@@ -228,12 +228,12 @@ RDOT_API rdot_status rdot_quantize_mxfp4_weight(const void* w, int32_t dtype, in
  *   out        device bf16 [M, N]
  * Plan: mode RDOT_MODE_FORWARD_MXFP4, in_dtype RDOT_E2M1, out_dtype RDOT_BF16, tile_n 0, K % 32 == 0,
  * N % 8 == 0. Few rows per group (at most 32, spread evenly over min(M, G) groups; up to 128 where
- * the CTA pairs would not all find a tile) run on the swapped kernel (64 token rows x 128 columns,
- * 16 x 128 when m <= 16), more on CTA pairs (256 x 256);
- * RDOT_FLAG_SKINNY, RDOT_FLAG_NO_SKINNY and RDOT_FLAG_CTA_PAIR force either, and
- * RDOT_FLAG_NO_CTA_PAIR is RDOT_ERR_UNSUPPORTED without RDOT_FLAG_SKINNY. lhs_scale may have any
- * alignment (8 bytes is fastest), the others 16 bytes; same workspace, status and stream rules as
- * rdot_forward, and every call can be captured in a CUDA graph (nothing is kept between calls). */
+ * the CTA pairs would not all find a tile) run on the swapped kernel (64 token rows x 128 columns),
+ * more on CTA pairs (256 x 256); RDOT_FLAG_SKINNY, RDOT_FLAG_NO_SKINNY and RDOT_FLAG_CTA_PAIR force
+ * either, and RDOT_FLAG_NO_CTA_PAIR is RDOT_ERR_UNSUPPORTED without RDOT_FLAG_SKINNY. lhs_scale may
+ * have any alignment (16 bytes and K % 512 == 0 are fastest), the others 16 bytes; same workspace,
+ * status and stream rules as rdot_forward, and every call can be captured in a CUDA graph (nothing
+ * is kept between calls). */
 RDOT_API rdot_status rdot_forward_mxfp4(rdot_plan_t plan, const void* lhs, const uint8_t* lhs_scale, const void* rhs,
                                         const uint8_t* rhs_scale, const int32_t* group_sizes, void* out,
                                         void* workspace, void* stream);

@@ -120,7 +120,7 @@ def run(xq, xs, wq, ws, sizes, variant):
     m, n, k = xq.shape[0], wq.shape[1], 2 * xq.shape[1]
     plan = gg.Plan(m, k, n, len(sizes), "forward_mxfp4", "e2m1", "bf16", flags=VARIANTS[variant])
     if variant != "default":
-        assert (plan.info["tile_m"], plan.info["tile_n"]) == {"pair": (256, 256), "skinny": (64 if m > 16 else 16, 128)}[variant]
+        assert (plan.info["tile_m"], plan.info["tile_n"]) == {"pair": (256, 256), "skinny": (64, 128)}[variant]
     out = torch.full((m, n), float("nan"), dtype=torch.bfloat16, device=DEV)
     gg.rdot_forward_mxfp4(plan.handle, xq, xs, wq, mx.tile_scales(ws),
                           torch.tensor(sizes, dtype=torch.int32, device=DEV), out, plan.workspace)
@@ -225,7 +225,7 @@ def test_scales_at_any_byte_offset():
 def test_quantised_product_of_real_values_and_default_kernels():
     """quantize -> product through the high-level calls, against the 64-bit product of the quantised
     values; a few rows a group take the swapped kernel, more the pairs."""
-    for m, groups, tile in ((6, 4, (16, 128)), (90, 4, (64, 128)), (500, 4, (64, 128)), (900, 4, (256, 256))):
+    for m, groups, tile in ((6, 4, (64, 128)), (90, 4, (64, 128)), (500, 4, (64, 128)), (900, 4, (256, 256))):
         k, n = 1024, 512
         g = gen(m)
         x = torch.randn((m, k), generator=g, device=DEV).to(torch.bfloat16)
