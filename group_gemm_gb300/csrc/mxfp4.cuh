@@ -50,7 +50,8 @@ __device__ __forceinline__ void mma_mxf4(uint32_t d_tmem, uint64_t a_desc, uint6
 }
 
 // group_scan_warp (sched.cuh) with each size loaded once, for up to 32 groups a lane's: its three passes
-// over the sizes are three L2 round trips at the start of every CTA, 1 us of a one-token call.
+// over the sizes are three L2 round trips at the start of every CTA (one token top-2 of 8, 4096 -> 14336:
+// 15.0 against 15.6 us; 300 rows x 1024 -> 1408, 8 experts: 5.5 against 6.5 us).
 __device__ __forceinline__ int mx4_group_scan(const int32_t* __restrict__ group_sizes, int G, int M, int BM, int NT,
                                               int32_t* off, int32_t* tile_prefix) {
     if (G > 32) return group_scan_warp(group_sizes, G, M, BM, NT, off, tile_prefix);
@@ -84,8 +85,8 @@ __device__ __forceinline__ int mx4_group_scan(const int32_t* __restrict__ group_
     return bad || over ? RDOT_STATUS_BIT_GROUP_SIZES : 0;
 }
 
-// mbar_wait (ptx.cuh) that looks at the clock only after MX4_TRIES waits: reading the global timer takes
-// longer than these rings' waits usually do, and mbar_wait reads it before its second look.
+// mbar_wait (ptx.cuh) that looks at the clock only after MX4_TRIES waits, where mbar_wait reads the global
+// timer before its second look (16384 rows x 4096 -> 14336: 304 against 320 us; one token 15.0 against 15.7).
 constexpr int MX4_TRIES = 32;
 
 __device__ __forceinline__ bool mx4_wait(uint64_t* bar, uint32_t parity, const WaitGuard& g) {

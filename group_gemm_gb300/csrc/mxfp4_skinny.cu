@@ -17,8 +17,8 @@
 // quarter each.
 //
 // Measured: one token top-2 of 8, 4096 -> 14336: 15.1 us, of which a launch with one stage takes 4.9 (62 MB at
-// 6.1 TB/s in the rest; row tiles on pairs 25 us); 64 tokens top-8 of 256 (143 experts routed), 7168 -> 4096:
-// 314.5 us, 7.1 TB/s of codes and scales. The ring's depth does not matter above five stages for one token;
+// 6.1 TB/s in the rest; the pair kernel 19.9 us); 64 tokens top-8 of 256 (143 experts routed), 7168 -> 4096:
+// 314-321 us by GPU, 7.0-7.1 TB/s of codes and scales. The ring's depth does not matter above five stages for one token;
 // 64 tokens take 2 % longer with five than with eight.
 #include <cuda_bf16.h>
 

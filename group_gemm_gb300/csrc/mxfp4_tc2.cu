@@ -9,8 +9,8 @@
 // clock and SM of L2, a pair tile 68.
 //
 // Scales reach tensor memory through registers, not through tcgen05.cp: the six copies a stage would need
-// run in order with the MMAs on the tensor pipe (145 of 531 us in an earlier form of this kernel, at the
-// shapes below). Four scale warps per CTA, one for each lane quarter, write the stage's 24 columns with
+// run in order with the MMAs on the tensor pipe (386 us without them against 531 with, in a timing copy
+// of an earlier form without its row-scale gather, at the shapes below). Four scale warps per CTA, one for each lane quarter, write the stage's 24 columns with
 // tcgen05.st: the rows' scales, gathered by another warp from global memory a group of stages ahead and
 // put down as atoms; the weights' atoms (laid out once, by the quantiser), brought by TMA in a ring of
 // their own. The even CTA issues M = 256, N = 256, K = 64 MMAs.
