@@ -315,6 +315,8 @@ def rdot_moe_unpermute_grad(dout, y_sorted, order, inv, topk_weights, dy_sorted,
 
 def rdot_moe_permute_grad(dx_sorted, inv, dx, stream=None) -> None:
     """dx_sorted [T*k, N] (fp32 or bf16) -> dx [T, N], the same dtype."""
+    if dx.dtype != dx_sorted.dtype:
+        raise TypeError("dx must have dx_sorted's dtype")
     t = dx.shape[0]
     _check(load().rdot_moe_permute_grad(_ptr(dx_sorted), _float_dtype(dx_sorted, "dx_sorted"), _ptr(inv), int(t),
                                         inv.numel() // t if t else 1, int(dx.shape[1]), _ptr(dx),
@@ -324,6 +326,8 @@ def rdot_moe_permute_grad(dx_sorted, inv, dx, stream=None) -> None:
 def rdot_router_topk_grad(logits, topk_ids, topk_weights, dweights, weights_mode: int, dlogits, stream=None) -> None:
     """The logits' gradient, dlogits [T, E] (fp32 or bf16), from the weights' (fp32 [T, k]); logits
     (the same dtype) may be None unless the weights are the softmax over all experts."""
+    if logits is not None and logits.dtype != dlogits.dtype:
+        raise TypeError("logits must have dlogits' dtype")
     t, e = dlogits.shape
     _check(load().rdot_router_topk_grad(_ptr(logits), _float_dtype(dlogits, "dlogits"), _ptr(topk_ids),
                                         _ptr(topk_weights), _ptr(dweights), int(t), int(e), int(topk_ids.shape[1]),

@@ -89,3 +89,15 @@ def test_high_level_calls_check_shapes_and_types():
         gg.router_topk_grad(torch.zeros((2, 8)), ids, w, w[:1])
     with pytest.raises(TypeError):
         gg.rdot_router_topk_grad(None, ids, w, w, 0, torch.zeros((2, 8), dtype=torch.float16), stream=0)
+
+
+def test_raw_calls_refuse_two_element_sizes():
+    """The element size is taken from one tensor and used for the other."""
+    import torch
+    ids = torch.zeros((2, 2), dtype=torch.int32)
+    w = torch.zeros((2, 2))
+    with pytest.raises(TypeError):
+        gg.rdot_router_topk_grad(torch.zeros((2, 8), dtype=torch.bfloat16), ids, w, w, gg.RDOT_ROUTER_SOFTMAX,
+                                 torch.zeros((2, 8)), stream=0)
+    with pytest.raises(TypeError):
+        gg.rdot_moe_permute_grad(torch.zeros((4, 16)), ids.view(-1), torch.zeros((2, 16), dtype=torch.bfloat16), stream=0)
