@@ -164,11 +164,12 @@ def _ptr(t):
 
 def _stream(stream, device):
     """The cudaStream_t of a torch stream, a raw handle, or (None) the device's current stream. The last
-    is asked for as a raw handle: building a torch.cuda.Stream costs more than the library's own call."""
+    is asked for as a raw handle where a tensor's device is given: building a torch.cuda.Stream costs more than
+    the library's own call. Any other device (None: the current one) is torch.cuda.current_stream's to resolve."""
     if stream is None:
         import torch
         raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-        if raw is not None and device.type == "cuda" and device.index is not None:
+        if raw is not None and isinstance(device, torch.device) and device.type == "cuda" and device.index is not None:
             return raw(device.index)
         stream = torch.cuda.current_stream(device)
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
