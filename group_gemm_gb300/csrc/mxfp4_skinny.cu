@@ -297,8 +297,8 @@ __global__ void __launch_bounds__(THREADS, 1)
                 __syncwarp();
                 if (lane == 0 && last) mbar_arrive(&aempty[buf]);   // every lane's values are in registers
                 ok = mx4_wait_uniform(&full[stage], phase, guard);
+                tmem_st_wait();   // also on a stop: tensor memory is freed with no store of this warp in flight
                 if (!ok) break;
-                tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sfull[stage]);
