@@ -22,6 +22,7 @@
 // 64 tokens take 2 % longer with five than with eight.
 #include <cuda_bf16.h>
 
+#include "drain.cuh"
 #include "kernels.h"
 #include "mxfp4.cuh"
 #include "pdl.cuh"
@@ -197,13 +198,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 }
             }
         }
-        if (!ok && elected) {
-            // stopping early: let every load still in flight land before the CTA exits
-            int dummy;
-            const WaitGuard dguard = drain_guard(guard, &dummy);
-            for (int s = 0; s < STAGES; ++s)
-                if (issued_mask & (1u << s)) (void)mbar_wait(&full[s], (issued_phase >> s) & 1u, dguard);
-        }
+        if (elected) drain_loads<STAGES>(full, issued_mask, issued_phase, guard);
         __syncwarp();
     } else if (warp == 7) {
         // ------------------------------------------------------------------ token codes, weight scales
@@ -237,12 +232,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 }
             }
         }
-        if (!ok && elected) {   // as warp 0
-            int dummy;
-            const WaitGuard dguard = drain_guard(guard, &dummy);
-            for (int s = 0; s < STAGES; ++s)
-                if (issued_mask & (1u << s)) (void)mbar_wait(&xfull[s], (issued_phase >> s) & 1u, dguard);
-        }
+        if (elected) drain_loads<STAGES>(xfull, issued_mask, issued_phase, guard);
         __syncwarp();
     } else if (warp == 6) {
         // ------------------------------------------------------------------ token scale gather

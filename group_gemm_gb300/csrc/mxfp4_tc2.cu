@@ -28,6 +28,7 @@
 // 120 us, 4.5 TB/s of output).
 #include <cuda_bf16.h>
 
+#include "drain.cuh"
 #include "kernels.h"
 #include "mxfp4.cuh"
 #include "pairdrain.cuh"
@@ -251,13 +252,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                 }
             }
         }
-        if (!ok && elected) {
-            // stopping early: let every load still in flight land before the CTA exits
-            int dummy;
-            const WaitGuard dguard = drain_guard(guard, &dummy);
-            for (int s = 0; s < SFB_STAGES; ++s)
-                if (issued_mask & (1u << s)) (void)mbar_wait(&bfull[s], (issued_phase >> s) & 1u, dguard);
-        }
+        if (elected) drain_loads<SFB_STAGES>(bfull, issued_mask, issued_phase, guard);
         __syncwarp();
     } else if (warp == 3) {
         // ------------------------------------------------------------------ row scale gather (both CTAs)

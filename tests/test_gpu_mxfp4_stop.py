@@ -69,3 +69,22 @@ def test_a_stop_with_scale_stores_issued(limit):
         c.stopped()
         outs.append(c.call(c.whole).clone())
     c.check(outs)
+
+
+@pytest.mark.parametrize("limit", [1, 1_000])
+@pytest.mark.parametrize("variant,m,k,sizes", [("skinny", 48, 1024, [20, 0, 28, 0]),      # 4 of 8 stages
+                                               ("skinny", 48, 2048, [20, 0, 28, 0]),      # all 8
+                                               ("pair", 700, 1024, [300, 0, 400, 0]),     # 4 of 5, 4 of 10 scale stages
+                                               ("pair", 700, 2560, [300, 0, 400, 0])])    # more than 5, 10 of 10
+def test_a_stop_after_the_producers_have_finished(variant, m, k, sizes, limit):
+    """All of a CTA's loads fit its rings, so the producers end normally while the consumers give up: the
+    loads still land before the CTA leaves, not in the shared memory of the next call's CTA."""
+    c = Case(m, k, 512, sizes, variant, 2)
+    gg.rdot_set_wait_timeout(c.stopping.handle, limit)
+    cold = torch.empty(1 << 28, dtype=torch.uint8, device=DEV)      # twice the L2
+    outs = []
+    for _ in range(4):
+        cold.zero_()
+        c.stopped()
+        outs.append(c.call(c.whole).clone())
+    c.check(outs)
