@@ -26,6 +26,7 @@
 // or N columns past the tensor come back zero-filled from TMA.
 #include <cuda_bf16.h>
 
+#include "drain.cuh"
 #include "epilogue.cuh"
 #include "kernels.h"
 #include "pdl.cuh"
@@ -157,13 +158,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                     }
                 }
             }
-            if (!ok) {
-                // stopping early: let every load still in flight land before the CTA exits
-                int dummy;
-                const WaitGuard dguard = drain_guard(guard, &dummy);
-                for (int s = 0; s < STAGES; ++s)
-                    if (issued_mask & (1u << s)) (void)mbar_wait(&full[s], (issued_phase >> s) & 1u, dguard);
-            }
+            drain_loads<STAGES>(full, issued_mask, issued_phase, guard);
         }
         __syncwarp();
     } else if (warp == 1) {

@@ -26,6 +26,7 @@
 //                    warps 2..5 run the ragged bf16 epilogue.
 #include <cuda_bf16.h>
 
+#include "drain.cuh"
 #include "epilogue.cuh"
 #include "kernels.h"
 #include "pdl.cuh"
@@ -385,12 +386,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                     }
                 }
             }
-            if (!ok) {
-                int dummy;
-                const WaitGuard dguard = drain_guard(guard, &dummy);
-                for (int s = 0; s < STAGES; ++s)
-                    if (issued_mask & (1u << s)) (void)mbar_wait(&full[s], (issued_phase >> s) & 1u, dguard);
-            }
+            drain_loads<STAGES>(full, issued_mask, issued_phase, guard);
         }
         __syncwarp();
     } else if (warp == 1) {

@@ -35,6 +35,7 @@
 //                    group's slab is written as zeros.
 //   mxw_tc_wide_kernel  the same on 128 x 256 tiles for a bf16 dw (below).
 // Every 128-row stage and every block above is the same for both tile widths.
+#include "drain.cuh"
 #include "epilogue.cuh"
 #include "kernels.h"
 #include "pdl.cuh"
@@ -254,13 +255,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                     }
                 }
             }
-            if (!ok) {
-                // stopping early: let every load still in flight land before the CTA exits
-                int dummy;
-                const WaitGuard dguard = drain_guard(guard, &dummy);
-                for (int s = 0; s < STAGES; ++s)
-                    if (issued_mask & (1u << s)) (void)mbar_wait(&full[s], (issued_phase >> s) & 1u, dguard);
-            }
+            drain_loads<STAGES>(full, issued_mask, issued_phase, guard);
         }
         __syncwarp();
     } else if (warp == 1) {
@@ -541,12 +536,7 @@ __global__ void __launch_bounds__(wide::THREADS, 1)
                     }
                 }
             }
-            if (!ok) {
-                int dummy;
-                const WaitGuard dguard = drain_guard(guard, &dummy);
-                for (int s = 0; s < STAGES; ++s)
-                    if (issued_mask & (1u << s)) (void)mbar_wait(&full[s], (issued_phase >> s) & 1u, dguard);
-            }
+            drain_loads<STAGES>(full, issued_mask, issued_phase, guard);
         }
         __syncwarp();
     } else if (warp == 1) {

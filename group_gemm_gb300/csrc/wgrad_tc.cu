@@ -15,6 +15,7 @@
 // both operands and NaN/Inf there cannot leak through 0 * x; only the K=16 steps that hold group
 // rows are issued. Roles: warp 0 TMA, warp 1 MMA, warps 2..5 epilogue; two TMEM accumulators let
 // the epilogue of one tile overlap the next tile's mainloop.
+#include "drain.cuh"
 #include "epilogue.cuh"
 #include "kernels.h"
 #include "pdl.cuh"
@@ -186,12 +187,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                     }
                 }
             }
-            if (!ok) {
-                int dummy;
-                const WaitGuard dguard = drain_guard(guard, &dummy);
-                for (int s = 0; s < STAGES; ++s)
-                    if (issued_mask & (1u << s)) (void)mbar_wait(&full[s], (issued_phase >> s) & 1u, dguard);
-            }
+            drain_loads<STAGES>(full, issued_mask, issued_phase, guard);
         }
         __syncwarp();
     } else if (warp == 1) {
