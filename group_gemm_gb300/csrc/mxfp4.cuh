@@ -87,14 +87,10 @@ __device__ __forceinline__ int mx4_group_scan(const int32_t* __restrict__ group_
 
 // mbar_wait (ptx.cuh) that looks at the clock only after MX4_TRIES waits, where mbar_wait reads the global
 // timer before its second look (16384 rows x 4096 -> 14336: 304 against 320 us; one token 15.0 against 15.7).
-// A wait whose limit is shorter than a drain's goes to mbar_wait at once: the waits ahead of the clock
-// would let the limit pass unnoticed, with a limit of a nanosecond as long as the data arrive within them.
 constexpr int MX4_TRIES = 32;
 
-__device__ __forceinline__ int mx4_tries(const WaitGuard& g) { return g.timeout_ns >= kDrainTimeoutNs ? MX4_TRIES : 0; }
-
 __device__ __forceinline__ bool mx4_wait(uint64_t* bar, uint32_t parity, const WaitGuard& g) {
-    for (int i = mx4_tries(g); i > 0; --i)
+    for (int i = 0; i < MX4_TRIES; ++i)
         if (mbar_try_wait(bar, parity)) return true;
     return mbar_wait(bar, parity, g);
 }
@@ -110,7 +106,7 @@ __device__ __forceinline__ bool mx4_wait_warp(uint64_t* bar, uint32_t parity, co
 // registers. (In a lane-0 branch each MMA took about 100 clocks to issue, more than it takes to run with
 // N = 64; see mxfp4_tc2.cu.)
 __device__ __forceinline__ bool mx4_wait_uniform(uint64_t* bar, uint32_t parity, const WaitGuard& g) {
-    for (int i = mx4_tries(g); i > 0; --i)
+    for (int i = 0; i < MX4_TRIES; ++i)
         if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
     return __all_sync(0xffffffffu, mbar_wait(bar, parity, g)) != 0;
 }
