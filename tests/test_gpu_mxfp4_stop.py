@@ -88,3 +88,19 @@ def test_a_stop_after_the_producers_have_finished(variant, m, k, sizes, limit):
         c.stopped()
         outs.append(c.call(c.whole).clone())
     c.check(outs)
+
+
+@pytest.mark.parametrize("variant,m,k,sizes", [("skinny", 48, 8192, [20, 0, 28, 0]), ("pair", 700, 8192, [300, 0, 400, 0])])
+def test_a_short_limit_takes_effect(variant, m, k, sizes):
+    """A nanosecond runs out in every call (the first loads alone take longer) and is reported; the limit's
+    default then gives the output of before."""
+    c = Case(m, k, 512, sizes, variant, 3)
+    gg.rdot_set_wait_timeout(c.stopping.handle, 1)
+    for _ in range(4):
+        c.stopping.clear_status()
+        c.call(c.stopping)
+        assert c.stopping.status() == gg.RDOT_STATUS_BIT_TIMEOUT
+    gg.rdot_set_wait_timeout(c.stopping.handle, 0)
+    c.stopping.clear_status()
+    c.out.fill_(float("nan"))
+    assert torch.equal(c.call(c.stopping), c.want) and c.stopping.status() == 0
