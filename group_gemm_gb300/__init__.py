@@ -483,6 +483,15 @@ def _torch_dtype_name(dt):
     return {torch.float32: "f32", torch.bfloat16: "bf16"}[dt]
 
 
+def _check_out(out, elements, dtype, device, what="out"):
+    """Refuses a caller's output that a kernel, which gets its pointer alone, would write past the end of or
+    with values of another type or order."""
+    if out.dtype != dtype:
+        raise TypeError(f"{what} must be {dtype}")
+    if out.numel() < elements or not out.is_contiguous() or out.device != device:
+        raise ValueError(f"{what} must be contiguous, of at least {elements} elements, on {device}")
+
+
 # The high-level calls below allocate what they return (and any scratch) on the stream their
 # kernels run on, so PyTorch's caching allocator never hands that memory to other work while
 # those kernels may still use it.
@@ -703,6 +712,10 @@ def ragged_dot_mxfp4(lhs_q, lhs_scale, rhs_q, rhs_scale, group_sizes, out=None, 
         raise ValueError("shape mismatch between lhs, rhs, their scales and group_sizes")
     if any(t.dtype != torch.uint8 for t in (lhs_q, lhs_scale, rhs_q, rhs_scale)):
         raise TypeError("codes and scales must be uint8")
+    if out is not None:
+        if out.shape != (m, n):
+            raise ValueError("out must be [M, N]")
+        _check_out(out, m * n, torch.bfloat16, lhs_q.device)
     s = _run_stream(stream, lhs_q.device)
     key = ("mxfp4", m, k, n, g, lhs_q.device)
     plan, ws = _cached_plan(key, s, m=m, k=k, n=n, groups=g, mode="forward_mxfp4", in_dtype="e2m1", out_dtype="bf16",
