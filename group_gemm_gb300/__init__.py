@@ -508,6 +508,8 @@ def ragged_dot(lhs, rhs, group_sizes, out_dtype=None, out=None, stream=None):
         raise ValueError("shape mismatch between lhs, rhs and group_sizes")
     in_dt = _torch_dtype_name(lhs.dtype)
     out_dtype = out_dtype or lhs.dtype
+    if out is not None:
+        _check_out(out, m * n, out_dtype, lhs.device)
     s = _run_stream(stream, lhs.device)
     key = ("fwd", m, k, n, g, in_dt, out_dtype, lhs.device)
     plan, ws = _cached_plan(key, s, m=m, k=k, n=n, groups=g, mode="forward", in_dtype=in_dt,
@@ -528,6 +530,8 @@ def grad_weight(lhs, dy, group_sizes, out_dtype=None, dw=None, stream=None):
     _, n = dy.shape
     g = group_sizes.shape[0]
     out_dtype = out_dtype or (dw.dtype if dw is not None else torch.float32)
+    if dw is not None:
+        _check_out(dw, g * k * n, out_dtype, lhs.device, "dw")
     names = {torch.bfloat16: "bf16", torch.float32: "f32"}
     s = _run_stream(stream, lhs.device)
     key = ("wgrad", m, k, n, g, out_dtype, lhs.device)
@@ -548,6 +552,8 @@ def grad_input(dy, rhs, group_sizes, out_dtype=None, dlhs=None, stream=None):
     m, n = dy.shape
     g, k, _ = rhs.shape
     out_dtype = out_dtype or dy.dtype
+    if dlhs is not None:
+        _check_out(dlhs, m * k, out_dtype, dy.device, "dlhs")
     names = {torch.bfloat16: "bf16", torch.float32: "f32"}
     s = _run_stream(stream, dy.device)
     key = ("dgrad", m, k, n, g, out_dtype, dy.device)
@@ -568,6 +574,8 @@ def ragged_dot_gated(lhs, w0, w1, group_sizes, out_dtype=None, out=None, stream=
     m, k = lhs.shape
     g, _, n = w0.shape
     out_dtype = out_dtype or lhs.dtype
+    if out is not None:
+        _check_out(out, m * n, out_dtype, lhs.device)
     names = {torch.bfloat16: "bf16", torch.float32: "f32"}
     s = _run_stream(stream, lhs.device)
     key = ("gated", m, k, n, g, out_dtype, lhs.device)
@@ -590,6 +598,8 @@ def grad_weight_mxfp8(lhs_q, lhs_s, dy_q, dy_s, group_sizes, out=None, stream=No
     n = dy_q.shape[1]
     g = group_sizes.shape[0]
     out_dtype = out_dtype or (out.dtype if out is not None else torch.float32)
+    if out is not None:
+        _check_out(out, g * k * n, out_dtype, lhs_q.device)
     names = {torch.bfloat16: "bf16", torch.float32: "f32"}
     s = _run_stream(stream, lhs_q.device)
     key = ("wgrad_mxfp8", m, k, n, g, out_dtype, lhs_q.device)
@@ -610,6 +620,8 @@ def ragged_dot_combine(lhs, rhs, group_sizes, order, topk_weights, out=None, str
     m, kdim = lhs.shape
     g, _, n = rhs.shape
     t, k = topk_weights.shape
+    if out is not None:
+        _check_out(out, t * n, torch.float32, lhs.device)
     s = _run_stream(stream, lhs.device)
     key = ("fwd", m, kdim, n, g, "bf16", torch.float32, lhs.device)     # the fp32-out forward's plan
     plan, ws = _cached_plan(key, s, m=m, k=kdim, n=n, groups=g, mode="forward", in_dtype="bf16", out_dtype="f32",
@@ -659,6 +671,8 @@ def moe_unpermute(y_sorted, inv, topk_weights, out=None, stream=None):
     """``out[t] = sum_j w[t, j] * y_sorted[inv[t*k + j]]`` (bf16 [T, N])."""
     import torch
     t, _ = topk_weights.shape
+    if out is not None:
+        _check_out(out, t * y_sorted.shape[1], torch.bfloat16, y_sorted.device)
     s = _run_stream(stream, y_sorted.device)
     with torch.cuda.stream(s):
         if out is None:
@@ -781,6 +795,8 @@ def ragged_dot_mxfp8(lhs_q, lhs_scale, rhs_q, rhs_scale, group_sizes, out=None, 
     import torch
     m, k = lhs_q.shape
     g, _, n = rhs_q.shape
+    if out is not None:
+        _check_out(out, m * n, torch.bfloat16, lhs_q.device)
     s = _run_stream(stream, lhs_q.device)
     key = ("mxfp8", m, k, n, g, lhs_q.device)
     plan, ws = _cached_plan(key, s, m=m, k=k, n=n, groups=g, mode="forward_mxfp8", in_dtype="e4m3", out_dtype="bf16",
@@ -799,6 +815,8 @@ def padded_ragged_dot(lhs, rhs, group_sizes, capacity, out=None, pad_workspace=N
     import torch
     m, k = lhs.shape
     g, _, n = rhs.shape
+    if out is not None:
+        _check_out(out, m * n, torch.bfloat16, lhs.device)
     s = _run_stream(stream, lhs.device)
     key = ("fwd", m, k, n, g, "bf16", torch.bfloat16, lhs.device)
     plan, ws = _cached_plan(key, s, m=m, k=k, n=n, groups=g, mode="forward", in_dtype="bf16", out_dtype="bf16",

@@ -59,3 +59,47 @@ def test_mxfp4_forward_refuses_outputs_it_cannot_fill():
                                                         (torch.empty((m + 1, n), dtype=torch.bfloat16), ValueError)]:
         with pytest.raises(error, match="out must be"):
             gg.ragged_dot_mxfp4(*args, out=out)
+
+
+def older_calls():
+    m, k, n, g, t = 8, 64, 64, 2, 4
+    bf = lambda *shape: torch.zeros(shape, dtype=torch.bfloat16)
+    u8 = lambda *shape: torch.zeros(shape, dtype=torch.uint8)
+    gs, order, w = torch.zeros(g, dtype=torch.int32), torch.zeros(m, dtype=torch.int32), torch.zeros((t, 2))
+    bf16, f32 = torch.bfloat16, torch.float32
+    x, y, r = bf(m, k), bf(m, n), bf(g, k, n)
+    return {
+        "ragged_dot": (lambda out: gg.ragged_dot(x, r, gs, out=out), (m, n), bf16),
+        "ragged_dot, fp32 out": (lambda out: gg.ragged_dot(x, r, gs, out_dtype=f32, out=out), (m, n), f32),
+        "grad_weight": (lambda out: gg.grad_weight(x, y, gs, out_dtype=f32, dw=out), (g * k, n), f32),
+        "grad_input": (lambda out: gg.grad_input(y, r, gs, dlhs=out), (m, k), bf16),
+        "ragged_dot_gated": (lambda out: gg.ragged_dot_gated(x, r, r, gs, out=out), (m, n), bf16),
+        "grad_weight_mxfp8": (lambda out: gg.grad_weight_mxfp8(u8(m, k), u8(g, k), u8(m, n), u8(g, n), gs, out=out,
+                                                               out_dtype=f32), (g * k, n), f32),
+        "ragged_dot_combine": (lambda out: gg.ragged_dot_combine(x, r, gs, order, w, out=out), (t, n), f32),
+        "moe_unpermute": (lambda out: gg.moe_unpermute(y, order, w, out=out), (t, n), bf16),
+        "ragged_dot_mxfp8": (lambda out: gg.ragged_dot_mxfp8(u8(m, k), u8(m, 2), u8(g, k, n), u8(g, 2, n), gs, out=out),
+                             (m, n), bf16),
+        "padded_ragged_dot": (lambda out: gg.padded_ragged_dot(x, r, gs, 128, out=out), (m, n), bf16),
+    }
+
+
+@pytest.mark.parametrize("name", list(older_calls()))
+def test_calls_refuse_outputs_they_cannot_fill(name, monkeypatch):
+    """A larger or reshaped contiguous output still does; the call then goes on to its stream."""
+    call, (rows, cols), dtype = older_calls()[name]
+    for out, error in bad_outs(rows, cols, dtype):
+        with pytest.raises(error, match="must be"):
+            call(out)
+
+    class Reached(Exception):
+        pass
+
+    def run_stream(stream, device):
+        raise Reached
+
+    monkeypatch.setattr(gg, "_run_stream", run_stream)
+    for out in (None, torch.empty((rows, cols), dtype=dtype), torch.empty((rows + 3, cols), dtype=dtype),
+                torch.empty(rows * cols, dtype=dtype)):
+        with pytest.raises(Reached):
+            call(out)
