@@ -492,6 +492,12 @@ def _check_out(out, elements, dtype, device, what="out"):
         raise ValueError(f"{what} must be contiguous, of at least {elements} elements, on {device}")
 
 
+def _same_device(*tensors):
+    """Refuses tensors of several devices: a kernel would follow a pointer that is not its device's."""
+    if any(t.device != tensors[0].device for t in tensors):
+        raise ValueError("all tensors must be on one device")
+
+
 # The high-level calls below allocate what they return (and any scratch) on the stream their
 # kernels run on, so PyTorch's caching allocator never hands that memory to other work while
 # those kernels may still use it.
@@ -726,6 +732,7 @@ def ragged_dot_mxfp4(lhs_q, lhs_scale, rhs_q, rhs_scale, group_sizes, out=None, 
         raise ValueError("shape mismatch between lhs, rhs, their scales and group_sizes")
     if any(t.dtype != torch.uint8 for t in (lhs_q, lhs_scale, rhs_q, rhs_scale)):
         raise TypeError("codes and scales must be uint8")
+    _same_device(lhs_q, lhs_scale, rhs_q, rhs_scale, group_sizes)
     if out is not None:
         if out.shape != (m, n):
             raise ValueError("out must be [M, N]")
@@ -752,6 +759,7 @@ def moe_unpermute_grad(dout, y_sorted, order, inv, topk_weights, stream=None):
         raise TypeError("dout and y_sorted must be bfloat16")
     if dout.shape != (t, y_sorted.shape[1]) or y_sorted.shape[0] != t * k or order.numel() != t * k or inv.numel() != t * k:
         raise ValueError("shape mismatch between dout, y_sorted, order, inv and topk_weights")
+    _same_device(dout, y_sorted, order, inv, topk_weights)
     s = _run_stream(stream, dout.device)
     with torch.cuda.stream(s):
         dy = torch.empty_like(y_sorted, memory_format=torch.contiguous_format)
@@ -767,6 +775,7 @@ def moe_permute_grad(dx_sorted, inv, k, stream=None):
     import torch
     if k < 1 or dx_sorted.dim() != 2 or dx_sorted.shape[0] % k or inv.numel() != dx_sorted.shape[0]:
         raise ValueError("dx_sorted must have T*k rows and inv T*k elements")
+    _same_device(dx_sorted, inv)
     s = _run_stream(stream, dx_sorted.device)
     with torch.cuda.stream(s):
         dx = torch.empty((dx_sorted.shape[0] // k, dx_sorted.shape[1]), dtype=dx_sorted.dtype, device=dx_sorted.device)
@@ -781,6 +790,7 @@ def router_topk_grad(logits, topk_ids, topk_weights, dweights, weights="softmax_
     t, _ = logits.shape
     if topk_ids.shape != topk_weights.shape or topk_ids.shape != dweights.shape or topk_ids.shape[0] != t:
         raise ValueError("topk_ids, topk_weights and dweights must all be [T, k]")
+    _same_device(logits, topk_ids, topk_weights, dweights)
     s = _run_stream(stream, logits.device)
     with torch.cuda.stream(s):
         dlogits = torch.empty_like(logits, memory_format=torch.contiguous_format)

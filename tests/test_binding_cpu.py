@@ -103,3 +103,27 @@ def test_calls_refuse_outputs_they_cannot_fill(name, monkeypatch):
                 torch.empty(rows * cols, dtype=dtype)):
         with pytest.raises(Reached):
             call(out)
+
+
+def two_device_calls():
+    """Calls of the MXFP4 product and the routing gradients, and their operands."""
+    m, k, n, g, t = 4, 64, 64, 2, 2
+    u8 = lambda *shape: torch.zeros(shape, dtype=torch.uint8)
+    bf = lambda *shape: torch.zeros(shape, dtype=torch.bfloat16)
+    i32 = lambda *shape: torch.zeros(shape, dtype=torch.int32)
+    return {
+        "ragged_dot_mxfp4": (gg.ragged_dot_mxfp4, [u8(m, k // 2), u8(m, k // 32), u8(g, n, k // 2), u8(g, 1, 1, 512),
+                                                   i32(g)]),
+        "moe_unpermute_grad": (gg.moe_unpermute_grad, [bf(t, n), bf(m, n), i32(m), i32(m), torch.zeros((t, 2))]),
+        "moe_permute_grad": (lambda dxs, inv: gg.moe_permute_grad(dxs, inv, 2), [bf(m, n), i32(m)]),
+        "router_topk_grad": (gg.router_topk_grad, [torch.zeros((t, 8)), i32(t, 2), torch.zeros((t, 2)),
+                                                   torch.zeros((t, 2))]),
+    }
+
+
+@pytest.mark.parametrize("name", list(two_device_calls()))
+def test_calls_refuse_tensors_of_two_devices(name):
+    call, args = two_device_calls()[name]
+    for i in range(len(args)):
+        with pytest.raises(ValueError, match="one device"):
+            call(*[a.to("meta") if j == i else a for j, a in enumerate(args)])
