@@ -1419,7 +1419,8 @@ rdot_status rdot_mxfp4_weight_scale_bytes(int32_t groups, int64_t k, int64_t n, 
 rdot_status rdot_quantize_mxfp4_weight(const void* w, int32_t dtype, int32_t groups, int64_t k, int64_t n,
                                        uint8_t* codes, uint8_t* scales, void* values, void* stream) {
     if (groups < 1 || k < 1 || n < 1 || (dtype != RDOT_F32 && dtype != RDOT_BF16)) return RDOT_ERR_INVALID_ARG;
-    if (groups > RDOT_MAX_GROUPS || k % 32 || n % 8 || k > 0x7fffffffLL || n > 0x7fffffffLL ||
+    // the kernel counts 128-column atoms as (n + 127) / 128 in 32 bits
+    if (groups > RDOT_MAX_GROUPS || k % 32 || n % 8 || k > 0x7fffffffLL || n > 0x7fffffffLL - 127 ||
         2 * ((n + 127) / 128) * ((k + 127) / 128) > 0x7fffffffLL / groups)
         return RDOT_ERR_UNSUPPORTED;
     if (!w || !codes || !scales) return RDOT_ERR_INVALID_ARG;

@@ -215,7 +215,8 @@ RDOT_API rdot_status rdot_quantize_mxfp4(const void* x, int32_t dtype, int64_t r
  *           columns x 4 scale blocks, the scale of column n and block b at byte
  *           16 (n % 32) + 4 ((n / 32) % 4) + b % 4 of atom (n / 128, b / 4); zeros past N and K/32
  *   values  device bf16 [G, K, N] out, or null
- * K % 32 == 0, N % 8 == 0, G <= RDOT_MAX_GROUPS, else RDOT_ERR_UNSUPPORTED; 16-byte alignment for all.
+ * K % 32 == 0, N % 8 == 0 and N <= 2^31 - 128, G <= RDOT_MAX_GROUPS, else RDOT_ERR_UNSUPPORTED; 16-byte
+ * alignment for all.
  * rdot_mxfp4_weight_scale_bytes gives the size of `scales`. */
 RDOT_API rdot_status rdot_mxfp4_weight_scale_bytes(int32_t groups, int64_t k, int64_t n, size_t* bytes);
 RDOT_API rdot_status rdot_quantize_mxfp4_weight(const void* w, int32_t dtype, int32_t groups, int64_t k, int64_t n,
