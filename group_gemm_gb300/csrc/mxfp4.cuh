@@ -87,6 +87,7 @@ __device__ __forceinline__ int mx4_group_scan(const int32_t* __restrict__ group_
 
 // mbar_wait (ptx.cuh) that looks at the clock only after MX4_TRIES waits, where mbar_wait reads the global
 // timer before its second look (16384 rows x 4096 -> 14336: 304 against 320 us; one token 15.0 against 15.7).
+// A caller's wait limit counts from there: a nanosecond still stops every call (8 of 8 at K = 256 to 8192).
 constexpr int MX4_TRIES = 32;
 
 __device__ __forceinline__ bool mx4_wait(uint64_t* bar, uint32_t parity, const WaitGuard& g) {
@@ -140,7 +141,8 @@ constexpr int MX4_GROUP_BYTES = MX4_GROUP * 2 * MX4_ATOM_BYTES;   // atoms of a 
 
 // R rows a lane: first, first + 32, ... of a tile of `rows` rows at row0 (rows past it read as 0). The paths
 // by width are kept apart, each with all its loads ahead of their uses: merged into one, every load was
-// waited for (65536 rows x 256 -> 1024: 67 against 36 us).
+// waited for (65536 rows x 256 -> 1024: 67 against 36 us). Reading single bytes is the slow one: a load a byte,
+// one stage in flight (65536 rows x 96 -> 1024: 55 us for 20 us of bytes; see also mxfp4_tc2.cu).
 template <int R>
 __device__ __forceinline__ void load_scale_group(const Mx4Args& a, int row0, int rows, int first, int ks0,
                                                  uint2 (&v)[R][MX4_GROUP]) {

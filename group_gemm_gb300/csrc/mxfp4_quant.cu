@@ -8,8 +8,9 @@
 // The optional values, code x scale, are bf16 without rounding: two significant bits and exponents
 // from -128 to 127 fit it (its subnormals reach 2^-133).
 //
-// Both kernels are HBM-bound streams: each element is read once. Rows: 16384 x 4096 bf16 with values in
-// 47.1 us (6.5 TB/s), codes alone in 28.6 us.
+// Both kernels are one-pass streams: each element is read once. HBM bounds rows (16384 x 4096 bf16 with
+// values 47.1 us, 6.5 TB/s, codes alone 28.6 us) and fp32 weights; bf16 weights stay below it (figures at
+// the kernel).
 #include <cuda_bf16.h>
 
 #include "kernels.h"
@@ -87,8 +88,10 @@ __device__ __forceinline__ void load_vec8(const uint4* __restrict__ x, long long
 }
 
 // CHUNKS: a block takes QR_UNROLL * 256 consecutive vectors a pass, so that its loads and stores share DRAM
-// pages (16384 x 4096 bf16: 53.9 against 55.7 us); without, they are spread over the grid, so that more
-// blocks share a small input (37 x 1408 fp32: 1.3 against 2.3 us).
+// pages (16384 x 4096 bf16 with values: 47.1 against 48.6 us, codes alone 28.6 / 30.2); without, they are spread over
+// the grid, so that more blocks share a small input (37 x 1408 fp32: 1.3 against 2.3 us). The launch takes
+// chunks where they fill the grid, from 4864 rows of 4096: there 16.1 against 15.7 us, at 5500 rows 17.3 / 17.7.
+// They also win below that (2432 rows 9.4 / 9.7, 1216 rows 5.9 / 6.4), so the border could lie lower.
 template <bool BF16, bool VALUES, bool CHUNKS>
 __global__ void __launch_bounds__(256) quantize_rows_kernel(const uint4* __restrict__ x, long long vecs,
                                                             uint32_t* __restrict__ codes,
@@ -140,7 +143,10 @@ __global__ void __launch_bounds__(256) quantize_rows_kernel(const uint4* __restr
 // column lies in one thread's registers (all 32 loads in flight); the codes are turned through shared
 // memory into rows of up to 64 bytes, the scales into one atom's words. Four such blocks share an SM and
 // so load, compute and store at different times: 456 us (6.7 TB/s) for 8 x 4096 x 14336 fp32 with
-// values, against 568 us for two blocks of 8 warps, 642 us for one of 16, and 599 us for five of 4 (spills).
+// values, against 568 us for two blocks of 8 warps, 642 us for one of 16, and 599 us for five of 4. With values
+// the kernel uses the 128 registers that four blocks leave and spills 52 bytes a thread (bf16: 48); five
+// blocks leave 96 and spill 240. Codes alone (no spills): fp32 304 us, bf16 209 (floor 175). bf16 with values
+// is the form farthest from its floor: 499 us against 313; a lane loads 4 bytes there, half the bytes in flight.
 constexpr int QW_COLS = 64;
 constexpr int QW_BLOCKS = 4;    // scale blocks (32 rows each) per thread block
 constexpr int QW_THREADS = 32 * QW_BLOCKS;

@@ -61,7 +61,7 @@ typedef enum {
     RDOT_MODE_FORWARD_GATED = 4, /* out[M,N] = silu(lhs @ w0[g(i)]) * (lhs @ w1[g(i)]) (gated up projection) */
     RDOT_MODE_GRAD_INPUT_MXFP8 = 5, /* the data gradient on MXFP8 operands (scales along N) */
     RDOT_MODE_GRAD_WEIGHT_MXFP8 = 6, /* the weight gradient on MXFP8 operands (scales along the rows) */
-    RDOT_MODE_FORWARD_MXFP4 = 8  /* forward with E2M1 operands and E8M0 scales per 32 K elements */
+    RDOT_MODE_FORWARD_MXFP4 = 8  /* forward with E2M1 operands and E8M0 scales per 32 K elements (7: no mode) */
 } rdot_mode;
 
 /* Bits of the device status word (int32 at offset 0 of the workspace). */
