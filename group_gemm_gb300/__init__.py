@@ -31,7 +31,10 @@ __all__ = [
     "rdot_moe_unpermute_grad", "rdot_moe_permute_grad", "rdot_router_topk_grad",
     "rdot_quantize_mxfp4", "rdot_quantize_mxfp4_weight", "rdot_mxfp4_weight_scale_bytes", "rdot_forward_mxfp4",
     "quantize_mxfp4", "quantize_mxfp4_weight", "ragged_dot_mxfp4",
-    "moe_unpermute_grad", "moe_permute_grad", "router_topk_grad", "EXPORTED_SYMBOLS",
+    "moe_unpermute_grad", "moe_permute_grad", "router_topk_grad",
+    "rdot_quantize_mxfp8", "rdot_dequantize_mxfp8", "rdot_lora_group", "rdot_lora_forward", "rdot_lora_grad_input",
+    "rdot_lora_grad_weight", "quantize_mxfp8", "dequantize_mxfp8", "lora_group", "lora_forward", "lora_grad_input",
+    "lora_grad_weight", "EXPORTED_SYMBOLS",
 ]
 
 RDOT_OK, RDOT_ERR_INVALID_ARG, RDOT_ERR_UNSUPPORTED, RDOT_ERR_CUDA = 0, 1, 2, 3
@@ -46,6 +49,7 @@ RDOT_FLAG_CTA_PAIR, RDOT_FLAG_NO_CTA_PAIR, RDOT_FLAG_NATURAL_ORDER = 0x4, 0x8, 0
 RDOT_FLAG_SKINNY, RDOT_FLAG_NO_SKINNY = 0x20, 0x40
 RDOT_MAX_GROUPS = 1024
 RDOT_ROUTER_VALUES, RDOT_ROUTER_SOFTMAX, RDOT_ROUTER_SOFTMAX_TOPK, RDOT_ROUTER_MAX_TOPK = 0, 1, 2, 32
+RDOT_LORA_MAX_RANK = 128
 _ROUTER_MODES = {"values": RDOT_ROUTER_VALUES, "softmax": RDOT_ROUTER_SOFTMAX, "softmax_topk": RDOT_ROUTER_SOFTMAX_TOPK}
 
 # every function include/rdot.h declares
@@ -59,6 +63,8 @@ EXPORTED_SYMBOLS = (
     "rdot_forward_combine", "rdot_grad_weight_mxfp8",
     "rdot_moe_unpermute_grad", "rdot_moe_permute_grad", "rdot_router_topk_grad",
     "rdot_quantize_mxfp4", "rdot_quantize_mxfp4_weight", "rdot_mxfp4_weight_scale_bytes", "rdot_forward_mxfp4",
+    "rdot_quantize_mxfp8", "rdot_dequantize_mxfp8", "rdot_lora_group", "rdot_lora_forward", "rdot_lora_grad_input",
+    "rdot_lora_grad_weight",
 )
 
 _DTYPE_CODES = {"f32": RDOT_F32, "bf16": RDOT_BF16, "e4m3": RDOT_E4M3, "e2m1": RDOT_E2M1}
@@ -143,6 +149,13 @@ def load():
             "rdot_moe_unpermute_grad": ([vp, vp, vp, vp, vp, i64, ctypes.c_int32, i64, vp, vp, vp], st),
             "rdot_moe_permute_grad": ([vp, ctypes.c_int32, vp, i64, ctypes.c_int32, i64, vp, vp], st),
             "rdot_router_topk_grad": ([vp, ctypes.c_int32, vp, vp, vp, i64, ctypes.c_int32, ctypes.c_int32,
+                                       ctypes.c_int32, vp, vp], st),
+            "rdot_quantize_mxfp8": ([vp, ctypes.c_int32, i64, i64, vp, vp, vp], st),
+            "rdot_dequantize_mxfp8": ([vp, vp, i64, i64, ctypes.c_int32, vp, vp], st),
+            "rdot_lora_group": ([vp, i64, ctypes.c_int32, vp, vp, vp], st),
+            "rdot_lora_forward": ([vp] * 7 + [i64, i64, i64, ctypes.c_int32, ctypes.c_int32, vp, vp, vp], st),
+            "rdot_lora_grad_input": ([vp] * 7 + [i64, i64, i64, ctypes.c_int32, ctypes.c_int32, vp, vp, vp], st),
+            "rdot_lora_grad_weight": ([vp, vp, ctypes.c_int32, vp, vp, vp, i64, i64, ctypes.c_int32, ctypes.c_int32,
                                        ctypes.c_int32, vp, vp], st),
         }
         for name, (args, res) in sig.items():
@@ -334,6 +347,52 @@ def rdot_router_topk_grad(logits, topk_ids, topk_weights, dweights, weights_mode
                                         _ptr(topk_weights), _ptr(dweights), int(t), int(e), int(topk_ids.shape[1]),
                                         int(weights_mode), _ptr(dlogits), _stream(stream, dlogits.device)),
            "rdot_router_topk_grad")
+
+
+def rdot_quantize_mxfp8(x, codes, scales, stream=None) -> None:
+    """x [rows, K] (fp32 or bf16) -> codes uint8 [rows, K], scales uint8 [rows, K/32]."""
+    _check(load().rdot_quantize_mxfp8(_ptr(x), _float_dtype(x, "x"), int(x.shape[0]), int(x.shape[1]), _ptr(codes),
+                                      _ptr(scales), _stream(stream, x.device)), "rdot_quantize_mxfp8")
+
+
+def rdot_dequantize_mxfp8(codes, scales, out, stream=None) -> None:
+    """codes uint8 [rows, K], scales uint8 [rows, K/32] -> out [rows, K] (fp32 or bf16)."""
+    _check(load().rdot_dequantize_mxfp8(_ptr(codes), _ptr(scales), int(out.shape[0]), int(out.shape[1]),
+                                        _float_dtype(out, "out"), _ptr(out), _stream(stream, out.device)),
+           "rdot_dequantize_mxfp8")
+
+
+def rdot_lora_group(ids, groups: int, group_sizes, order, stream=None) -> None:
+    """ids int32 [M] -> group_sizes int32 [groups], order int32 [M]."""
+    _check(load().rdot_lora_group(_ptr(ids), int(ids.shape[0]), int(groups), _ptr(group_sizes), _ptr(order),
+                                  _stream(stream, group_sizes.device)), "rdot_lora_group")
+
+
+def _lora_apply(name, x, down, up, group_sizes, order, scale, base, out, t, stream):
+    g, r, k = down.shape
+    _check(getattr(load(), name)(_ptr(x), _ptr(down), _ptr(up), _ptr(group_sizes), _ptr(order), _ptr(scale), _ptr(base),
+                                 int(x.shape[0]), k, int(up.shape[2]), g, r, _ptr(out), _ptr(t),
+                                 _stream(stream, out.device)), name)
+
+
+def rdot_lora_forward(x, down, up, group_sizes, out, t=None, order=None, scale=None, base=None, stream=None) -> None:
+    """x bf16 [M, K], down bf16 [G, r, K], up bf16 [G, r, N], base bf16 [M, N] -> out bf16 [M, N], t bf16 [M, r]."""
+    _lora_apply("rdot_lora_forward", x, down, up, group_sizes, order, scale, base, out, t, stream)
+
+
+def rdot_lora_grad_input(dy, down, up, group_sizes, dx, dt=None, order=None, scale=None, base=None, stream=None) -> None:
+    """dy bf16 [M, N], down bf16 [G, r, K], up bf16 [G, r, N], base bf16 [M, K] -> dx bf16 [M, K], dt bf16 [M, r]."""
+    _lora_apply("rdot_lora_grad_input", dy, down, up, group_sizes, order, scale, base, dx, dt, stream)
+
+
+def rdot_lora_grad_weight(t, z, group_sizes, dw, order=None, z_scale=None, stream=None) -> None:
+    """t bf16 [M, r], z bf16 [M, width] (or E4M3 codes uint8 with z_scale uint8 [M, width/32]) -> dw [G, r, width]
+    (fp32 or bf16)."""
+    g, r, width = dw.shape
+    _check(load().rdot_lora_grad_weight(_ptr(t), _ptr(z), RDOT_BF16 if z_scale is None else RDOT_E4M3, _ptr(z_scale),
+                                        _ptr(group_sizes), _ptr(order), int(t.shape[0]), width, g, r,
+                                        _float_dtype(dw, "dw"), _ptr(dw), _stream(stream, dw.device)),
+           "rdot_lora_grad_weight")
 
 
 def rdot_padded_workspace_size(plan, capacity: int) -> int:
@@ -798,6 +857,126 @@ def router_topk_grad(logits, topk_ids, topk_weights, dweights, weights="softmax_
                               topk_weights.to(torch.float32).contiguous(), dweights.to(torch.float32).contiguous(),
                               _ROUTER_MODES[weights], dlogits, s)
     return dlogits
+
+
+def quantize_mxfp8(x, stream=None):
+    """MXFP8 quantisation of x [rows, K] (fp32 or bf16) in blocks of 32 along K, for an 8-bit checkpoint of an
+    activation or an MXFP8 product: returns ``(codes uint8 [rows, K], scales uint8 [rows, K/32])``."""
+    import torch
+    if x.dim() != 2:
+        raise ValueError("x must be [rows, K]")
+    m, k = x.shape
+    s = _run_stream(stream, x.device)
+    with torch.cuda.stream(s):
+        codes = torch.empty((m, k), dtype=torch.uint8, device=x.device)
+        scales = torch.empty((m, k // 32), dtype=torch.uint8, device=x.device)
+        rdot_quantize_mxfp8(x.contiguous(), codes, scales, s)
+    return codes, scales
+
+
+def dequantize_mxfp8(codes, scales, dtype=None, stream=None):
+    """The values [rows, K] (bf16, or ``dtype`` fp32) that :func:`quantize_mxfp8`'s codes and scales stand for."""
+    import torch
+    if codes.dim() != 2 or scales.shape != (codes.shape[0], codes.shape[1] // 32):
+        raise ValueError("codes must be [rows, K] and scales [rows, K/32]")
+    if codes.dtype != torch.uint8 or scales.dtype != torch.uint8:
+        raise TypeError("codes and scales must be uint8")
+    _same_device(codes, scales)
+    s = _run_stream(stream, codes.device)
+    with torch.cuda.stream(s):
+        out = torch.empty(codes.shape, dtype=dtype or torch.bfloat16, device=codes.device)
+        rdot_dequantize_mxfp8(codes.contiguous(), scales.contiguous(), out, s)
+    return out
+
+
+def lora_group(ids, n_adapters, stream=None):
+    """Sorts a batch's rows by adapter for the calls below: returns ``(group_sizes int32 [n_adapters], order
+    int32 [M])`` for ids int [M] (outside [0, n_adapters): no adapter, sorted last)."""
+    import torch
+    if ids.dim() != 1:
+        raise ValueError("ids must be [M]")
+    s = _run_stream(stream, ids.device)
+    with torch.cuda.stream(s):
+        if ids.dtype != torch.int32:     # an id past 32 bits stays outside the range
+            ids = ids.clamp(-1, 2 ** 31 - 1).to(torch.int32)
+        sizes = torch.empty(n_adapters, dtype=torch.int32, device=ids.device)
+        order = torch.empty(ids.shape[0], dtype=torch.int32, device=ids.device)
+        rdot_lora_group(ids.contiguous(), n_adapters, sizes, order, s)
+    return sizes, order
+
+
+def _lora(call, x, first, second, down, up, group_sizes, order, scale, base, out, stream):
+    import torch
+    if down.dim() != 3 or up.dim() != 3 or down.shape[:2] != up.shape[:2] or x.dim() != 2:
+        raise ValueError("down and up must be [G, r, K] and [G, r, N], the rows [M, width]")
+    m, g, r, width = x.shape[0], down.shape[0], down.shape[1], second.shape[2]
+    if (x.shape[1] != first.shape[2] or group_sizes.shape != (g,) or (order is not None and order.shape != (m,))
+            or (scale is not None and scale.shape != (g,)) or (base is not None and base.shape != (m, width))):
+        raise ValueError("shape mismatch between the rows, down, up, group_sizes, order, scale and base")
+    if any(v.dtype != torch.bfloat16 for v in (x, down, up, *(() if base is None else (base,)))):
+        raise TypeError("the rows, down, up and base must be bfloat16")
+    _same_device(x, down, up, group_sizes, *(v for v in (order, scale, base) if v is not None))
+    if out is not None:
+        if out.shape != (m, width):
+            raise ValueError("the output must be [M, width]")
+        _check_out(out, m * width, torch.bfloat16, x.device)
+    s = _run_stream(stream, x.device)
+    with torch.cuda.stream(s):
+        if out is None:
+            out = torch.empty((m, width), dtype=torch.bfloat16, device=x.device)
+        t = torch.empty((m, r), dtype=torch.bfloat16, device=x.device)
+        call(x.contiguous(), down.contiguous(), up.contiguous(), group_sizes.to(torch.int32).contiguous(), out, t,
+             order=None if order is None else order.to(torch.int32).contiguous(),
+             scale=None if scale is None else scale.to(torch.float32).contiguous(),
+             base=None if base is None else base.contiguous(), stream=s)
+    return out, t
+
+
+def lora_forward(x, down, up, group_sizes, order=None, scale=None, base=None, out=None, stream=None):
+    """Low-rank adapters beside a projection: ``t = scale[g] x down[g]^T`` and ``out = base + t up[g]`` for bf16 x
+    [M, K], down [G, r, K], up [G, r, N], base [M, N] (None: zeros). The rows of group g are the next
+    ``group_sizes[g]`` of ``order`` (:func:`lora_group`; None: rows already sorted); rows past the last group keep
+    base. Returns ``(out bf16 [M, N], t bf16 [M, r])``, t in sorted order, for :func:`lora_grad_weight`. ``out`` may
+    be ``base``."""
+    return _lora(rdot_lora_forward, x, down, up, down, up, group_sizes, order, scale, base, out, stream)
+
+
+def lora_grad_input(dy, down, up, group_sizes, order=None, scale=None, base=None, dx=None, stream=None):
+    """The gradient of :func:`lora_forward`'s x: ``dt = scale[g] dy up[g]^T`` and ``dx = base + dt down[g]`` for dy bf16
+    [M, N]; base [M, K] is the gradient through the projection itself. Returns ``(dx bf16 [M, K], dt bf16
+    [M, r])``, dt in sorted order. ``dx`` may be ``base``."""
+    return _lora(rdot_lora_grad_input, dy, up, down, down, up, group_sizes, order, scale, base, dx, stream)
+
+
+def lora_grad_weight(t, z, group_sizes, order=None, z_scale=None, out_dtype=None, dw=None, stream=None):
+    """The gradients of the adapters, ``dw[g] = t_g^T z_g`` [G, r, width] (fp32 by default, or bf16): of up from
+    :func:`lora_forward`'s t and z = dy, of down from :func:`lora_grad_input`'s dt and z = x. z is bf16 [M, width]
+    or the codes of :func:`quantize_mxfp8` with ``z_scale``."""
+    import torch
+    if t.dim() != 2 or z.dim() != 2 or group_sizes.dim() != 1:
+        raise ValueError("t must be [M, r], z [M, width] and group_sizes [G]")
+    m, r = t.shape
+    width, g = z.shape[1], group_sizes.shape[0]
+    if (z.shape[0] != m or (order is not None and order.shape != (m,))
+            or (z_scale is not None and z_scale.shape != (m, width // 32))):
+        raise ValueError("shape mismatch between t, z, z_scale and order")
+    if (t.dtype != torch.bfloat16 or z.dtype != (torch.bfloat16 if z_scale is None else torch.uint8)
+            or (z_scale is not None and z_scale.dtype != torch.uint8)):
+        raise TypeError("t must be bfloat16, z bfloat16 or, with a uint8 z_scale, uint8 codes")
+    _same_device(t, z, group_sizes, *(v for v in (order, z_scale) if v is not None))
+    out_dtype = out_dtype or (dw.dtype if dw is not None else torch.float32)
+    if dw is not None:
+        _check_out(dw, g * r * width, out_dtype, t.device, "dw")
+        if dw.shape != (g, r, width):
+            raise ValueError("dw must be [G, r, width]")
+    s = _run_stream(stream, t.device)
+    with torch.cuda.stream(s):
+        if dw is None:
+            dw = torch.empty((g, r, width), dtype=out_dtype, device=t.device)
+        rdot_lora_grad_weight(t.contiguous(), z.contiguous(), group_sizes.to(torch.int32).contiguous(), dw,
+                              order=None if order is None else order.to(torch.int32).contiguous(),
+                              z_scale=None if z_scale is None else z_scale.contiguous(), stream=s)
+    return dw
 
 
 def ragged_dot_mxfp8(lhs_q, lhs_scale, rhs_q, rhs_scale, group_sizes, out=None, stream=None):

@@ -1545,6 +1545,109 @@ rdot_status rdot_router_topk_grad(const void* logits, int32_t dtype, const int32
     return e == cudaSuccess ? RDOT_OK : cuda_fail(e, "router top-k gradient launch");
 }
 
+rdot_status rdot_quantize_mxfp8(const void* x, int32_t dtype, int64_t rows, int64_t k, uint8_t* codes,
+                                uint8_t* scales, void* stream) {
+    if (rows < 0 || k < 1 || (dtype != RDOT_F32 && dtype != RDOT_BF16)) return RDOT_ERR_INVALID_ARG;
+    if (k % 32 || k > 0x7fffffffLL || rows > (1LL << 46) / k) return RDOT_ERR_UNSUPPORTED;
+    if (rows == 0) return RDOT_OK;
+    if (!x || !codes || !scales) return RDOT_ERR_INVALID_ARG;
+    if (!aligned16(x) || !aligned16(codes)) return RDOT_ERR_INVALID_ARG;
+    const int sms = current_sm_count();
+    if (sms <= 0) return cuda_fail(cudaGetLastError(), "cudaDeviceGetAttribute");
+    cudaError_t e = launch_quantize_mxfp8(x, dtype == RDOT_BF16, rows * k, codes, scales, sms,
+                                          static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? RDOT_OK : cuda_fail(e, "mxfp8 quantise launch");
+}
+
+rdot_status rdot_dequantize_mxfp8(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t k, int32_t dtype,
+                                  void* out, void* stream) {
+    if (rows < 0 || k < 1 || (dtype != RDOT_F32 && dtype != RDOT_BF16)) return RDOT_ERR_INVALID_ARG;
+    if (k % 32 || k > 0x7fffffffLL || rows > (1LL << 46) / k) return RDOT_ERR_UNSUPPORTED;
+    if (rows == 0) return RDOT_OK;
+    if (!codes || !scales || !out) return RDOT_ERR_INVALID_ARG;
+    if (!aligned16(codes) || !aligned16(out)) return RDOT_ERR_INVALID_ARG;
+    const int sms = current_sm_count();
+    if (sms <= 0) return cuda_fail(cudaGetLastError(), "cudaDeviceGetAttribute");
+    cudaError_t e = launch_dequantize_mxfp8(codes, scales, rows * k, out, dtype == RDOT_BF16, sms,
+                                            static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? RDOT_OK : cuda_fail(e, "mxfp8 restore launch");
+}
+
+rdot_status rdot_lora_group(const int32_t* ids, int64_t m, int32_t groups, int32_t* group_sizes, int32_t* order,
+                            void* stream) {
+    if (m < 0 || groups < 1 || !group_sizes || !aligned4(group_sizes)) return RDOT_ERR_INVALID_ARG;
+    if (groups > RDOT_MAX_GROUPS || m > 0x7fffffffLL) return RDOT_ERR_UNSUPPORTED;
+    if (m > 0 && (!ids || !order || !aligned4(ids) || !aligned4(order))) return RDOT_ERR_INVALID_ARG;
+    cudaError_t e = launch_lora_group(ids, static_cast<int>(m), groups, group_sizes, order,
+                                      static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? RDOT_OK : cuda_fail(e, "lora group launch");
+}
+
+namespace {
+// What every adapter call checks of its sizes: 16-byte rows and widths that 32-bit column counts hold.
+rdot_status lora_sizes(int64_t m, int64_t k, int64_t n, int32_t groups, int32_t rank) {
+    if (m < 0 || k < 1 || n < 1 || groups < 1 || rank < 1) return RDOT_ERR_INVALID_ARG;
+    if (m > 0x7fffffffLL || k % 8 || n % 8 || k > (1LL << 30) || n > (1LL << 30) || groups > RDOT_MAX_GROUPS ||
+        rank % 8 || rank > RDOT_LORA_MAX_RANK)
+        return RDOT_ERR_UNSUPPORTED;
+    return RDOT_OK;
+}
+
+// out = base + scale (x first^T) second: the forward, and with the weights exchanged the gradient of the input.
+rdot_status lora_apply(const void* x, const void* first, const void* second, const int32_t* group_sizes,
+                       const int32_t* order, const float* scale, const void* base, int64_t m, int64_t k, int64_t n,
+                       int32_t groups, int32_t rank, void* out, void* t, void* stream) {
+    const rdot_status st = lora_sizes(m, k, n, groups, rank);
+    if (st != RDOT_OK) return st;
+    if (m == 0) return RDOT_OK;
+    if (!x || !first || !second || !group_sizes || !out || out == x) return RDOT_ERR_INVALID_ARG;
+    if (!aligned16(x) || !aligned16(first) || !aligned16(second) || !aligned16(base) || !aligned16(out) ||
+        !aligned16(t) || !aligned4(group_sizes) || !aligned4(order) || !aligned4(scale))
+        return RDOT_ERR_INVALID_ARG;
+    const int sms = current_sm_count();
+    if (sms <= 0) return cuda_fail(cudaGetLastError(), "cudaDeviceGetAttribute");
+    const LoraArgs a{x, first, second, group_sizes, order, scale, base, out, t, static_cast<int>(m),
+                     static_cast<int>(k), static_cast<int>(n), groups, rank};
+    const cudaError_t e = launch_lora_apply(a, sms, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? RDOT_OK : cuda_fail(e, "lora launch");
+}
+}  // namespace
+
+rdot_status rdot_lora_forward(const void* x, const void* down, const void* up, const int32_t* group_sizes,
+                              const int32_t* order, const float* scale, const void* base, int64_t m, int64_t k,
+                              int64_t n, int32_t groups, int32_t rank, void* out, void* t, void* stream) {
+    return lora_apply(x, down, up, group_sizes, order, scale, base, m, k, n, groups, rank, out, t, stream);
+}
+
+rdot_status rdot_lora_grad_input(const void* dy, const void* down, const void* up, const int32_t* group_sizes,
+                                 const int32_t* order, const float* scale, const void* base, int64_t m, int64_t k,
+                                 int64_t n, int32_t groups, int32_t rank, void* dx, void* dt, void* stream) {
+    return lora_apply(dy, up, down, group_sizes, order, scale, base, m, n, k, groups, rank, dx, dt, stream);
+}
+
+rdot_status rdot_lora_grad_weight(const void* t, const void* z, int32_t z_dtype, const uint8_t* z_scale,
+                                  const int32_t* group_sizes, const int32_t* order, int64_t m, int64_t width,
+                                  int32_t groups, int32_t rank, int32_t out_dtype, void* dw, void* stream) {
+    if ((z_dtype != RDOT_BF16 && z_dtype != RDOT_E4M3) || (out_dtype != RDOT_F32 && out_dtype != RDOT_BF16))
+        return RDOT_ERR_INVALID_ARG;
+    const rdot_status st = lora_sizes(m, width, width, groups, rank);
+    if (st != RDOT_OK) return st;
+    // a block per group, 128 columns and up to 8 shares of its rows
+    if ((z_dtype == RDOT_E4M3 && width % 32) || (width + 127) / 128 > 0x7fffffffLL / 8 / groups) return RDOT_ERR_UNSUPPORTED;
+    if (!group_sizes || !dw || !aligned4(group_sizes) || !aligned16(dw)) return RDOT_ERR_INVALID_ARG;
+    if (m > 0) {
+        if (!t || !z || (z_dtype == RDOT_E4M3 && !z_scale)) return RDOT_ERR_INVALID_ARG;
+        if (!aligned16(t) || !aligned16(z) || !aligned4(order) || (z_dtype == RDOT_E4M3 && !aligned4(z_scale)))
+            return RDOT_ERR_INVALID_ARG;
+    }
+    const int sms = current_sm_count();
+    if (sms <= 0) return cuda_fail(cudaGetLastError(), "cudaDeviceGetAttribute");
+    const LoraGradArgs a{t, z, z_scale, group_sizes, order, dw, static_cast<int>(m), static_cast<int>(width), groups, rank};
+    const cudaError_t e = launch_lora_grad(a, z_dtype == RDOT_E4M3, out_dtype == RDOT_BF16, sms,
+                                           static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? RDOT_OK : cuda_fail(e, "lora weight gradient launch");
+}
+
 const char* rdot_status_string(rdot_status status) {
     switch (status) {
         case RDOT_OK: return "RDOT_OK";

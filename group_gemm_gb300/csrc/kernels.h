@@ -255,6 +255,44 @@ cudaError_t launch_router_topk_grad(const void* logits, bool bf16, const int32_t
                                     const float* dweights, long long tokens, int E, int k, int mode, void* dlogits,
                                     int sm_count, cudaStream_t stream);
 
+// Low-rank adapters. lora_apply.cu: t = scale[g] x first[g]^T, out = base + t second[g] over rows sorted by
+// group, sorted position p standing for row order[p] of x, base and out (null: row p).
+struct LoraArgs {
+    const void* x;               // device bf16 [M, K]
+    const void* first;           // device bf16 [G, rank, K]
+    const void* second;          // device bf16 [G, rank, N]
+    const int32_t* group_sizes;  // device [G]
+    const int32_t* order;        // device [M], or null
+    const float* scale;          // device [G], or null (1)
+    const void* base;            // device bf16 [M, N], or null (0)
+    void* out;                   // device bf16 [M, N]; may be base
+    void* t;                     // device bf16 [M, rank], or null
+    int M, K, N, G, rank;
+};
+cudaError_t launch_lora_apply(const LoraArgs& a, int sm_count, cudaStream_t stream);
+
+// lora_grad.cu: dw[g] = sum over the sorted positions p of group g of t[p]^T z[order[p]].
+struct LoraGradArgs {
+    const void* t;               // device bf16 [M, rank]
+    const void* z;               // device bf16 [M, C], or E4M3 codes [M, C]
+    const uint8_t* z_scale;      // device [M, C/32] with codes, else null
+    const int32_t* group_sizes;  // device [G]
+    const int32_t* order;        // device [M], or null
+    void* dw;                    // device [G, rank, C], fp32 or bf16
+    int M, C, G, rank;
+};
+cudaError_t launch_lora_grad(const LoraGradArgs& a, bool codes, bool out_bf16, int sm_count, cudaStream_t stream);
+
+// lora_group.cu: rows sorted by id (stable; ids outside [0, G) last), and the rows of each id.
+cudaError_t launch_lora_group(const int32_t* ids, int M, int G, int32_t* group_sizes, int32_t* order,
+                              cudaStream_t stream);
+
+// MXFP8 quantisation of rows and its inverse (mxfp8_quant.cu), as arrays of 32-element blocks.
+cudaError_t launch_quantize_mxfp8(const void* x, bool bf16, long long elements, uint8_t* codes, uint8_t* scales,
+                                  int sm_count, cudaStream_t stream);
+cudaError_t launch_dequantize_mxfp8(const uint8_t* codes, const uint8_t* scales, long long elements, void* out,
+                                    bool bf16, int sm_count, cudaStream_t stream);
+
 // Padded-dense baseline data movement (padded.cu).
 cudaError_t launch_pad_scatter(const void* lhs, const int32_t* gs, void* lhs_pad, int32_t* uniform_gs, int M, int G,
                                int C, long long row_bytes, int grid, int32_t* status, cudaStream_t stream);

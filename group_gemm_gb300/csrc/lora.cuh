@@ -1,0 +1,151 @@
+// lora.cuh -- what the low-rank adapter kernels share: asynchronous row copies, the 16 x 8 x 16 bf16 MMA on
+// register fragments, and the scan that finds a block's rows.
+#pragma once
+
+#include <stdint.h>
+
+#include "ptx.cuh"
+
+namespace rdot {
+
+// 16 bytes global -> shared, or 16 zero bytes where `live` is false (src is then not read).
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool live) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
+}
+
+// 4 bytes of which the first `bytes` are read, the others 0.
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, int bytes) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// Four 8 x 8 matrices of 16-bit elements; lanes 8i .. 8i+7 give the row addresses of matrix i.
+__device__ __forceinline__ void ldmatrix_x4(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+
+__device__ __forceinline__ void ldmatrix_x4_trans(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+
+// d [16 x 8] += a [16 x 16] b [16 x 8], fp32 sums.
+__device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+
+__device__ __forceinline__ uint32_t cluster_ctas() {
+    uint32_t n;
+    asm volatile("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(n));
+    return n;
+}
+
+__device__ __forceinline__ float4 ld_shared_cluster_f4(uint32_t addr) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(addr)
+                 : "memory");
+    return v;
+}
+
+// Sum over a block of 128 threads of `v`, and of the threads before this one. `part`: shared, 4 entries; the
+// caller synchronises between uses.
+__device__ __forceinline__ long long block_scan128(long long v, long long* part, long long* total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    long long incl = v;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const long long u = __shfl_up_sync(0xffffffffu, incl, d);
+        if (lane >= d) incl += u;
+    }
+    if (lane == 31) part[warp] = incl;
+    __syncthreads();
+    long long before = 0, all = 0;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+        before += w < warp ? part[w] : 0;
+        all += part[w];
+    }
+    *total = all;
+    return before + incl - v;
+}
+
+constexpr int LORA_THREADS = 128;
+constexpr int LORA_SIZES = 8;   // sizes a thread holds: 1024 groups
+
+// A block's tile: the rows of group g (G: rows of no group), sorted positions p0 .. p0 + rows - 1.
+struct LoraTile {
+    int g;
+    int p0;
+    int rows;
+};
+
+// Tile `w` of the rows cut into tiles of at most R rows that do not cross a group's end: the groups in
+// order, then the rows past the last one. rows = 0 past the last tile. A negative size counts as 0, ends are
+// clamped to M. Every thread gets the tile; all sizes are loaded at once, one pass.
+template <int R>
+__device__ __forceinline__ LoraTile lora_find_tile(const int32_t* __restrict__ sizes, int G, int M, int w) {
+    __shared__ long long part[2][4];
+    __shared__ LoraTile found;
+    const int per = (G + LORA_THREADS - 1) / LORA_THREADS;   // consecutive groups per thread, <= LORA_SIZES
+    const int g0 = threadIdx.x * per;
+    int s[LORA_SIZES];
+    long long sum = 0;
+#pragma unroll
+    for (int i = 0; i < LORA_SIZES; ++i) s[i] = (i < per && g0 + i < G) ? max(__ldg(sizes + g0 + i), 0) : 0;
+#pragma unroll
+    for (int i = 0; i < LORA_SIZES; ++i) sum += s[i];
+    if (threadIdx.x == 0) found = LoraTile{G, 0, 0};
+    long long total, tiles_total;
+    const long long first = block_scan128(sum, part[0], &total);
+    long long at = first, tiles = 0;
+#pragma unroll
+    for (int i = 0; i < LORA_SIZES; ++i) {
+        const long long b = min(at, static_cast<long long>(M)), e = min(at + s[i], static_cast<long long>(M));
+        tiles += (e - b + R - 1) / R;
+        at += s[i];
+    }
+    long long t = block_scan128(tiles, part[1], &tiles_total);
+    if (w >= t && w < t + tiles) {
+        at = first;
+#pragma unroll
+        for (int i = 0; i < LORA_SIZES; ++i) {
+            const int b = static_cast<int>(min(at, static_cast<long long>(M)));
+            const int e = static_cast<int>(min(at + s[i], static_cast<long long>(M)));
+            const int n = static_cast<int>((static_cast<long long>(e) - b + R - 1) / R);
+            if (w >= t && w < t + n) {
+                const int p0 = b + static_cast<int>(w - t) * R;
+                found = LoraTile{g0 + i, p0, min(R, e - p0)};
+            }
+            t += n;
+            at += s[i];
+        }
+    }
+    if (threadIdx.x == 0 && w >= tiles_total) {
+        const long long p0 = min(total, static_cast<long long>(M)) + (w - tiles_total) * R;
+        if (p0 < M) found = LoraTile{G, static_cast<int>(p0), static_cast<int>(min(static_cast<long long>(R), M - p0))};
+    }
+    __syncthreads();
+    return found;
+}
+
+}  // namespace rdot

@@ -1,0 +1,285 @@
+// lora_apply.cu -- low-rank adapters beside a projection: out = base + scale[g] (x first[g]^T) second[g].
+//
+// For a tile of R rows of one group the kernel forms t = scale[g] x first[g]^T (contraction over the K columns
+// of x) and then base + t second[g], in one launch and without t's round trip through memory. Both weights lie
+// [G, r, width], their long axis contiguous, so the forward (first = down, second = up) and the gradient of the
+// input (first = up, second = down) are the same kernel. Up to 16 x 2 flops for a byte at rank 16: HBM is the
+// bound, and x, base and out pass once.
+//
+// A cluster of C blocks takes a tile: each contracts its share of the columns of x, the fp32 partial sums are
+// added through distributed shared memory in a fixed order, and each then writes its share of the output's
+// columns. So a few rows still spread over many SMs, and results do not depend on timing.
+//
+// t keeps fp32 accuracy into the second product: it enters as two bf16 terms, t = hi + lo with lo the rounded
+// rest (relative error 2^-17, below the output's own rounding of 2^-9), two MMAs in place of one. hi is also
+// what is returned as t, the operand of the weight gradient.
+#include <cuda_bf16.h>
+
+#include "kernels.h"
+#include "lora.cuh"
+#include "pdl.cuh"
+
+namespace rdot {
+
+namespace {
+
+template <int R_, int RP_>
+struct ApplyCfg {
+    static constexpr int R = R_;                       // rows of a tile
+    static constexpr int RP = RP_;                     // rank, rounded up
+    static constexpr int WR = R / 16;                  // warps along the rows
+    static constexpr int WK = 4 / WR;                  // warps along the columns (both products)
+    static constexpr int BK = RP <= 32 ? 128 : 64;     // columns per stage
+    static constexpr int PITCH = 2 * BK + 16;          // bytes: 16 off a multiple of 128, so ldmatrix has no conflicts
+    static constexpr int SLOT = (R + RP) * PITCH;      // x or base rows, then weight rows
+    static constexpr int STAGES = RP == 16 || RP == 64 ? 4 : 3;
+    static constexpr int PP = RP + 4;                  // pitch of the partial sums (fp32)
+    static constexpr int TP = RP + 8;                  // pitch of hi and lo (bf16)
+    static constexpr int PART = WK * R * PP * 4;
+    static constexpr int SMEM = STAGES * SLOT + PART + 2 * R * TP * 2;
+};
+
+template <class Cfg>
+__global__ void __launch_bounds__(LORA_THREADS) lora_apply_kernel(LoraArgs a) {
+    constexpr int R = Cfg::R, RP = Cfg::RP, WR = Cfg::WR, WK = Cfg::WK, BK = Cfg::BK, PITCH = Cfg::PITCH;
+    constexpr int S = Cfg::STAGES, PP = Cfg::PP, TP = Cfg::TP;
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ int row_of[R];   // each tile row's row of x, base and out; -1 for none
+    float* part = reinterpret_cast<float*>(smem + S * Cfg::SLOT);
+    uint16_t* thi = reinterpret_cast<uint16_t*>(smem + S * Cfg::SLOT + Cfg::PART);
+    uint16_t* tlo = thi + R * TP;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int wr = warp % WR, wk = warp / WR;
+    const int C = static_cast<int>(cluster_ctas()), rank = static_cast<int>(cluster_ctarank());
+
+    grid_dependency_enter();
+    const LoraTile tile = lora_find_tile<R>(a.group_sizes, a.G, a.M, static_cast<int>(blockIdx.x) / C);
+    if (tile.rows == 0) return;   // the whole cluster
+    const bool live = tile.g < a.G;
+    for (int i = tid; i < R; i += LORA_THREADS) {
+        int row = -1;
+        if (i < tile.rows) {
+            row = a.order ? __ldg(a.order + tile.p0 + i) : tile.p0 + i;
+            if (row < 0 || row >= a.M) row = -1;
+        }
+        row_of[i] = row;
+    }
+    __syncthreads();
+
+    const int nk = live ? (a.K + BK - 1) / BK : 0, nn = (a.N + BK - 1) / BK;
+    const int k0 = static_cast<int>(static_cast<long long>(nk) * rank / C), k1 = static_cast<int>(static_cast<long long>(nk) * (rank + 1) / C);
+    int n0 = static_cast<int>(static_cast<long long>(nn) * rank / C), n1 = static_cast<int>(static_cast<long long>(nn) * (rank + 1) / C);
+    if (!live && a.base == a.out) n1 = n0;   // rows without an adapter, in place: they stay as they are
+    const int first_stages = k1 - k0, stages = first_stages + n1 - n0;
+    const uint32_t ring = smem_u32(smem);
+
+    // stage i of this block into its slot: 16-byte pieces, zeros outside the tensors
+    const auto load = [&](int i) {
+        if (i < stages) {
+            constexpr int V = BK / 8;   // pieces of a row
+            const bool one = i < first_stages;
+            const int width = one ? a.K : a.N;
+            const int c0 = (one ? k0 + i : n0 + i - first_stages) * BK + (tid % V) * 8;
+            const uint16_t* rows = static_cast<const uint16_t*>(one ? a.x : a.base);
+            const uint16_t* weight = static_cast<const uint16_t*>(one ? a.first : a.second);
+            const bool in = c0 < width;
+            const uint32_t dst = ring + (i % S) * Cfg::SLOT + (tid % V) * 16;
+            if (rows) {
+#pragma unroll
+                for (int r = tid / V; r < R; r += LORA_THREADS / V) {
+                    const int row = row_of[r];
+                    const bool ok = in && row >= 0;
+                    cp_async16(dst + r * PITCH, rows + (ok ? static_cast<long long>(row) * width + c0 : 0), ok);
+                }
+            }
+            if (live) {
+#pragma unroll
+                for (int r = tid / V; r < RP; r += LORA_THREADS / V) {
+                    const bool ok = in && r < a.rank;
+                    cp_async16(dst + (R + r) * PITCH,
+                               weight + (ok ? (static_cast<long long>(tile.g) * a.rank + r) * width + c0 : 0), ok);
+                }
+            }
+        }
+        cp_async_commit();
+    };
+#pragma unroll
+    for (int i = 0; i < S - 1; ++i) load(i);
+
+    int i = 0;
+    if (live) {
+        float acc[RP / 8][4] = {};
+        for (; i < first_stages; ++i) {
+            cp_async_wait<S - 2>();
+            __syncthreads();
+            load(i + S - 1);
+            const uint32_t slot = ring + (i % S) * Cfg::SLOT;
+            const uint32_t ax = slot + (wr * 16 + (lane & 15)) * PITCH + (lane >> 4) * 16;
+            const uint32_t bx = slot + (R + (lane & 7) + ((lane >> 4) << 3)) * PITCH + ((lane >> 3) & 1) * 16;
+#pragma unroll
+            for (int kk = wk; kk < BK / 16; kk += WK) {
+                uint32_t fa[4];
+                ldmatrix_x4(fa, ax + kk * 32);
+#pragma unroll
+                for (int j = 0; j < RP / 16; ++j) {
+                    uint32_t fb[4];
+                    ldmatrix_x4(fb, bx + j * 16 * PITCH + kk * 32);
+                    mma_16816(acc[2 * j], fa, fb[0], fb[1]);
+                    mma_16816(acc[2 * j + 1], fa, fb[2], fb[3]);
+                }
+            }
+        }
+        // partial sums of the warps, then of the cluster's blocks
+        float* mine = part + wk * R * PP + (wr * 16 + (lane >> 2)) * PP + 2 * (lane & 3);
+#pragma unroll
+        for (int j = 0; j < RP / 8; ++j) {
+            *reinterpret_cast<float2*>(mine + 8 * j) = make_float2(acc[j][0], acc[j][1]);
+            *reinterpret_cast<float2*>(mine + 8 * PP + 8 * j) = make_float2(acc[j][2], acc[j][3]);
+        }
+        __syncthreads();
+        if (C > 1) {
+            if (WK > 1) {
+                for (int e = tid; e < R * RP / 4; e += LORA_THREADS) {
+                    float4* p = reinterpret_cast<float4*>(part + (e / (RP / 4)) * PP + 4 * (e % (RP / 4)));
+                    float4 s = *p;
+#pragma unroll
+                    for (int w = 1; w < WK; ++w) {
+                        const float4 v = p[w * R * PP / 4];
+                        s = make_float4(s.x + v.x, s.y + v.y, s.z + v.z, s.w + v.w);
+                    }
+                    *p = s;
+                }
+            }
+            cluster_sync();
+        }
+        const float scale = a.scale ? __ldg(a.scale + tile.g) : 1.f;
+        for (int e = tid; e < R * RP / 4; e += LORA_THREADS) {
+            const int r = e / (RP / 4), c = 4 * (e % (RP / 4));
+            float* p = part + r * PP + c;
+            float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (C > 1) {
+                const uint32_t addr = smem_u32(p);
+#pragma unroll 4
+                for (int q = 0; q < C; ++q) {
+                    const float4 v = ld_shared_cluster_f4(mapa_shared(addr, q));
+                    s = make_float4(s.x + v.x, s.y + v.y, s.z + v.z, s.w + v.w);
+                }
+            } else {
+#pragma unroll
+                for (int w = 0; w < WK; ++w) {
+                    const float4 v = *reinterpret_cast<const float4*>(p + w * R * PP);
+                    s = make_float4(s.x + v.x, s.y + v.y, s.z + v.z, s.w + v.w);
+                }
+            }
+            // ranks past the adapter's are 0 whatever x holds (there x times the zero weights may be NaN)
+            const bool in = c < a.rank;
+            const float v[4] = {in ? s.x * scale : 0.f, in ? s.y * scale : 0.f, in ? s.z * scale : 0.f, in ? s.w * scale : 0.f};
+            float rest[4];
+            uint2 hi;
+            hi.x = pack_bf16x2(v[0], v[1]);
+            hi.y = pack_bf16x2(v[2], v[3]);
+            const uint32_t h[2] = {hi.x, hi.y};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float f = __uint_as_float(j & 1 ? h[j >> 1] & 0xffff0000u : h[j >> 1] << 16);
+                rest[j] = isfinite(f) ? v[j] - f : 0.f;   // an infinity or NaN is hi alone
+            }
+            *reinterpret_cast<uint2*>(thi + r * TP + c) = hi;
+            *reinterpret_cast<uint2*>(tlo + r * TP + c) = make_uint2(pack_bf16x2(rest[0], rest[1]), pack_bf16x2(rest[2], rest[3]));
+            if (rank == 0 && a.t && r < tile.rows && in)
+                *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.t) + static_cast<long long>(tile.p0 + r) * a.rank + c) = hi;
+        }
+        if (C > 1) {
+            __syncwarp();
+            cluster_arrive();   // this block has read the others' sums
+        }
+        __syncthreads();
+    } else if (rank == 0 && a.t) {
+        for (long long e = tid; e < static_cast<long long>(tile.rows) * a.rank / 4; e += LORA_THREADS)
+            reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.t) + static_cast<long long>(tile.p0) * a.rank)[e] = make_uint2(0u, 0u);
+    }
+
+    for (; i < stages; ++i) {
+        cp_async_wait<S - 2>();
+        __syncthreads();
+        load(i + S - 1);
+        uint8_t* slot = smem + (i % S) * Cfg::SLOT;
+        const uint32_t bx = smem_u32(slot) + (R + (lane & 15)) * PITCH + (lane >> 4) * 16;
+        const uint32_t ahi = smem_u32(thi) + (wr * 16 + (lane & 15)) * TP * 2 + (lane >> 4) * 16;
+        const uint32_t alo = ahi + R * TP * 2;
+        constexpr int COLS = BK / WK;   // this warp's columns of the stage
+#pragma unroll
+        for (int n = 0; n < COLS; n += 16) {
+            float acc[2][4] = {};
+            if (live) {
+#pragma unroll
+                for (int kk = 0; kk < RP / 16; ++kk) {
+                    uint32_t fb[4], fh[4], fl[4];
+                    ldmatrix_x4_trans(fb, bx + kk * 16 * PITCH + (wk * COLS + n) * 2);
+                    ldmatrix_x4(fh, ahi + kk * 32);
+                    ldmatrix_x4(fl, alo + kk * 32);
+                    mma_16816(acc[0], fh, fb[0], fb[1]);
+                    mma_16816(acc[1], fh, fb[2], fb[3]);
+                    mma_16816(acc[0], fl, fb[0], fb[1]);
+                    mma_16816(acc[1], fl, fb[2], fb[3]);
+                }
+            }
+            if (!live && a.base) continue;   // a copy
+            // onto base, in place in the stage; a 32-bit word holds two columns of one lane
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    uint32_t* p = reinterpret_cast<uint32_t*>(slot + (wr * 16 + (lane >> 2) + 8 * half) * PITCH +
+                                                             (wk * COLS + n + 8 * h + 2 * (lane & 3)) * 2);
+                    const uint32_t b = a.base ? *p : 0u;
+                    *p = pack_bf16x2(__uint_as_float(b << 16) + acc[h][2 * half],
+                                     __uint_as_float(b & 0xffff0000u) + acc[h][2 * half + 1]);
+                }
+        }
+        __syncwarp();
+        // the warp's rows and columns of the stage, 16 bytes a lane
+        constexpr int V = COLS / 8;
+        const int c0 = (n0 + i - first_stages) * BK + wk * COLS + (lane % V) * 8;
+#pragma unroll
+        for (int r = lane / V; r < 16; r += 32 / V) {
+            const int row = row_of[wr * 16 + r];
+            if (row >= 0 && c0 < a.N)
+                *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + static_cast<long long>(row) * a.N + c0) =
+                    *reinterpret_cast<const uint4*>(slot + (wr * 16 + r) * PITCH + (wk * COLS + (lane % V) * 8) * 2);
+        }
+    }
+    if (live && C > 1) cluster_wait();   // the others have read this block's sums
+}
+
+template <class Cfg>
+cudaError_t launch_cfg(const LoraArgs& a, long long tiles, int C, cudaStream_t stream) {
+    auto kern = lora_apply_kernel<Cfg>;
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::SMEM);
+    if (e != cudaSuccess) return e;
+    return launch_pdl_cluster(kern, dim3(static_cast<unsigned>(tiles * C)), dim3(LORA_THREADS), C, Cfg::SMEM, stream, a);
+}
+
+template <int R>
+cudaError_t launch_rows(const LoraArgs& a, int C, cudaStream_t stream) {
+    // a tile more for each group that ends inside one, one more for the rows of no group
+    const long long tiles = (static_cast<long long>(a.M) + R - 1) / R + (a.G < a.M ? a.G : a.M) + 1;
+    if (a.rank <= 16) return launch_cfg<ApplyCfg<R, 16>>(a, tiles, C, stream);
+    if (a.rank <= 32) return launch_cfg<ApplyCfg<R, 32>>(a, tiles, C, stream);
+    if (a.rank <= 64) return launch_cfg<ApplyCfg<R, 64>>(a, tiles, C, stream);
+    return launch_cfg<ApplyCfg<R, 128>>(a, tiles, C, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_lora_apply(const LoraArgs& a, int sm_count, cudaStream_t stream) {
+    const long long groups = a.G < a.M ? a.G : a.M;         // groups that can have a row
+    const long long rows = (a.M + groups - 1) / groups;     // rows of an average one
+    const int R = rows <= 16 ? 16 : 64;
+    const long long tiles = groups * ((rows + R - 1) / R);
+    int C = 1;
+    while (C < 8 && tiles * C * 2 <= 2LL * sm_count) C *= 2;
+    return R == 16 ? launch_rows<16>(a, C, stream) : launch_rows<64>(a, C, stream);
+}
+
+}  // namespace rdot

@@ -419,6 +419,89 @@ RDOT_API rdot_status rdot_router_topk_grad(const void* logits, int32_t dtype, co
                                            int32_t n_experts, int32_t topk, int32_t weights, void* dlogits,
                                            void* stream);
 
+/* MXFP8 rows: activations kept in 8 bits (OCP Microscaling Formats v1.0: E4M3 codes, one E8M0 scale byte s
+ * per 32 consecutive elements of a row, value = e4m3(code) * 2^(s-127), s = 255 is NaN). Codes and scales are
+ * what rdot_forward_mxfp8 takes as lhs and rdot_grad_input_mxfp8 as dy, and what rdot_lora_grad_weight
+ * takes as a checkpoint of an activation.
+ *
+ * Quantisation rule: the scale of a block is the smallest power of two with amax / scale <= 448, at least
+ * 2^-127 (amax the largest magnitude), so that no element saturates; an element is divided by it and rounded
+ * to E4M3 to nearest even. A block holding a NaN or an infinity gets s = 255 and codes 0.
+ *
+ * rdot_quantize_mxfp8
+ *   x       device [rows, k], dtype RDOT_F32 or RDOT_BF16
+ *   codes   device uint8 [rows, k] out;  scales  device uint8 [rows, k/32] out
+ * rdot_dequantize_mxfp8
+ *   out     device [rows, k] out, dtype RDOT_F32 (exact) or RDOT_BF16 (exact unless the value is below 2^-126:
+ *           to nearest even)
+ * k % 32 == 0, else RDOT_ERR_UNSUPPORTED; 16-byte alignment for x, codes and out, any for scales. Both run on
+ * the calling thread's current device and never synchronise the host; rows = 0 launches nothing. */
+RDOT_API rdot_status rdot_quantize_mxfp8(const void* x, int32_t dtype, int64_t rows, int64_t k, uint8_t* codes,
+                                         uint8_t* scales, void* stream);
+RDOT_API rdot_status rdot_dequantize_mxfp8(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t k,
+                                           int32_t dtype, void* out, void* stream);
+
+/* Low-rank adapters: beside a projection whose weights are shared or frozen (its result is `base`), each row
+ * adds the product with the two thin matrices of its own adapter. The rows of one call may use up to
+ * RDOT_MAX_GROUPS adapters: many requests served together, or one adapter for each expert of a layer.
+ *   down  device bf16 [G, r, K];  up  device bf16 [G, r, N]: the long axis contiguous on both
+ *   t[p]      = scale[g] * x[row] down[g]^T           (r numbers)
+ *   out[row]  = base[row] + t[p] up[g]
+ * for the sorted positions p of group g (consecutive, group_sizes[g] of them, as everywhere in this library)
+ * and row = order[p], or p where order is null. rdot_lora_group makes group_sizes and order from one adapter
+ * id per row, once for all projections of a batch; rows that the router sorted by expert
+ * (rdot_moe_permute) need no order. A negative size counts as 0 and ends are clamped to M, as in the
+ * products; positions past the last group have no adapter: their rows of out are base's (zeros without a
+ * base), their rows of t zeros. order must hold every row once; an entry outside [0, M) counts as none (its
+ * row is not written). There is no workspace and no state between calls; every call can be captured in a
+ * CUDA graph. They run on the calling thread's current device and never synchronise the host.
+ *
+ * Sums are fp32 in a fixed order. t enters the second product with an error of 2^-17, out is rounded to
+ * bf16 once. m = 0 launches nothing, except that the weight gradient still writes its zeros. k % 8 == 0,
+ * n % 8 == 0 (at most 2^30), r % 8 == 0 and r <= RDOT_LORA_MAX_RANK (pad smaller adapters with zero rows),
+ * m < 2^31, G <= RDOT_MAX_GROUPS, else RDOT_ERR_UNSUPPORTED; 16-byte alignment, 4 for group_sizes, order,
+ * scale and z_scale. */
+#define RDOT_LORA_MAX_RANK 128
+
+/* rdot_lora_group: the stable sort of a batch's rows by adapter
+ *   ids          device int32 [M]: each row's adapter; outside [0, groups): none
+ *   group_sizes  device int32 [groups] out: rows of each adapter
+ *   order        device int32 [M] out: the rows in sorted order, rows without an adapter last */
+RDOT_API rdot_status rdot_lora_group(const int32_t* ids, int64_t m, int32_t groups, int32_t* group_sizes,
+                                     int32_t* order, void* stream);
+
+/* rdot_lora_forward
+ *   x      device bf16 [M, K];  base  device bf16 [M, N], or null for zeros
+ *   scale  device fp32 [G], or null for 1
+ *   out    device bf16 [M, N]: may be base itself (rows without an adapter are then left alone), not x
+ *   t      device bf16 [M, r] out, in sorted order (what the gradients take), or null */
+RDOT_API rdot_status rdot_lora_forward(const void* x, const void* down, const void* up, const int32_t* group_sizes,
+                                       const int32_t* order, const float* scale, const void* base, int64_t m,
+                                       int64_t k, int64_t n, int32_t groups, int32_t rank, void* out, void* t,
+                                       void* stream);
+
+/* rdot_lora_grad_input, the gradient of x: dt[p] = scale[g] * dy[row] up[g]^T, dx[row] = base[row] + dt[p] down[g]
+ *   dy   device bf16 [M, N];  base  device bf16 [M, K] (the gradient through the projection itself), or null
+ *   dx   device bf16 [M, K]: may be base, not dy;  dt  device bf16 [M, r] out, in sorted order, or null */
+RDOT_API rdot_status rdot_lora_grad_input(const void* dy, const void* down, const void* up,
+                                          const int32_t* group_sizes, const int32_t* order, const float* scale,
+                                          const void* base, int64_t m, int64_t k, int64_t n, int32_t groups,
+                                          int32_t rank, void* dx, void* dt, void* stream);
+
+/* rdot_lora_grad_weight, the gradients of the adapters: dw[g] = sum over the positions p of group g of
+ * t[p]^T z[order[p]]. The gradient of up is that of the forward's t with z = dy (width N), the gradient of down
+ * that of dt with z = x (width K); scale is already in t and dt.
+ *   t    device bf16 [M, r], in sorted order
+ *   z    device [M, width], z_dtype RDOT_BF16, or RDOT_E4M3: the codes of rdot_quantize_mxfp8 with z_scale
+ *        device uint8 [M, width/32] (width % 32 == 0; values below 2^-126 are rounded to bf16); z_scale is
+ *        not read for RDOT_BF16
+ *   dw   device [G, r, width], out_dtype RDOT_F32 or RDOT_BF16 (rounded once); zeros for an adapter without rows
+ * Rows outside every group are never read into the result. */
+RDOT_API rdot_status rdot_lora_grad_weight(const void* t, const void* z, int32_t z_dtype, const uint8_t* z_scale,
+                                           const int32_t* group_sizes, const int32_t* order, int64_t m,
+                                           int64_t width, int32_t groups, int32_t rank, int32_t out_dtype, void* dw,
+                                           void* stream);
+
 /* Bytes of the padded baseline's scratch for a capacity of `capacity` rows per group
  * (the padded lhs [G, capacity, K] plus the padded output [G, capacity, N] plus a small table). */
 RDOT_API rdot_status rdot_padded_workspace_size(rdot_plan_t plan, int64_t capacity, size_t* bytes);
