@@ -33,7 +33,7 @@ __all__ = [
     "quantize_mxfp4", "quantize_mxfp4_weight", "ragged_dot_mxfp4",
     "moe_unpermute_grad", "moe_permute_grad", "router_topk_grad",
     "rdot_quantize_mxfp8", "rdot_dequantize_mxfp8", "rdot_lora_group", "rdot_lora_forward", "rdot_lora_grad_input",
-    "rdot_lora_grad_weight", "quantize_mxfp8", "dequantize_mxfp8", "lora_group", "lora_forward", "lora_grad_input",
+    "rdot_lora_grad_weight", "rdot_lora_read_status", "rdot_lora_clear_status", "rdot_lora_set_wait_timeout", "quantize_mxfp8", "dequantize_mxfp8", "lora_group", "lora_forward", "lora_grad_input",
     "lora_grad_weight", "EXPORTED_SYMBOLS",
 ]
 
@@ -64,7 +64,7 @@ EXPORTED_SYMBOLS = (
     "rdot_moe_unpermute_grad", "rdot_moe_permute_grad", "rdot_router_topk_grad",
     "rdot_quantize_mxfp4", "rdot_quantize_mxfp4_weight", "rdot_mxfp4_weight_scale_bytes", "rdot_forward_mxfp4",
     "rdot_quantize_mxfp8", "rdot_dequantize_mxfp8", "rdot_lora_group", "rdot_lora_forward", "rdot_lora_grad_input",
-    "rdot_lora_grad_weight",
+    "rdot_lora_grad_weight", "rdot_lora_read_status", "rdot_lora_clear_status", "rdot_lora_set_wait_timeout",
 )
 
 _DTYPE_CODES = {"f32": RDOT_F32, "bf16": RDOT_BF16, "e4m3": RDOT_E4M3, "e2m1": RDOT_E2M1}
@@ -152,6 +152,9 @@ def load():
                                        ctypes.c_int32, vp, vp], st),
             "rdot_quantize_mxfp8": ([vp, ctypes.c_int32, i64, i64, vp, vp, vp], st),
             "rdot_dequantize_mxfp8": ([vp, vp, i64, i64, ctypes.c_int32, vp, vp], st),
+            "rdot_lora_read_status": ([i32p, vp], st),
+            "rdot_lora_clear_status": ([vp], st),
+            "rdot_lora_set_wait_timeout": ([ctypes.c_uint64], st),
             "rdot_lora_group": ([vp, i64, ctypes.c_int32, vp, vp, vp], st),
             "rdot_lora_forward": ([vp] * 7 + [i64, i64, i64, ctypes.c_int32, ctypes.c_int32, vp, vp, vp], st),
             "rdot_lora_grad_input": ([vp] * 7 + [i64, i64, i64, ctypes.c_int32, ctypes.c_int32, vp, vp, vp], st),
@@ -366,6 +369,27 @@ def rdot_lora_group(ids, groups: int, group_sizes, order, stream=None) -> None:
     """ids int32 [M] -> group_sizes int32 [groups], order int32 [M]."""
     _check(load().rdot_lora_group(_ptr(ids), int(ids.shape[0]), int(groups), _ptr(group_sizes), _ptr(order),
                                   _stream(stream, group_sizes.device)), "rdot_lora_group")
+
+
+def rdot_lora_read_status(stream=None, device=None) -> int:
+    """The adapter calls' status bits of a device (the current one by default; synchronises the stream)."""
+    import torch
+    v = ctypes.c_int32()
+    with torch.cuda.device(device):
+        st = load().rdot_lora_read_status(ctypes.byref(v), _stream(stream, device))
+    if st not in (RDOT_OK, RDOT_ERR_DEVICE_TIMEOUT):
+        _check(st, "rdot_lora_read_status")
+    return v.value
+
+
+def rdot_lora_clear_status(stream=None, device=None) -> None:
+    import torch
+    with torch.cuda.device(device):
+        _check(load().rdot_lora_clear_status(_stream(stream, device)), "rdot_lora_clear_status")
+
+
+def rdot_lora_set_wait_timeout(timeout_ns: int) -> None:
+    _check(load().rdot_lora_set_wait_timeout(int(timeout_ns)), "rdot_lora_set_wait_timeout")
 
 
 def _lora_apply(name, x, down, up, group_sizes, order, scale, base, out, t, stream):

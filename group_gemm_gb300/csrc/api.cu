@@ -8,6 +8,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cstdio>
 #include <cstring>
 #include <mutex>
@@ -1593,6 +1594,13 @@ rdot_status lora_sizes(int64_t m, int64_t k, int64_t n, int32_t groups, int32_t 
     return RDOT_OK;
 }
 
+std::atomic<uint64_t> g_lora_timeout_ns{0};   // 0: the default
+
+uint64_t lora_timeout_ns() {
+    const uint64_t ns = g_lora_timeout_ns.load();
+    return ns ? ns : kDefaultTimeoutNs;
+}
+
 // out = base + scale (x first^T) second: the forward, and with the weights exchanged the gradient of the input.
 rdot_status lora_apply(const void* x, const void* first, const void* second, const int32_t* group_sizes,
                        const int32_t* order, const float* scale, const void* base, int64_t m, int64_t k, int64_t n,
@@ -1608,10 +1616,73 @@ rdot_status lora_apply(const void* x, const void* first, const void* second, con
     if (sms <= 0) return cuda_fail(cudaGetLastError(), "cudaDeviceGetAttribute");
     const LoraArgs a{x, first, second, group_sizes, order, scale, base, out, t, static_cast<int>(m),
                      static_cast<int>(k), static_cast<int>(n), groups, rank};
-    const cudaError_t e = launch_lora_apply(a, sms, static_cast<cudaStream_t>(stream));
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const long long routed = std::min<long long>(m, groups);   // groups that can have a row
+    const long long rows = (m + routed - 1) / routed;          // rows of an average one
+    // Tiles of 16 rows while they give an SM no more than one and a third, or groups have no more rows; else the 128-row
+    // tcgen05 form (4096 -> 4096, 4 groups through an order, rank 16: 2048 rows 24 against 43 us, 4096 rows 47 / 35;
+    // rank 64: 39 / 51 and 73 / 39).
+    const long long tiles16 = routed * ((rows + LORA_FEW_ROWS - 1) / LORA_FEW_ROWS);
+    int C = 1;
+    if (rows <= LORA_FEW_ROWS || 3 * tiles16 <= 4LL * sms) {
+        // Clusters up to two blocks per SM (256 rows of 64 groups, 4096 -> 4096: C = 4 16.4, C = 8 22.5 us); up to four where
+        // a row or two of a group leave each block long strips of weights (64 rows of 256 groups, 4096 -> 14336:
+        // C = 4 26.6, C = 8 20.4 us).
+        while (C < 8 && tiles16 * C * 2 <= 2LL * sms + 16) C *= 2;
+        if (C < 8 && rows <= 2 && tiles16 * C * 2 <= 4LL * sms && (k + n) / (128 * 2 * C) >= 16) C *= 2;
+        const cudaError_t e = launch_lora_apply(a, C, s);
+        return e == cudaSuccess ? RDOT_OK : cuda_fail(e, "lora launch");
+    }
+    // Of the 128-row form, one block per SM with a deep ring where clusters of it fill the SMs (8192 rows of 8 groups,
+    // 4096 -> 4096, rank 64: 49 us against 57 for two blocks), else two (8192 rows of 32 groups through an order,
+    // rank 16: 77 against 90).
+    const long long tiles = m / LORA_TALL_ROWS + (3 * routed + 3) / 4;   // three groups in four end inside one, about
+    while (C < 8 && tiles * C * 2 <= sms) C *= 2;
+    const bool deep = rank > 64 || (5 * tiles * C >= 4LL * sms && tiles * C <= sms);
+    if (!deep)
+        while (C < 8 && tiles * C * 2 <= 2LL * sms) C *= 2;
+    CUtensorMap maps[4];
+    const uint32_t box_rows = LORA_TALL_BOX_ROWS;
+    rdot_status ms = encode_2d(&maps[0], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, x, k, m, k * 2, 64, box_rows);
+    if (ms == RDOT_OK) ms = encode_2d(&maps[1], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, base ? base : out, n, m, n * 2, 64, box_rows);
+    const uint32_t box_rank = lora_tall_box_rank(rank);
+    if (ms == RDOT_OK)
+        ms = encode_3d(&maps[2], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, first, k, rank, groups, k * 2, k * 2 * rank, 64, box_rank, 1);
+    if (ms == RDOT_OK)
+        ms = encode_3d(&maps[3], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, second, n, rank, groups, n * 2, n * 2 * rank, 64, box_rank, 1);
+    if (ms != RDOT_OK) return ms;
+    const cudaError_t e = launch_lora_tall(maps, a, C, deep, lora_timeout_ns(), s);
     return e == cudaSuccess ? RDOT_OK : cuda_fail(e, "lora launch");
 }
 }  // namespace
+
+rdot_status rdot_lora_read_status(int32_t* flags, void* stream) {
+    if (!flags) return RDOT_ERR_INVALID_ARG;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    int32_t v[2] = {0, 0}, *word[2];
+    cudaError_t e = lora_tall_status(&word[0]);
+    if (e == cudaSuccess) e = lora_grad_status(&word[1]);
+    for (int i = 0; i < 2 && e == cudaSuccess; ++i)
+        e = cudaMemcpyAsync(&v[i], word[i], sizeof v[i], cudaMemcpyDeviceToHost, s);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+    if (e != cudaSuccess) return cuda_fail(e, "rdot_lora_read_status");
+    *flags = v[0] | v[1];
+    return *flags & RDOT_STATUS_BIT_TIMEOUT ? RDOT_ERR_DEVICE_TIMEOUT : RDOT_OK;
+}
+
+rdot_status rdot_lora_clear_status(void* stream) {
+    int32_t* word[2];
+    cudaError_t e = lora_tall_status(&word[0]);
+    if (e == cudaSuccess) e = lora_grad_status(&word[1]);
+    for (int i = 0; i < 2 && e == cudaSuccess; ++i)
+        e = cudaMemsetAsync(word[i], 0, sizeof(int32_t), static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? RDOT_OK : cuda_fail(e, "rdot_lora_clear_status");
+}
+
+rdot_status rdot_lora_set_wait_timeout(uint64_t timeout_ns) {
+    g_lora_timeout_ns.store(timeout_ns);
+    return RDOT_OK;
+}
 
 rdot_status rdot_lora_forward(const void* x, const void* down, const void* up, const int32_t* group_sizes,
                               const int32_t* order, const float* scale, const void* base, int64_t m, int64_t k,
@@ -1643,7 +1714,7 @@ rdot_status rdot_lora_grad_weight(const void* t, const void* z, int32_t z_dtype,
     const int sms = current_sm_count();
     if (sms <= 0) return cuda_fail(cudaGetLastError(), "cudaDeviceGetAttribute");
     const LoraGradArgs a{t, z, z_scale, group_sizes, order, dw, static_cast<int>(m), static_cast<int>(width), groups, rank};
-    const cudaError_t e = launch_lora_grad(a, z_dtype == RDOT_E4M3, out_dtype == RDOT_BF16, sms,
+    const cudaError_t e = launch_lora_grad(a, z_dtype == RDOT_E4M3, out_dtype == RDOT_BF16, sms, lora_timeout_ns(),
                                            static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? RDOT_OK : cuda_fail(e, "lora weight gradient launch");
 }

@@ -269,7 +269,21 @@ struct LoraArgs {
     void* t;                     // device bf16 [M, rank], or null
     int M, K, N, G, rank;
 };
-cudaError_t launch_lora_apply(const LoraArgs& a, int sm_count, cudaStream_t stream);
+// Few rows: tiles of LORA_FEW_ROWS rows. C: blocks per cluster.
+cudaError_t launch_lora_apply(const LoraArgs& a, int C, cudaStream_t stream);
+constexpr int LORA_FEW_ROWS = 16;
+// Many rows, the tcgen05 form (lora_tall.cu): 128-row tiles. maps: x and base [M, width], boxes
+// (64, 32), neither read with an order; first and second [G, rank, width], boxes (64, lora_tall_box_rank, 1); all
+// 128-byte swizzled. Without a base its map is not read. C: blocks per cluster; deep: one block per SM with a
+// longer ring of stages, else two.
+cudaError_t launch_lora_tall(const CUtensorMap (&maps)[4], const LoraArgs& a, int C, bool deep, uint64_t timeout_ns,
+                             cudaStream_t stream);
+int lora_tall_box_rank(int rank);
+constexpr int LORA_TALL_ROWS = 128;
+constexpr int LORA_TALL_BOX_ROWS = 32;
+// The current device's status words of the tall form and of the weight gradient.
+cudaError_t lora_tall_status(int32_t** word);
+cudaError_t lora_grad_status(int32_t** word);
 
 // lora_grad.cu: dw[g] = sum over the sorted positions p of group g of t[p]^T z[order[p]].
 struct LoraGradArgs {
@@ -281,7 +295,8 @@ struct LoraGradArgs {
     void* dw;                    // device [G, rank, C], fp32 or bf16
     int M, C, G, rank;
 };
-cudaError_t launch_lora_grad(const LoraGradArgs& a, bool codes, bool out_bf16, int sm_count, cudaStream_t stream);
+cudaError_t launch_lora_grad(const LoraGradArgs& a, bool codes, bool out_bf16, int sm_count, uint64_t timeout_ns,
+                             cudaStream_t stream);
 
 // lora_group.cu: rows sorted by id (stable; ids outside [0, G) last), and the rows of each id.
 cudaError_t launch_lora_group(const int32_t* ids, int M, int G, int32_t* group_sizes, int32_t* order,

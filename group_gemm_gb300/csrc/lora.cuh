@@ -4,6 +4,7 @@
 
 #include <stdint.h>
 
+#include "kernels.h"
 #include "ptx.cuh"
 
 namespace rdot {
@@ -19,6 +20,11 @@ __device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, int byt
 }
 
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+
+// An arrival on `bar`, one of those it was initialised for, once this thread's copies so far have landed.
+__device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
 
 template <int N>
 __device__ __forceinline__ void cp_async_wait() {
@@ -67,9 +73,14 @@ __device__ __forceinline__ float4 ld_shared_cluster_f4(uint32_t addr) {
     return v;
 }
 
-// Sum over a block of 128 threads of `v`, and of the threads before this one. `part`: shared, 4 entries; the
-// caller synchronises between uses.
-__device__ __forceinline__ long long block_scan128(long long v, long long* part, long long* total) {
+__device__ __forceinline__ void st_shared_cluster_u4(uint32_t addr, const uint4& v) {
+    asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+
+// Sum over a block of THREADS threads of `v`, and of the threads before this one. `part`: shared, an entry a warp;
+// the caller synchronises between uses.
+template <int THREADS>
+__device__ __forceinline__ long long block_scan(long long v, long long* part, long long* total) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     long long incl = v;
 #pragma unroll
@@ -81,7 +92,7 @@ __device__ __forceinline__ long long block_scan128(long long v, long long* part,
     __syncthreads();
     long long before = 0, all = 0;
 #pragma unroll
-    for (int w = 0; w < 4; ++w) {
+    for (int w = 0; w < THREADS / 32; ++w) {
         before += w < warp ? part[w] : 0;
         all += part[w];
     }
@@ -90,7 +101,7 @@ __device__ __forceinline__ long long block_scan128(long long v, long long* part,
 }
 
 constexpr int LORA_THREADS = 128;
-constexpr int LORA_SIZES = 8;   // sizes a thread holds: 1024 groups
+constexpr int LORA_SIZES = 8;   // sizes a thread holds: 1024 groups over 128 threads
 
 // A block's tile: the rows of group g (G: rows of no group), sorted positions p0 .. p0 + rows - 1.
 struct LoraTile {
@@ -102,11 +113,12 @@ struct LoraTile {
 // Tile `w` of the rows cut into tiles of at most R rows that do not cross a group's end: the groups in
 // order, then the rows past the last one. rows = 0 past the last tile. A negative size counts as 0, ends are
 // clamped to M. Every thread gets the tile; all sizes are loaded at once, one pass.
-template <int R>
+template <int R, int THREADS>
 __device__ __forceinline__ LoraTile lora_find_tile(const int32_t* __restrict__ sizes, int G, int M, int w) {
-    __shared__ long long part[2][4];
+    static_assert(THREADS * LORA_SIZES >= RDOT_MAX_GROUPS, "every size has a thread");
+    __shared__ long long part[2][THREADS / 32];
     __shared__ LoraTile found;
-    const int per = (G + LORA_THREADS - 1) / LORA_THREADS;   // consecutive groups per thread, <= LORA_SIZES
+    const int per = (G + THREADS - 1) / THREADS;   // consecutive groups per thread, <= LORA_SIZES
     const int g0 = threadIdx.x * per;
     int s[LORA_SIZES];
     long long sum = 0;
@@ -116,7 +128,7 @@ __device__ __forceinline__ LoraTile lora_find_tile(const int32_t* __restrict__ s
     for (int i = 0; i < LORA_SIZES; ++i) sum += s[i];
     if (threadIdx.x == 0) found = LoraTile{G, 0, 0};
     long long total, tiles_total;
-    const long long first = block_scan128(sum, part[0], &total);
+    const long long first = block_scan<THREADS>(sum, part[0], &total);
     long long at = first, tiles = 0;
 #pragma unroll
     for (int i = 0; i < LORA_SIZES; ++i) {
@@ -124,7 +136,7 @@ __device__ __forceinline__ LoraTile lora_find_tile(const int32_t* __restrict__ s
         tiles += (e - b + R - 1) / R;
         at += s[i];
     }
-    long long t = block_scan128(tiles, part[1], &tiles_total);
+    long long t = block_scan<THREADS>(tiles, part[1], &tiles_total);
     if (w >= t && w < t + tiles) {
         at = first;
 #pragma unroll
@@ -146,6 +158,28 @@ __device__ __forceinline__ LoraTile lora_find_tile(const int32_t* __restrict__ s
     }
     __syncthreads();
     return found;
+}
+
+// Row numbers of a tile's sorted positions into shared memory, -1 for none (past the tile, or an entry of
+// `order` outside [0, M)). The caller synchronises.
+template <int R, int THREADS>
+__device__ __forceinline__ void lora_tile_rows(int* row_of, const LoraTile& tile, const int32_t* __restrict__ order, int M) {
+    for (int i = threadIdx.x; i < R; i += THREADS) {
+        int row = -1;
+        if (i < tile.rows) {
+            row = order ? __ldg(order + tile.p0 + i) : tile.p0 + i;
+            if (row < 0 || row >= M) row = -1;
+        }
+        row_of[i] = row;
+    }
+}
+
+// bf16 of a value and of what the rounding left, so that hi + lo has a relative error of 2^-16. Of an infinity or
+// NaN, hi alone.
+__device__ __forceinline__ void split_bf16x2(float a, float b, uint32_t& hi, uint32_t& lo) {
+    hi = pack_bf16x2(a, b);
+    const float fa = __uint_as_float(hi << 16), fb = __uint_as_float(hi & 0xffff0000u);
+    lo = pack_bf16x2(isfinite(fa) ? a - fa : 0.f, isfinite(fb) ? b - fb : 0.f);
 }
 
 }  // namespace rdot

@@ -1,17 +1,20 @@
-// lora_apply.cu -- low-rank adapters beside a projection: out = base + scale[g] (x first[g]^T) second[g].
+// lora_apply.cu -- low-rank adapters beside a projection: out = base + scale[g] (x first[g]^T) second[g]. The form for
+// few rows (lora_tall.cu: many).
 //
-// For a tile of R rows of one group the kernel forms t = scale[g] x first[g]^T (contraction over the K columns
-// of x) and then base + t second[g], in one launch and without t's round trip through memory. Both weights lie
+// For a tile of 16 rows of one group the kernel forms t = scale[g] x first[g]^T (contraction over the K columns of
+// x) and then base + t second[g], in one launch and without t's round trip through memory. Both weights lie
 // [G, r, width], their long axis contiguous, so the forward (first = down, second = up) and the gradient of the
-// input (first = up, second = down) are the same kernel. Up to 16 x 2 flops for a byte at rank 16: HBM is the
-// bound, and x, base and out pass once.
+// input (first = up, second = down) are the same kernel. With a row or two to an adapter it streams weights:
+// HBM's latency and rate bound it, not the MMAs (mma.sync, 16 x 8 x 16, half of a tile's rows empty or more).
 //
 // A cluster of C blocks takes a tile: each contracts its share of the columns of x, the fp32 partial sums are
 // added through distributed shared memory in a fixed order, and each then writes its share of the output's
-// columns. So a few rows still spread over many SMs, and results do not depend on timing.
+// columns. So a few rows still spread over many SMs, and results do not depend on timing. 64 rows over 256
+// adapters, 4096 -> 14336, rank 16: 20.4 us with C = 8, 72 us with C = 1. Stages of 128 columns, six in the ring:
+// 64 columns, four in the ring, 24.6 us.
 //
 // t keeps fp32 accuracy into the second product: it enters as two bf16 terms, t = hi + lo with lo the rounded
-// rest (relative error 2^-17, below the output's own rounding of 2^-9), two MMAs in place of one. hi is also
+// rest (relative error 2^-16, below the output's own rounding of 2^-8), two MMAs in place of one. hi is also
 // what is returned as t, the operand of the weight gradient.
 #include <cuda_bf16.h>
 
@@ -23,16 +26,15 @@ namespace rdot {
 
 namespace {
 
-template <int R_, int RP_>
+template <int RP_>
 struct ApplyCfg {
-    static constexpr int R = R_;                       // rows of a tile
+    static constexpr int R = LORA_FEW_ROWS;            // rows of a tile: an MMA's
     static constexpr int RP = RP_;                     // rank, rounded up
-    static constexpr int WR = R / 16;                  // warps along the rows
-    static constexpr int WK = 4 / WR;                  // warps along the columns (both products)
-    static constexpr int BK = RP <= 32 ? 128 : 64;     // columns per stage
+    static constexpr int WK = LORA_THREADS / 32;       // warps, along the columns in both products
+    static constexpr int BK = RP <= 64 ? 128 : 64;     // columns per stage
     static constexpr int PITCH = 2 * BK + 16;          // bytes: 16 off a multiple of 128, so ldmatrix has no conflicts
     static constexpr int SLOT = (R + RP) * PITCH;      // x or base rows, then weight rows
-    static constexpr int STAGES = RP == 16 || RP == 64 ? 4 : 3;
+    static constexpr int STAGES = RP <= 16 ? 6 : RP <= 32 ? 5 : RP <= 64 ? 4 : 5;
     static constexpr int PP = RP + 4;                  // pitch of the partial sums (fp32)
     static constexpr int TP = RP + 8;                  // pitch of hi and lo (bf16)
     static constexpr int PART = WK * R * PP * 4;
@@ -41,36 +43,30 @@ struct ApplyCfg {
 
 template <class Cfg>
 __global__ void __launch_bounds__(LORA_THREADS) lora_apply_kernel(LoraArgs a) {
-    constexpr int R = Cfg::R, RP = Cfg::RP, WR = Cfg::WR, WK = Cfg::WK, BK = Cfg::BK, PITCH = Cfg::PITCH;
+    constexpr int R = Cfg::R, RP = Cfg::RP, WK = Cfg::WK, BK = Cfg::BK, PITCH = Cfg::PITCH;
     constexpr int S = Cfg::STAGES, PP = Cfg::PP, TP = Cfg::TP;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ int row_of[R];   // each tile row's row of x, base and out; -1 for none
     float* part = reinterpret_cast<float*>(smem + S * Cfg::SLOT);
     uint16_t* thi = reinterpret_cast<uint16_t*>(smem + S * Cfg::SLOT + Cfg::PART);
     uint16_t* tlo = thi + R * TP;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int wr = warp % WR, wk = warp / WR;
+    const int tid = threadIdx.x, lane = tid & 31, wk = tid >> 5;
     const int C = static_cast<int>(cluster_ctas()), rank = static_cast<int>(cluster_ctarank());
 
     grid_dependency_enter();
-    const LoraTile tile = lora_find_tile<R>(a.group_sizes, a.G, a.M, static_cast<int>(blockIdx.x) / C);
+    const LoraTile tile = lora_find_tile<R, LORA_THREADS>(a.group_sizes, a.G, a.M, static_cast<int>(blockIdx.x) / C);
     if (tile.rows == 0) return;   // the whole cluster
     const bool live = tile.g < a.G;
-    for (int i = tid; i < R; i += LORA_THREADS) {
-        int row = -1;
-        if (i < tile.rows) {
-            row = a.order ? __ldg(a.order + tile.p0 + i) : tile.p0 + i;
-            if (row < 0 || row >= a.M) row = -1;
-        }
-        row_of[i] = row;
-    }
+    lora_tile_rows<R, LORA_THREADS>(row_of, tile, a.order, a.M);
     __syncthreads();
 
     const int nk = live ? (a.K + BK - 1) / BK : 0, nn = (a.N + BK - 1) / BK;
-    const int k0 = static_cast<int>(static_cast<long long>(nk) * rank / C), k1 = static_cast<int>(static_cast<long long>(nk) * (rank + 1) / C);
-    int n0 = static_cast<int>(static_cast<long long>(nn) * rank / C), n1 = static_cast<int>(static_cast<long long>(nn) * (rank + 1) / C);
-    if (!live && a.base == a.out) n1 = n0;   // rows without an adapter, in place: they stay as they are
-    const int first_stages = k1 - k0, stages = first_stages + n1 - n0;
+    // this block's stages: chunks rank, rank + C, ... of both widths, so that the cluster reads and writes
+    // neighbouring columns at a time
+    const int first_stages = nk > rank ? (nk - rank + C - 1) / C : 0;
+    int second_stages = nn > rank ? (nn - rank + C - 1) / C : 0;
+    if (!live && a.base == a.out) second_stages = 0;   // rows without an adapter, in place: they stay as they are
+    const int stages = first_stages + second_stages;
     const uint32_t ring = smem_u32(smem);
 
     // stage i of this block into its slot: 16-byte pieces, zeros outside the tensors
@@ -79,7 +75,7 @@ __global__ void __launch_bounds__(LORA_THREADS) lora_apply_kernel(LoraArgs a) {
             constexpr int V = BK / 8;   // pieces of a row
             const bool one = i < first_stages;
             const int width = one ? a.K : a.N;
-            const int c0 = (one ? k0 + i : n0 + i - first_stages) * BK + (tid % V) * 8;
+            const int c0 = ((one ? i : i - first_stages) * C + rank) * BK + (tid % V) * 8;
             const uint16_t* rows = static_cast<const uint16_t*>(one ? a.x : a.base);
             const uint16_t* weight = static_cast<const uint16_t*>(one ? a.first : a.second);
             const bool in = c0 < width;
@@ -114,7 +110,7 @@ __global__ void __launch_bounds__(LORA_THREADS) lora_apply_kernel(LoraArgs a) {
             __syncthreads();
             load(i + S - 1);
             const uint32_t slot = ring + (i % S) * Cfg::SLOT;
-            const uint32_t ax = slot + (wr * 16 + (lane & 15)) * PITCH + (lane >> 4) * 16;
+            const uint32_t ax = slot + (lane & 15) * PITCH + (lane >> 4) * 16;
             const uint32_t bx = slot + (R + (lane & 7) + ((lane >> 4) << 3)) * PITCH + ((lane >> 3) & 1) * 16;
 #pragma unroll
             for (int kk = wk; kk < BK / 16; kk += WK) {
@@ -130,7 +126,7 @@ __global__ void __launch_bounds__(LORA_THREADS) lora_apply_kernel(LoraArgs a) {
             }
         }
         // partial sums of the warps, then of the cluster's blocks
-        float* mine = part + wk * R * PP + (wr * 16 + (lane >> 2)) * PP + 2 * (lane & 3);
+        float* mine = part + wk * R * PP + (lane >> 2) * PP + 2 * (lane & 3);
 #pragma unroll
         for (int j = 0; j < RP / 8; ++j) {
             *reinterpret_cast<float2*>(mine + 8 * j) = make_float2(acc[j][0], acc[j][1]);
@@ -138,17 +134,15 @@ __global__ void __launch_bounds__(LORA_THREADS) lora_apply_kernel(LoraArgs a) {
         }
         __syncthreads();
         if (C > 1) {
-            if (WK > 1) {
-                for (int e = tid; e < R * RP / 4; e += LORA_THREADS) {
-                    float4* p = reinterpret_cast<float4*>(part + (e / (RP / 4)) * PP + 4 * (e % (RP / 4)));
-                    float4 s = *p;
+            for (int e = tid; e < R * RP / 4; e += LORA_THREADS) {
+                float4* p = reinterpret_cast<float4*>(part + (e / (RP / 4)) * PP + 4 * (e % (RP / 4)));
+                float4 s = *p;
 #pragma unroll
-                    for (int w = 1; w < WK; ++w) {
-                        const float4 v = p[w * R * PP / 4];
-                        s = make_float4(s.x + v.x, s.y + v.y, s.z + v.z, s.w + v.w);
-                    }
-                    *p = s;
+                for (int w = 1; w < WK; ++w) {
+                    const float4 v = p[w * R * PP / 4];
+                    s = make_float4(s.x + v.x, s.y + v.y, s.z + v.z, s.w + v.w);
                 }
+                *p = s;
             }
             cluster_sync();
         }
@@ -174,18 +168,11 @@ __global__ void __launch_bounds__(LORA_THREADS) lora_apply_kernel(LoraArgs a) {
             // ranks past the adapter's are 0 whatever x holds (there x times the zero weights may be NaN)
             const bool in = c < a.rank;
             const float v[4] = {in ? s.x * scale : 0.f, in ? s.y * scale : 0.f, in ? s.z * scale : 0.f, in ? s.w * scale : 0.f};
-            float rest[4];
-            uint2 hi;
-            hi.x = pack_bf16x2(v[0], v[1]);
-            hi.y = pack_bf16x2(v[2], v[3]);
-            const uint32_t h[2] = {hi.x, hi.y};
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float f = __uint_as_float(j & 1 ? h[j >> 1] & 0xffff0000u : h[j >> 1] << 16);
-                rest[j] = isfinite(f) ? v[j] - f : 0.f;   // an infinity or NaN is hi alone
-            }
+            uint2 hi, lo;
+            split_bf16x2(v[0], v[1], hi.x, lo.x);
+            split_bf16x2(v[2], v[3], hi.y, lo.y);
             *reinterpret_cast<uint2*>(thi + r * TP + c) = hi;
-            *reinterpret_cast<uint2*>(tlo + r * TP + c) = make_uint2(pack_bf16x2(rest[0], rest[1]), pack_bf16x2(rest[2], rest[3]));
+            *reinterpret_cast<uint2*>(tlo + r * TP + c) = lo;
             if (rank == 0 && a.t && r < tile.rows && in)
                 *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.t) + static_cast<long long>(tile.p0 + r) * a.rank + c) = hi;
         }
@@ -199,54 +186,76 @@ __global__ void __launch_bounds__(LORA_THREADS) lora_apply_kernel(LoraArgs a) {
             reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.t) + static_cast<long long>(tile.p0) * a.rank)[e] = make_uint2(0u, 0u);
     }
 
+    // t as MMA fragments: held in registers while they are few
+    constexpr bool KEEP = RP <= 32;
+    const uint32_t ahi = smem_u32(thi) + (lane & 15) * TP * 2 + (lane >> 4) * 16, alo = ahi + R * TP * 2;
+    uint32_t th[KEEP ? RP / 16 : 1][4], tl[KEEP ? RP / 16 : 1][4];
+    if (KEEP && live) {
+#pragma unroll
+        for (int kk = 0; kk < RP / 16; ++kk) {
+            ldmatrix_x4(th[kk], ahi + kk * 32);
+            ldmatrix_x4(tl[kk], alo + kk * 32);
+        }
+    }
     for (; i < stages; ++i) {
         cp_async_wait<S - 2>();
         __syncthreads();
         load(i + S - 1);
         uint8_t* slot = smem + (i % S) * Cfg::SLOT;
         const uint32_t bx = smem_u32(slot) + (R + (lane & 15)) * PITCH + (lane >> 4) * 16;
-        const uint32_t ahi = smem_u32(thi) + (wr * 16 + (lane & 15)) * TP * 2 + (lane >> 4) * 16;
-        const uint32_t alo = ahi + R * TP * 2;
         constexpr int COLS = BK / WK;   // this warp's columns of the stage
 #pragma unroll
         for (int n = 0; n < COLS; n += 16) {
-            float acc[2][4] = {};
+            if (!live && a.base) continue;   // a copy
+            // the sums start from base and go back to its place in the stage; a 32-bit word holds two columns of a lane
+            uint32_t* const p = reinterpret_cast<uint32_t*>(slot + (lane >> 2) * PITCH + (wk * COLS + n + 2 * (lane & 3)) * 2);
+            float acc[2][4];
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    const uint32_t b = a.base ? p[half * 2 * PITCH + 4 * h] : 0u;
+                    acc[h][2 * half] = __uint_as_float(b << 16);
+                    acc[h][2 * half + 1] = __uint_as_float(b & 0xffff0000u);
+                }
             if (live) {
 #pragma unroll
                 for (int kk = 0; kk < RP / 16; ++kk) {
-                    uint32_t fb[4], fh[4], fl[4];
+                    uint32_t fb[4];
                     ldmatrix_x4_trans(fb, bx + kk * 16 * PITCH + (wk * COLS + n) * 2);
-                    ldmatrix_x4(fh, ahi + kk * 32);
-                    ldmatrix_x4(fl, alo + kk * 32);
+                    uint32_t fh[4], fl[4];
+                    if (KEEP) {
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            fh[j] = th[KEEP ? kk : 0][j];
+                            fl[j] = tl[KEEP ? kk : 0][j];
+                        }
+                    } else {
+                        ldmatrix_x4(fh, ahi + kk * 32);
+                        ldmatrix_x4(fl, alo + kk * 32);
+                    }
                     mma_16816(acc[0], fh, fb[0], fb[1]);
                     mma_16816(acc[1], fh, fb[2], fb[3]);
                     mma_16816(acc[0], fl, fb[0], fb[1]);
                     mma_16816(acc[1], fl, fb[2], fb[3]);
                 }
             }
-            if (!live && a.base) continue;   // a copy
-            // onto base, in place in the stage; a 32-bit word holds two columns of one lane
 #pragma unroll
             for (int h = 0; h < 2; ++h)
 #pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    uint32_t* p = reinterpret_cast<uint32_t*>(slot + (wr * 16 + (lane >> 2) + 8 * half) * PITCH +
-                                                             (wk * COLS + n + 8 * h + 2 * (lane & 3)) * 2);
-                    const uint32_t b = a.base ? *p : 0u;
-                    *p = pack_bf16x2(__uint_as_float(b << 16) + acc[h][2 * half],
-                                     __uint_as_float(b & 0xffff0000u) + acc[h][2 * half + 1]);
-                }
+                for (int half = 0; half < 2; ++half)
+                    p[half * 2 * PITCH + 4 * h] = pack_bf16x2(acc[h][2 * half], acc[h][2 * half + 1]);
         }
         __syncwarp();
         // the warp's rows and columns of the stage, 16 bytes a lane
         constexpr int V = COLS / 8;
-        const int c0 = (n0 + i - first_stages) * BK + wk * COLS + (lane % V) * 8;
+        const int c0 = ((i - first_stages) * C + rank) * BK + wk * COLS + (lane % V) * 8;
 #pragma unroll
         for (int r = lane / V; r < 16; r += 32 / V) {
-            const int row = row_of[wr * 16 + r];
+            const int row = row_of[r];
             if (row >= 0 && c0 < a.N)
                 *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + static_cast<long long>(row) * a.N + c0) =
-                    *reinterpret_cast<const uint4*>(slot + (wr * 16 + r) * PITCH + (wk * COLS + (lane % V) * 8) * 2);
+                    *reinterpret_cast<const uint4*>(slot + r * PITCH + (wk * COLS + (lane % V) * 8) * 2);
         }
     }
     if (live && C > 1) cluster_wait();   // the others have read this block's sums
@@ -260,26 +269,16 @@ cudaError_t launch_cfg(const LoraArgs& a, long long tiles, int C, cudaStream_t s
     return launch_pdl_cluster(kern, dim3(static_cast<unsigned>(tiles * C)), dim3(LORA_THREADS), C, Cfg::SMEM, stream, a);
 }
 
-template <int R>
-cudaError_t launch_rows(const LoraArgs& a, int C, cudaStream_t stream) {
-    // a tile more for each group that ends inside one, one more for the rows of no group
-    const long long tiles = (static_cast<long long>(a.M) + R - 1) / R + (a.G < a.M ? a.G : a.M) + 1;
-    if (a.rank <= 16) return launch_cfg<ApplyCfg<R, 16>>(a, tiles, C, stream);
-    if (a.rank <= 32) return launch_cfg<ApplyCfg<R, 32>>(a, tiles, C, stream);
-    if (a.rank <= 64) return launch_cfg<ApplyCfg<R, 64>>(a, tiles, C, stream);
-    return launch_cfg<ApplyCfg<R, 128>>(a, tiles, C, stream);
-}
-
 }  // namespace
 
-cudaError_t launch_lora_apply(const LoraArgs& a, int sm_count, cudaStream_t stream) {
-    const long long groups = a.G < a.M ? a.G : a.M;         // groups that can have a row
-    const long long rows = (a.M + groups - 1) / groups;     // rows of an average one
-    const int R = rows <= 16 ? 16 : 64;
-    const long long tiles = groups * ((rows + R - 1) / R);
-    int C = 1;
-    while (C < 8 && tiles * C * 2 <= 2LL * sm_count) C *= 2;
-    return R == 16 ? launch_rows<16>(a, C, stream) : launch_rows<64>(a, C, stream);
+cudaError_t launch_lora_apply(const LoraArgs& a, int C, cudaStream_t stream) {
+    constexpr int R = LORA_FEW_ROWS;
+    // a tile more for each group that ends inside one, one more for the rows of no group
+    const long long tiles = (static_cast<long long>(a.M) + R - 1) / R + (a.G < a.M ? a.G : a.M) + 1;
+    if (a.rank <= 16) return launch_cfg<ApplyCfg<16>>(a, tiles, C, stream);
+    if (a.rank <= 32) return launch_cfg<ApplyCfg<32>>(a, tiles, C, stream);
+    if (a.rank <= 64) return launch_cfg<ApplyCfg<64>>(a, tiles, C, stream);
+    return launch_cfg<ApplyCfg<128>>(a, tiles, C, stream);
 }
 
 }  // namespace rdot

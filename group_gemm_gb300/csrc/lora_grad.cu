@@ -2,43 +2,63 @@
 //
 // With t = scale x down^T the gradient of up is t^T dy, and with dt = scale dy up^T that of down is dt^T x: one
 // kernel, [rank x C] sums for each group. z is bf16 or an 8-bit checkpoint (E4M3 codes with a scale per row
-// and 32 columns): the codes are widened to bf16 in registers, exactly, between shared memory and the MMA, so
-// the activation is never written in 16 bits. The scales do not run along the contraction, so the
-// block-scaled MMAs cannot take them.
+// and 32 columns), widened to bf16 on the way to shared memory, so the activation is never written in 16 bits.
+// The scales do not run along the contraction, so the block-scaled MMAs cannot take them.
 //
-// A block takes 128 columns of a group (each z element is read once; t, C/128 times from L2), a cluster
-// divides the group's rows. The fp32 partial sums of its blocks are added through distributed shared memory
-// in rank order: no atomics, the same result every time. HBM bounds it.
+// A work item is 128 columns of a group: D [128 columns x rank] in tensor memory, z as the MMA's A operand and t
+// as its B, both as they lie in memory (MN-major), 64 rows a stage. z is read once; t, C/128 times from L2.
+// Persistent blocks, one per SM, 19 warps:
+//   warps 0..13   loaders, seven teams of two warps that take the stages in turn: z and t by asynchronous 16-byte
+//                 copies into swizzled slots, zeros past the group's last row; codes instead through registers, a
+//                 team's next stage while it widens the last. They run ahead over the items' ends, so short
+//                 groups follow one another without a pause. (All loaders on every stage: 51 us against
+//                 33 for 16384 x 4096 codes, rank 16; each stage's waits then lie in a row.)
+//   warp 14       tcgen05.mma into one of four accumulators
+//   warps 15..18  epilogue: a lane a column, so that each rank's row of dw is stored in whole lines
+// Few items: a cluster divides the group's rows, a block a share, and adds the fp32 partial sums through distributed
+// shared memory in rank order. No atomics: the same result every time. HBM bounds it.
 #include <cuda_bf16.h>
 
 #include "kernels.h"
 #include "lora.cuh"
+#include "mxfp4.cuh"
 #include "pdl.cuh"
 
 namespace rdot {
 
 namespace {
 
-constexpr int GC = 128;    // columns of a block
-constexpr int GR = 64;     // rows of a stage
+constexpr int GC = 128;           // columns of an item
+constexpr int GR = 64;            // rows of a stage
+constexpr int LT = 64;            // threads of a team of loaders
+constexpr int CHUNK = GR * 128;   // 64 columns x 64 rows of bf16: 8 KB
+constexpr int ROW_RING = 4;       // a team's stages whose row numbers are held
+constexpr int ACCS = 4;           // accumulators
+constexpr int MASKS = 16;         // items whose NaN columns are held
 
-template <int RP_, bool CODES_>
+__device__ int32_t g_status;      // bits of the waits that ran out, until they are cleared
+
+template <int RP_, bool CODES_, bool ORDER_>
 struct GradCfg {
     static constexpr int RP = RP_;
     static constexpr bool CODES = CODES_;
-    static constexpr int ZP = (CODES ? GC : 2 * GC) + 16;   // pitches in bytes, 16 off a multiple of 128
-    static constexpr int TP = 2 * RP + 16;
-    static constexpr int SCALES = CODES ? GR * 9 + 64 : 0;  // a row: two aligned words that hold its four scales, their place
-    static constexpr int SLOT = GR * (ZP + TP) + SCALES;
-    static constexpr int STAGES = RP <= 32 ? 4 : 3;
-    static constexpr int PP = GC + 4;                       // pitch of the sums (fp32)
-    static constexpr int RING = STAGES * SLOT;
-    static constexpr int SMEM = RING > RP * PP * 4 ? RING : RP * PP * 4;
+    static constexpr bool ORDER = ORDER_;
+    static constexpr int TCHUNKS = (RP + 63) / 64;
+    static constexpr int SLOT = (2 + TCHUNKS) * CHUNK;
+    static constexpr int S = RP <= 64 ? 8 : 6;
+    // 14 loader warps: with the other five, five to a quarter of the SM leave 96 registers a thread
+    static constexpr int TEAMS = RP <= 64 ? 7 : 6;
+    static constexpr int LOADERS = TEAMS * LT / 32;
+    static constexpr int THREADS = 32 * (LOADERS + 5);
+    // A team that reaches stage u has passed the wait of stage u - TEAMS, so stage u - TEAMS - S has been read. That must
+    // cover stage u - 2S, else its wait could take the slot's phase before last for the last.
+    static_assert(TEAMS <= S, "a wait tells two phases of a slot apart");
+    static constexpr int RING = S * SLOT;                        // also the cluster's partial sums: RP x 512 bytes
+    static constexpr int ROWS_BYTES = ORDER ? TEAMS * ROW_RING * GR * 4 : 0;
+    static constexpr int SMEM = 1024 + RING + ROWS_BYTES;        // and the G + 1 offsets
+    static constexpr uint32_t TMEM_COLS = RP <= 16 ? 128 : ACCS * RP;   // (they are read 32 columns at a time)
+    static_assert(RP * 512 <= RING, "the partial sums fit the ring");
 };
-
-// Two E4M3 codes (bytes 1 and 3 of v) as bf16 times 2^-120: the exponent and mantissa bits move to the
-// bf16 field's low end, subnormals and all.
-__device__ __forceinline__ uint32_t widen_e4m3x2(uint32_t v) { return (v & 0x80008000u) | ((v >> 4) & 0x07f007f0u); }
 
 __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
     uint32_t r;
@@ -46,217 +66,457 @@ __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
     return r;
 }
 
-// Nonzero where one of four codes is NaN.
-__device__ __forceinline__ uint32_t nan_code(uint32_t w) { return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u; }
+// Two E4M3 codes, bytes J and J + 1 of w, as a bf16 pair times 2^-120. A code, sign-extended to 16 bits and moved up
+// by four, has its sign, exponent and mantissa where bf16 has its sign, low exponent bits and high mantissa bits,
+// subnormals included.
+template <int J>
+__device__ __forceinline__ uint32_t widen_e4m3x2(uint32_t w) {
+    uint32_t v;   // selector bit 3: the byte's sign, eight times
+    asm("prmt.b32 %0, %1, %1, %2;" : "=r"(v) : "r"(w), "n"(J | (J | 8) << 4 | (J + 1) << 8 | ((J + 1) | 8) << 12));
+    return (v * 16u) & 0x87f087f0u;
+}
 
-// 2^(s - 127) as bf16, 255 NaN.
-__device__ __forceinline__ uint32_t scale_bf16(uint32_t s) { return s == 0u ? 0x0040u : s == 255u ? 0x7fffu : s << 7; }
+// Bit 7 of each byte: whether the code there is NaN (magnitude 127).
+__device__ __forceinline__ uint32_t nan_code(uint32_t w) { return (w & 0x7f7f7f7fu) + 0x01010101u; }
+
+// What a block's items are cut from: item i is column block i % blocks of group i / blocks.
+struct Items {
+    const int32_t* off;     // [G + 1] shared: the groups' first positions
+    int G, blocks;
+    int dg, dcb;            // from one of the block's items to its next: groups, column blocks (no division on the way)
+    int rank, shift;        // the block's share of a group's stages: part `rank` of 2^shift
+
+    // The block's rows of group g: n from sorted position p0 on.
+    __device__ __forceinline__ void share(int g, int& p0, int& n) const {
+        p0 = off[g];
+        n = off[g + 1] - p0;
+        if (shift == 0) return;
+        const long long all = (static_cast<long long>(n) + GR - 1) / GR;
+        const long long s0 = all * rank >> shift, s1 = all * (rank + 1) >> shift;
+        p0 += static_cast<int>(s0 * GR);
+        n = static_cast<int>(min(s1 * GR, static_cast<long long>(n)) - s0 * GR);
+    }
+    __device__ __forceinline__ void step(int& g, int& cb) const {
+        g += dg;
+        cb += dcb;
+        if (cb >= blocks) {
+            cb -= blocks;
+            ++g;
+        }
+    }
+};
+
+// A place among the stages of a block's items.
+struct Stage {
+    int g, cb;      // the item after the current one
+    int p0 = 0;     // the stage's first sorted position
+    int n = 0;      // rows from there to the end of the block's share of the item; 0: no stage
+    int c0 = 0;     // the item's first column
+    int count = -1; // items with a row up to this one, less one
+
+    // k >= 1 stages on: the stage's rows are p0 .. p0 + min(n, GR) - 1. False past the last (n is then 0).
+    __device__ __forceinline__ bool advance(const Items& it, int k) {
+        while (true) {
+            const int left = n > GR ? (n - 1) / GR : 0;   // stages of this item after the current one
+            if (k <= left) {
+                p0 += k * GR;
+                n -= k * GR;
+                return true;
+            }
+            k -= left + 1;
+            n = 0;
+            while (n == 0) {
+                if (g >= it.G) return false;
+                c0 = cb * GC;
+                it.share(g, p0, n);
+                it.step(g, cb);
+            }
+            ++count;
+            if (k == 0) return true;
+        }
+    }
+};
 
 template <class Cfg>
-__global__ void __launch_bounds__(LORA_THREADS) lora_grad_kernel(LoraGradArgs a, int blocks, bool out_bf16) {
-    constexpr int RP = Cfg::RP, ZP = Cfg::ZP, TP = Cfg::TP, S = Cfg::STAGES, PP = Cfg::PP;
-    extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ long long scan_part[4];
+__global__ void __launch_bounds__(Cfg::THREADS, 1) lora_grad_kernel(LoraGradArgs a, int blocks, bool out_bf16, uint64_t timeout_ns) {
+    constexpr int RP = Cfg::RP, S = Cfg::S, TEAMS = Cfg::TEAMS, LOADERS = Cfg::LOADERS, THREADS = Cfg::THREADS;
+    constexpr bool CODES = Cfg::CODES, ORDER = Cfg::ORDER;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    int* rows = reinterpret_cast<int*>(smem + Cfg::RING);
+    int32_t* off = reinterpret_cast<int32_t*>(smem + Cfg::RING + Cfg::ROWS_BYTES);
+    __shared__ __align__(8) uint64_t full[S], empty[S], acc_full[ACCS], acc_empty[ACCS], drain;
+    __shared__ long long scan_part[THREADS / 32];
+    __shared__ uint32_t tmem_holder;
+    __shared__ uint32_t nan_cols[MASKS][GC / 32];
+    __shared__ int abort_flag;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int C = static_cast<int>(cluster_ctas()), rank = static_cast<int>(cluster_ctarank());
-    const int item = static_cast<int>(blockIdx.x) / C;
-    const int g = item / blocks, cb = item % blocks;
 
-    grid_dependency_enter();
-    // the group's first position: the sizes before it, each at least 0
-    long long before = 0;
-    for (int i = tid; i < g; i += LORA_THREADS) before += max(__ldg(a.group_sizes + i), 0);
-    long long total;
-    block_scan128(before, scan_part, &total);
-    const int p0 = static_cast<int>(min(total, static_cast<long long>(a.M)));
-    const int n = static_cast<int>(min(static_cast<long long>(max(__ldg(a.group_sizes + g), 0)), static_cast<long long>(a.M - p0)));
-    const long long all = (static_cast<long long>(n) + GR - 1) / GR;   // stages of the group
-    const long long s0 = all * rank / C, s1 = all * (rank + 1) / C;
-    const int stages = static_cast<int>(s1 - s0);
-    const uint32_t ring = smem_u32(smem);
-    const int sb = a.C / 32;   // scales of a row
-
-    // row of z at place q of the group, -1 for none
-    const auto row_at = [&](long long q) -> long long {
-        if (q >= n) return -1;
-        if (!a.order) return p0 + q;
-        const int row = __ldg(a.order + p0 + q);
-        return row >= 0 && row < a.M ? row : -1;
-    };
-    const auto load = [&](int i) {
-        if (i < stages) {
-            constexpr int V = Cfg::CODES ? GC / 16 : GC / 8;   // 16-byte pieces of a row of z
-            const uint32_t slot = ring + (i % S) * Cfg::SLOT;
-            const long long q0 = (s0 + i) * GR;                // the stage's first row of the group
-            const int c0 = cb * GC + (tid % V) * (Cfg::CODES ? 16 : 8);
-            constexpr int ESIZE = Cfg::CODES ? 1 : 2;
-#pragma unroll
-            for (int r = tid / V; r < GR; r += LORA_THREADS / V) {
-                const long long row = row_at(q0 + r);
-                const bool ok = row >= 0 && c0 < a.C;
-                cp_async16(slot + r * ZP + (tid % V) * 16,
-                           static_cast<const uint8_t*>(a.z) + (ok ? (row * a.C + c0) * ESIZE : 0), ok);
-            }
-            constexpr int W = RP / 8;
-            for (int e = tid; e < GR * W; e += LORA_THREADS) {
-                const int r = e / W, j = 8 * (e % W);
-                const bool ok = j < a.rank && row_at(q0 + r) >= 0;
-                cp_async16(slot + GR * ZP + r * TP + 2 * j,
-                           static_cast<const uint16_t*>(a.t) + (ok ? (p0 + q0 + r) * a.rank + j : 0), ok);
-            }
-            if (Cfg::CODES) {
-                // a row's scales start at any byte: the two aligned words around them, cut at the tensor's end
-                const int r = tid >> 1, w = tid & 1;
-                const long long row = row_at(q0 + r);
-                const long long at = ((row * sb + 4 * cb) & ~3LL) + 4 * w;
-                const long long left = static_cast<long long>(a.M) * sb - at;
-                const int bytes = row < 0 || left <= 0 ? 0 : left < 4 ? static_cast<int>(left) : 4;
-                cp_async4(slot + GR * (ZP + TP) + r * 8 + 4 * w, a.z_scale + (bytes ? at : 0), bytes);
-                if (w == 0) smem[(i % S) * Cfg::SLOT + GR * (ZP + TP + 8) + r] = static_cast<uint8_t>((row * sb) & 3);
-            }
+    if (tid == 0) {
+        for (int s = 0; s < S; ++s) {
+            mbar_init(&full[s], LT / 32);   // a team's warps
+            mbar_init(&empty[s], 1);
         }
-        cp_async_commit();
-    };
-
-    float acc[RP / 16][4][4] = {};
-    if (all > 0) {
-#pragma unroll
-        for (int i = 0; i < S - 1; ++i) load(i);
-        for (int i = 0; i < stages; ++i) {
-            cp_async_wait<S - 2>();
-            __syncthreads();
-            load(i + S - 1);
-            const uint8_t* slot = smem + (i % S) * Cfg::SLOT;
-            const uint32_t zs = smem_u32(slot), ts = zs + GR * ZP;
-#pragma unroll
-            for (int kk = 0; kk < GR / 16; ++kk) {
-                uint32_t fb[4][2];   // z: 16 rows x 32 columns, four tiles of 8
-                if (Cfg::CODES) {
-                    // lane (q, c): rows 2q, 2q + 1, 2q + 8, 2q + 9; columns 4c .. 4c + 3, column 4c + j in tile j
-                    const int q = lane & 3, c = lane >> 2;
-                    const uint8_t* p = slot + (16 * kk + 2 * q) * ZP + 32 * warp + 4 * c;
-                    uint32_t w[4], sc[4];
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const int r = 16 * kk + 2 * q + (j & 1) + 8 * (j >> 1);
-                        w[j] = *reinterpret_cast<const uint32_t*>(p + ((j & 1) + 8 * (j >> 1)) * ZP);
-                        const int off = (sb & 3) != 0 ? slot[GR * (ZP + TP + 8) + r] : 0;
-                        sc[j] = scale_bf16(slot[GR * (ZP + TP) + r * 8 + off + warp]);
-                    }
-                    const uint32_t up = 0x7b807b80u;   // 2^120 twice
-                    const uint32_t sa = sc[0] | sc[1] << 16, sd = sc[2] | sc[3] << 16;
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        // byte j of two rows to bytes 1 and 3
-                        const uint32_t sel = j | j << 4 | (4 + j) << 8 | (4 + j) << 12;
-                        fb[j][0] = mul_bf16x2(mul_bf16x2(widen_e4m3x2(__byte_perm(w[0], w[1], sel)), up), sa);
-                        fb[j][1] = mul_bf16x2(mul_bf16x2(widen_e4m3x2(__byte_perm(w[2], w[3], sel)), up), sd);
-                    }
-                    if (nan_code(w[0]) | nan_code(w[1]) | nan_code(w[2]) | nan_code(w[3])) {
-                        // code 0x7f or 0xff is NaN (the quantiser writes none)
-#pragma unroll
-                        for (int j = 0; j < 4; ++j)
-#pragma unroll
-                            for (int k = 0; k < 4; ++k)
-                                if ((w[k] >> (8 * j) & 0x7fu) == 0x7fu) fb[j][k >> 1] |= 0x7fffu << (16 * (k & 1));
-                    }
-                } else {
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        uint32_t f[4];
-                        ldmatrix_x4_trans(f, zs + (16 * kk + (lane & 15)) * ZP + (32 * warp + 16 * h + 8 * (lane >> 4)) * 2);
-                        fb[2 * h][0] = f[0];
-                        fb[2 * h][1] = f[1];
-                        fb[2 * h + 1][0] = f[2];
-                        fb[2 * h + 1][1] = f[3];
-                    }
-                }
-#pragma unroll
-                for (int m = 0; m < RP / 16; ++m) {
-                    // t^T: 16 ranks x 16 rows
-                    uint32_t fa[4];
-                    ldmatrix_x4_trans(fa, ts + (16 * kk + (lane & 7) + ((lane >> 4) << 3)) * TP +
-                                              (16 * m + 8 * ((lane >> 3) & 1)) * 2);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) mma_16816(acc[m][j], fa, fb[j][0], fb[j][1]);
-                }
-            }
+        for (int i = 0; i < ACCS; ++i) {
+            mbar_init(&acc_full[i], 1);
+            mbar_init(&acc_empty[i], 4);
         }
-        cp_async_wait<0>();
-        __syncthreads();   // the ring becomes the sums
-        float* sums = reinterpret_cast<float*>(smem);
-        const int q = lane & 3;
-#pragma unroll
-        for (int m = 0; m < RP / 16; ++m)
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                float* row = sums + (16 * m + (lane >> 2) + 8 * half) * PP + 32 * warp;
-                if (Cfg::CODES) {   // columns 2q and 2q + 1 of tile j: 8q + j, 8q + 4 + j
-                    *reinterpret_cast<float4*>(row + 8 * q) =
-                        make_float4(acc[m][0][2 * half], acc[m][1][2 * half], acc[m][2][2 * half], acc[m][3][2 * half]);
-                    *reinterpret_cast<float4*>(row + 8 * q + 4) = make_float4(
-                        acc[m][0][2 * half + 1], acc[m][1][2 * half + 1], acc[m][2][2 * half + 1], acc[m][3][2 * half + 1]);
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        *reinterpret_cast<float2*>(row + 8 * j + 2 * q) = make_float2(acc[m][j][2 * half], acc[m][j][2 * half + 1]);
-                }
-            }
-        if (C > 1) cluster_sync();
-        else __syncthreads();
+        mbar_init(&drain, 1);
+        abort_flag = 0;
+        fence_mbar_init();
     }
-    // this block's share of the rows of dw[g], zeros for an empty group
-    constexpr int V = GC / 4;
-    const int r0 = a.rank * rank / C, r1 = a.rank * (rank + 1) / C;
-    const int c0 = cb * GC + 4 * (tid % V);
-    for (int r = r0 + tid / V; r < r1; r += LORA_THREADS / V) {
-        float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (all > 0) {
-            const uint32_t addr = smem_u32(smem) + (r * PP + 4 * (tid % V)) * 4;
+    if (tid < MASKS * (GC / 32)) nan_cols[tid / (GC / 32)][tid % (GC / 32)] = 0;
+    if (warp == LOADERS) {
+        tmem_alloc(&tmem_holder, Cfg::TMEM_COLS);
+        tmem_relinquish();
+    }
+    grid_dependency_enter();
+    {
+        // the groups' first positions, ends clamped to M, a negative size as 0
+        constexpr int PER = (RDOT_MAX_GROUPS + THREADS - 1) / THREADS;
+        long long v[PER], sum = 0, total;
+#pragma unroll
+        for (int j = 0; j < PER; ++j) {
+            const int i = tid * PER + j;
+            v[j] = i < a.G ? max(__ldg(a.group_sizes + i), 0) : 0;
+        }
+#pragma unroll
+        for (int j = 0; j < PER; ++j) sum += v[j];
+        long long at = block_scan<THREADS>(sum, scan_part, &total);
+#pragma unroll
+        for (int j = 0; j < PER; ++j) {
+            const int i = tid * PER + j;
+            if (i < a.G) off[i] = static_cast<int32_t>(min(at, static_cast<long long>(a.M)));
+            at += v[j];
+        }
+        if (tid == 0) off[a.G] = static_cast<int32_t>(min(total, static_cast<long long>(a.M)));
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = tmem_holder;
+    const WaitGuard guard{&abort_flag, &g_status, timeout_ns};
+    const int shift = 31 - __clz(C);   // C is a power of two
+    const int first = static_cast<int>(blockIdx.x) >> shift, step = static_cast<int>(gridDim.x) >> shift;
+    const int first_g = first / blocks, first_cb = first - first_g * blocks;
+    const Items it{off, a.G, blocks, step / blocks, step % blocks, rank, shift};
+    const int ranks = (a.rank + 15) & ~15;   // the MMAs' N; t's columns past the rank are zeros
+
+    if (warp < LOADERS) {
+        // ---------------------------------------------------------------- loaders
+        const int team = tid / LT, lt = tid % LT;
+        Stage st{first_g, first_cb};   // the team's stage, and its next ones
+        bool run = st.advance(it, 1 + team);
+        Stage nx = st;
+        if (!run || !nx.advance(it, TEAMS)) nx.n = 0;
+        Stage far = nx;      // with `order`, of the row numbers: two of the team's stages on
+        bool stopped = false;      // a wait ran out: with `order` the warp still meets the team at its barrier
+        int* own_rows = rows + team * ROW_RING * GR;
+        static_assert(LT == GR, "a thread a row number");
+        const auto row_at = [&](const Stage& s, int i, int r) -> int {   // row of z for row r of the team's stage i, -1 for none
+            if (r >= s.n) return -1;
+            if (!ORDER) return s.p0 + r;
+            const int row = own_rows[(i % ROW_RING) * GR + r];
+            return row < a.M ? max(row, -1) : -1;
+        };
+        const auto row_number = [&](const Stage& s) -> int { return lt < s.n ? __ldg(a.order + s.p0 + lt) : -1; };
+        const auto team_sync = [&] { asm volatile("bar.sync %0, %1;" ::"r"(1 + team), "n"(LT) : "memory"); };
+        int number = -1;           // this thread's row number of the stage after the next
+        if (ORDER) {
+            own_rows[lt] = row_number(st);
+            own_rows[GR + lt] = row_number(nx);
+            if (far.n == 0 || !far.advance(it, TEAMS)) far.n = 0;
+            number = row_number(far);
+            team_sync();
+        }
+        // t's rows of the team's stage i into its slot
+        constexpr int W = RP / 8;
+        const auto load_t = [&](int i, uint32_t slot) {
+#pragma unroll
+            for (int e = lt; e < GR * W; e += LT) {
+                const int r = e / W, j = e % W;
+                const bool ok = 8 * j < a.rank && row_at(st, i, r) >= 0;
+                cp_async16(slot + (2 + (j >> 3)) * CHUNK + r * 128 + (((j & 7) ^ (r & 7)) << 4),
+                           static_cast<const uint16_t*>(a.t) + (ok ? static_cast<long long>(st.p0 + r) * a.rank + 8 * j : 0), ok);
+            }
+        };
+        // codes: eight pieces of 16 a row, rows lt / 8, lt / 8 + 8, ...; a piece and its scale byte in registers
+        constexpr int Q = CODES ? GR / 8 : 1;
+        const int piece = CODES ? lt & 7 : lt & 15, r0 = CODES ? lt >> 3 : lt >> 4;
+        const int sb = a.C / 32;   // scales of a row
+        uint4 code[Q];
+        uint32_t scale[Q];
+        const auto fetch = [&](const Stage& s, int i) {
+            const int c = s.c0 + 16 * piece;
+            if (!ORDER && s.n >= GR && c < a.C) {   // whole stages: a step along the rows
+                const uint8_t* p = static_cast<const uint8_t*>(a.z) + static_cast<long long>(s.p0 + r0) * a.C + c;
+                const uint8_t* ps = a.z_scale + static_cast<long long>(s.p0 + r0) * sb + (c >> 5);
+#pragma unroll
+                for (int k = 0; k < Q; ++k, p += 8 * static_cast<long long>(a.C), ps += 8 * sb) {
+                    code[k] = __ldg(reinterpret_cast<const uint4*>(p));
+                    scale[k] = __ldg(ps);
+                }
+                return;
+            }
+#pragma unroll
+            for (int k = 0; k < Q; ++k) {
+                const int row = c < a.C ? row_at(s, i, r0 + 8 * k) : -1;
+                code[k] = make_uint4(0u, 0u, 0u, 0u);
+                scale[k] = 127u;
+                if (row >= 0) {
+                    code[k] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(a.z) + static_cast<long long>(row) * a.C + c));
+                    scale[k] = __ldg(a.z_scale + static_cast<long long>(row) * sb + (c >> 5));
+                }
+            }
+        };
+        uint32_t seen[4] = {};   // bit 7 of a byte: a NaN code in that column of the item
+        if (CODES) fetch(st, 0);
+        for (int i = 0; run; ++i) {   // the team's stage i, the block's stage u
+            const int u = team + TEAMS * i, slot = u % S;
+            const bool next = nx.n > 0;
+            stopped = stopped || !mx4_wait_uniform(&empty[slot], ((u / S) & 1) ^ 1, guard);
+            if (stopped && !ORDER) break;
+            uint8_t* dst = smem + slot * Cfg::SLOT;
+            if (!stopped) {
+                load_t(i, smem_u32(dst));
+                if constexpr (!CODES) {
+                    const int c = st.c0 + 8 * piece;
+#pragma unroll
+                    for (int k = 0; k < GR / 4; ++k) {
+                        const int r = r0 + 4 * k, row = row_at(st, i, r);
+                        const bool ok = row >= 0 && c < a.C;
+                        cp_async16(smem_u32(dst) + (piece >> 3) * CHUNK + r * 128 + (((piece & 7) ^ (r & 7)) << 4),
+                                   static_cast<const uint16_t*>(a.z) + (ok ? static_cast<long long>(row) * a.C + c : 0), ok);
+                    }
+                }
+                cp_async_commit();
+            }
+            if constexpr (CODES) {
+#pragma unroll
+                for (int k = 0; k < Q; ++k) {
+                    const uint4 q = code[k];
+                    const uint32_t s = scale[k], s1 = min(s, 134u);
+                    seen[0] |= nan_code(q.x);
+                    seen[1] |= nan_code(q.y);
+                    seen[2] |= nan_code(q.z);
+                    seen[3] |= nan_code(q.w);
+                    // 2^120 x 2^(s - 127), in two steps where bf16 does not hold it
+                    const uint32_t f = (s1 + 120u) * 0x00800080u;
+                    uint32_t v[8] = {widen_e4m3x2<0>(q.x), widen_e4m3x2<2>(q.x), widen_e4m3x2<0>(q.y), widen_e4m3x2<2>(q.y),
+                                     widen_e4m3x2<0>(q.z), widen_e4m3x2<2>(q.z), widen_e4m3x2<0>(q.w), widen_e4m3x2<2>(q.w)};
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) v[j] = mul_bf16x2(v[j], f);
+                    if (s > 134u) {
+                        const uint32_t f2 = s == 255u ? 0x7fff7fffu : (s - s1 + 127u) * 0x00800080u;
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) v[j] = mul_bf16x2(v[j], f2);
+                    }
+                    const int r = r0 + 8 * k, unit = 2 * (piece & 3);
+                    uint8_t* row = dst + (piece >> 2) * CHUNK + r * 128;
+                    if (!stopped) {
+                        *reinterpret_cast<uint4*>(row + ((unit ^ (r & 7)) << 4)) = make_uint4(v[0], v[1], v[2], v[3]);
+                        *reinterpret_cast<uint4*>(row + (((unit + 1) ^ (r & 7)) << 4)) = make_uint4(v[4], v[5], v[6], v[7]);
+                    }
+                }
+                if (!next || nx.count != st.count) {
+                    // the team's last stage of the item. A NaN code went in as 480 x scale: its column's sums are NaN
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const uint32_t m = seen[j] & 0x80808080u;
+                        if (m) {
+                            const uint32_t bits = (m >> 7 & 1u) | (m >> 14 & 2u) | (m >> 21 & 4u) | (m >> 28 & 8u);
+                            atomicOr(&nan_cols[st.count % MASKS][piece >> 1], bits << (16 * (piece & 1) + 4 * j));
+                        }
+                        seen[j] = 0;
+                    }
+                }
+                fetch(nx, i + 1);
+            }
+            // the stage has landed; written in the generic proxy, read by the MMAs in the async one. (The fence once for all
+            // by the MMA warp: 0.35 us a stage, which it bound.)
+            cp_async_wait<0>();
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0 && !stopped) mbar_arrive(&full[slot]);
+            run = next;
+            st = nx;
+            if (ORDER) {
+                own_rows[((i + 2) % ROW_RING) * GR + lt] = number;
+                nx = far;
+                if (far.n == 0 || !far.advance(it, TEAMS)) far.n = 0;
+                number = row_number(far);
+                team_sync();
+            } else if (nx.n == 0 || !nx.advance(it, TEAMS)) {
+                nx.n = 0;
+            }
+        }
+        __syncwarp();
+    } else if (warp == LOADERS) {
+        // ---------------------------------------------------------------- MMA issuer (uniform, one lane elected)
+        const bool elected = elect_one();
+        const uint32_t idesc = idesc_f16(GC, ranks, true, true, true, true), ring = smem_u32(smem);
+        Stage st{first_g, first_cb};
+        bool fresh = true;
+        for (int u = 0; st.advance(it, 1); ++u) {
+            const int slot = u % S, b = st.count % ACCS;
+            if (fresh && !mx4_wait_uniform(&acc_empty[b], ((st.count / ACCS) & 1) ^ 1, guard)) break;
+            if (!mx4_wait_uniform(&full[slot], (u / S) & 1, guard)) break;
+            tc_fence_after();
+            const uint32_t sa = ring + slot * Cfg::SLOT, sb = sa + 2 * CHUNK;
+            if (elected) {
+#pragma unroll
+                for (int kk = 0; kk < GR / 16; ++kk)   // 16 rows: two groups of 8, 2 KB
+                    mma_f16(tmem + b * RP, smem_desc_sw128(sa + kk * 2048, CHUNK, 1024), smem_desc_sw128(sb + kk * 2048, CHUNK, 1024),
+                            idesc, !fresh || kk != 0 ? 1u : 0u);
+                mma_commit(&empty[slot]);
+                if (st.n <= GR) mma_commit(&acc_full[b]);
+            }
+            __syncwarp();
+            fresh = st.n <= GR;
+        }
+        // all MMAs issued by this thread complete before teardown frees tensor memory
+        if (elected) {
+            mma_commit(&drain);
+            int dummy;
+            (void)mbar_wait(&drain, 0, drain_guard(guard, &dummy));
+        }
+        __syncwarp();
+    } else {
+        // ---------------------------------------------------------------- epilogue
+        const int q = warp & 3;                        // the lane quarter of tensor memory that this warp may read
+        const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * q) << 16);
+        float* part = reinterpret_cast<float*>(smem);  // [rank][128 columns], once the ring is done with
+        int count = 0;
+        for (int g = first_g, cb = first_cb; g < a.G; it.step(g, cb)) {
+            const int col = cb * GC + 32 * q + lane;
+            int p0, n;
+            it.share(g, p0, n);
+            const int b = count % ACCS;
+            bool nan = false;
+            if (n > 0) {
+                if (!mx4_wait_warp(&acc_full[b], (count / ACCS) & 1, guard)) break;
+                tc_fence_after();
+                if (CODES) {
+                    const uint32_t mask = nan_cols[count % MASKS][q];
+                    nan = mask >> lane & 1;
+                    __syncwarp();
+                    if (lane == 0 && mask) nan_cols[count % MASKS][q] = 0;
+                }
+            }
+#pragma unroll 1
+            for (int j0 = 0; j0 < a.rank; j0 += 32) {
+                uint32_t v[32];
+                if (n > 0) {
+                    tmem_ld_32x32b_x32(lanes + b * RP + j0, v);
+                    tmem_ld_wait();
+                }
+                const int js = min(32, a.rank - j0);
+                if (n == 0 || nan) {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) v[j] = n == 0 ? 0u : 0x7fffffffu;
+                }
+                if (C > 1) {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j)
+                        if (j < js) part[(j0 + j) * GC + 32 * q + lane] = __uint_as_float(v[j]);
+                } else if (col < a.C) {
+                    const long long at = (static_cast<long long>(g) * a.rank + j0) * a.C + col;
+                    if (out_bf16) {
+                        __nv_bfloat16* p = static_cast<__nv_bfloat16*>(a.dw) + at;
+#pragma unroll
+                        for (int j = 0; j < 32; ++j, p += a.C)
+                            if (j < js) *p = __float2bfloat16_rn(__uint_as_float(v[j]));
+                    } else {
+                        float* p = static_cast<float*>(a.dw) + at;
+#pragma unroll
+                        for (int j = 0; j < 32; ++j, p += a.C)
+                            if (j < js) *p = __uint_as_float(v[j]);
+                    }
+                }
+            }
+            if (n > 0) {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&acc_empty[b]);
+                ++count;
+            }
+        }
+        __syncwarp();
+    }
+    if (C > 1) {
+        // one item a cluster: this block's share of the ranks, summed over the blocks
+        cluster_sync();
+        const int g = first_g, cb = first_cb;
+        constexpr int V = GC / 4;
+        const int r1 = a.rank * (rank + 1) / C, c0 = cb * GC + 4 * (tid % V);
+        for (int r = a.rank * rank / C + tid / V; r < r1; r += THREADS / V) {
+            const uint32_t addr = smem_u32(smem) + (r * GC + 4 * (tid % V)) * 4;
+            float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-            for (int q = 0; q < C; ++q) {
-                const float4 v = ld_shared_cluster_f4(mapa_shared(addr, q));
+            for (int p = 0; p < C; ++p) {
+                const float4 v = ld_shared_cluster_f4(mapa_shared(addr, p));
                 s = make_float4(s.x + v.x, s.y + v.y, s.z + v.z, s.w + v.w);
             }
+            if (c0 >= a.C) continue;
+            const long long at = (static_cast<long long>(g) * a.rank + r) * a.C + c0;
+            if (out_bf16)
+                *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.dw) + at) = make_uint2(pack_bf16x2(s.x, s.y), pack_bf16x2(s.z, s.w));
+            else
+                *reinterpret_cast<float4*>(static_cast<float*>(a.dw) + at) = s;
         }
-        if (c0 >= a.C) continue;
-        const long long at = (static_cast<long long>(g) * a.rank + r) * a.C + c0;
-        if (out_bf16)
-            *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.dw) + at) = make_uint2(pack_bf16x2(s.x, s.y), pack_bf16x2(s.z, s.w));
-        else
-            *reinterpret_cast<float4*>(static_cast<float*>(a.dw) + at) = s;
+        cluster_sync();   // the others have read this block's sums
     }
-    if (all > 0 && C > 1) cluster_sync();   // the others have read this block's sums
+
+    // ---------------------------------------------------------------------- teardown
+    tc_fence_before();
+    __syncthreads();
+    if (warp == LOADERS) {
+        tc_fence_after();
+        tmem_dealloc(tmem, Cfg::TMEM_COLS);
+    }
 }
 
-template <int RP, bool CODES>
-cudaError_t launch_cfg(const LoraGradArgs& a, bool out_bf16, int C, cudaStream_t stream) {
-    using Cfg = GradCfg<RP, CODES>;
+template <int RP, bool CODES, bool ORDER>
+cudaError_t launch_cfg(const LoraGradArgs& a, bool out_bf16, int C, int slots, uint64_t timeout_ns, cudaStream_t stream) {
+    using Cfg = GradCfg<RP, CODES, ORDER>;
     auto kern = lora_grad_kernel<Cfg>;
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::SMEM);
+    const int shm = Cfg::SMEM + (a.G + 1) * static_cast<int>(sizeof(int32_t));
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, shm);
     if (e != cudaSuccess) return e;
     const int blocks = (a.C + GC - 1) / GC;
-    return launch_pdl_cluster(kern, dim3(static_cast<unsigned>(static_cast<long long>(a.G) * blocks * C)),
-                              dim3(LORA_THREADS), C, Cfg::SMEM, stream, a, blocks, out_bf16);
+    const long long items = static_cast<long long>(a.G) * blocks;
+    const long long grid = C > 1 ? items * C : items < slots ? items : slots;
+    return launch_pdl_cluster(kern, dim3(static_cast<unsigned>(grid)), dim3(Cfg::THREADS), C, shm, stream, a, blocks, out_bf16, timeout_ns);
 }
 
-template <bool CODES>
-cudaError_t launch_codes(const LoraGradArgs& a, bool out_bf16, int C, cudaStream_t stream) {
-    if (a.rank <= 16) return launch_cfg<16, CODES>(a, out_bf16, C, stream);
-    if (a.rank <= 32) return launch_cfg<32, CODES>(a, out_bf16, C, stream);
-    if (a.rank <= 64) return launch_cfg<64, CODES>(a, out_bf16, C, stream);
-    return launch_cfg<128, CODES>(a, out_bf16, C, stream);
+template <bool CODES, bool ORDER>
+cudaError_t launch_rank(const LoraGradArgs& a, bool out_bf16, int C, int slots, uint64_t timeout_ns, cudaStream_t stream) {
+    if (a.rank <= 16) return launch_cfg<16, CODES, ORDER>(a, out_bf16, C, slots, timeout_ns, stream);
+    if (a.rank <= 32) return launch_cfg<32, CODES, ORDER>(a, out_bf16, C, slots, timeout_ns, stream);
+    if (a.rank <= 64) return launch_cfg<64, CODES, ORDER>(a, out_bf16, C, slots, timeout_ns, stream);
+    return launch_cfg<128, CODES, ORDER>(a, out_bf16, C, slots, timeout_ns, stream);
 }
 
 }  // namespace
 
-cudaError_t launch_lora_grad(const LoraGradArgs& a, bool codes, bool out_bf16, int sm_count, cudaStream_t stream) {
+cudaError_t launch_lora_grad(const LoraGradArgs& a, bool codes, bool out_bf16, int sm_count, uint64_t timeout_ns,
+                             cudaStream_t stream) {
     const long long groups = a.G < a.M ? a.G : a.M > 0 ? a.M : 1;   // groups that can have a row
     const long long items = groups * ((a.C + GC - 1) / GC);
     const long long stages = (a.M + groups * GR - 1) / (groups * GR);
     int C = 1;
-    while (C < 8 && items * C * 2 <= 4LL * sm_count && 2 * C <= stages) C *= 2;
-    return codes ? launch_codes<true>(a, out_bf16, C, stream) : launch_codes<false>(a, out_bf16, C, stream);
+    while (C < 8 && items * C * 2 <= sm_count && 2 * C <= stages) C *= 2;
+    const int slots = sm_count;
+    if (codes) return a.order ? launch_rank<true, true>(a, out_bf16, C, slots, timeout_ns, stream) : launch_rank<true, false>(a, out_bf16, C, slots, timeout_ns, stream);
+    return a.order ? launch_rank<false, true>(a, out_bf16, C, slots, timeout_ns, stream) : launch_rank<false, false>(a, out_bf16, C, slots, timeout_ns, stream);
+}
+
+cudaError_t lora_grad_status(int32_t** word) {
+    void* p = nullptr;
+    const cudaError_t e = cudaGetSymbolAddress(&p, g_status);
+    *word = static_cast<int32_t*>(p);
+    return e;
 }
 
 }  // namespace rdot
