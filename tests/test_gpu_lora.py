@@ -65,6 +65,15 @@ def reference(x, first, second, sizes, order, scale, base):
     return out, t, tol + H * out.abs() * (1 if base is None else 1), tol_t + H * t.abs()
 
 
+def ragged(m, g, seed, spare=0):
+    """g group sizes that sum to m - spare: an empty one, short and long ones."""
+    cuts = torch.randint(0, m - spare + 1, (g - 1,), generator=torch.Generator().manual_seed(seed)).sort().values.tolist()
+    sizes = [b - a for a, b in zip([0] + cuts, cuts + [m - spare])]
+    if g > 2:
+        sizes[1], sizes[2] = 0, sizes[1] + sizes[2]
+    return sizes
+
+
 def make(m, k, n, g, r, sizes, order, seed=0, base=True, scale=True):
     gen = torch.Generator(device=DEV).manual_seed(seed)
     d = {"x": randn(gen, (m, k)), "dy": randn(gen, (m, n)), "down": randn(gen, (g, r, k), k ** -0.5), "up": randn(gen, (g, r, n), 0.1)}
@@ -90,6 +99,15 @@ APPLY = [       # m, k, n, r, group sizes, order, base, scale
     (128, 256, 192, 8, [-5, 60, 1 << 30, 7], True, True, True), (40, 64, 192, 16, [0] * 1023 + [33], True, True, True),
     (5000, 136, 136, 8, [5] * 1000, False, True, True),
 ]
+
+
+# Many rows: the 128-row form, with clusters of 4, 2 and 1 and a deep ring, of 2 and 1 and a short one
+for _i, (_m, _g) in enumerate([(4100, 1), (4100, 3), (8000, 3), (12000, 40), (7000, 60), (20000, 9), (70000, 2)]):
+    for _r in ((8, 24, 40, 128) if _m < 20000 else (16, 64)):
+        APPLY.append((_m, 200 + 64 * _i, 328 - 8 * _i, _r, ragged(_m, _g, _i, 130), _r % 16 == 0, _i % 3 != 1, _r != 24))
+APPLY += [(4500, 8, 8, 8, [4500], True, True, True), (4500, 2056, 8, 16, [4000, 100], False, True, True),
+          (4500, 64, 2056, 32, [100, 129, 4200], True, False, True), (4500, 64, 64, 64, [0, 0], True, False, False),
+          (4500, 64, 64, 64, [0, 0], True, True, False), (5000, 72, 136, 16, [-3, 2000, 1 << 30, 5], True, True, True)]
 
 
 @pytest.mark.parametrize("m,k,n,r,sizes,order,base,scale", APPLY)
@@ -204,31 +222,34 @@ def test_group_without_rows():
     assert torch.all(sizes == 0) and order.numel() == 0
 
 
+@pytest.mark.parametrize("m", [300, 6000])
 @pytest.mark.parametrize("order", [False, True])
-def test_in_place_and_rows_without_an_adapter(order):
+def test_in_place_and_rows_without_an_adapter(order, m):
     """out may be base: rows past the last group stay bit for bit, also as a copy; their t is zero."""
-    d = make(300, 256, 264, 3, 16, [100, 0, 77], order, 5)
-    base = d["base_n"]
-    rows = d["order"].long() if order else torch.arange(300, device=DEV)
-    base[rows[177:]] = torch.tensor([float("nan"), -0.0, float("inf")], dtype=torch.bfloat16, device=DEV).repeat(88)
+    d = make(m, 256, 264, 3, 16, [m - 200, 0, 77], order, 5)
+    base, end = d["base_n"], m - 123
+    rows = d["order"].long() if order else torch.arange(m, device=DEV)
+    base[rows[end:]] = torch.tensor([float("nan"), -0.0, float("inf")], dtype=torch.bfloat16, device=DEV).repeat(88)
     out, t = gg.lora_forward(d["x"], d["down"], d["up"], d["sizes"], d["order"], d["scale"], base)
-    assert torch.equal(out.view(torch.int16)[rows[177:]], base.view(torch.int16)[rows[177:]])
-    assert torch.all(t[177:] == 0)
+    assert torch.equal(out.view(torch.int16)[rows[end:]], base.view(torch.int16)[rows[end:]])
+    assert torch.all(t[end:] == 0)
     same = base.clone()
     got, _ = gg.lora_forward(d["x"], d["down"], d["up"], d["sizes"], d["order"], d["scale"], same, out=same)
     assert got is same and torch.equal(same.view(torch.int16), out.view(torch.int16))
 
 
-def test_a_row_keeps_its_nan_to_itself():
+@pytest.mark.parametrize("more", [0, 5000])
+def test_a_row_keeps_its_nan_to_itself(more):
     """A NaN or infinity in a row, an adapter or a scale reaches that row's, adapter's outputs alone."""
-    d = make(200, 136, 72, 3, 8, [90, 0, 100], True, 6)
+    m = 200 + more
+    d = make(m, 136, 72, 3, 8, [90, 0, 100 + more], True, 6)
     clean, clean_t = gg.lora_forward(d["x"], d["down"], d["up"], d["sizes"], d["order"], d["scale"], d["base_n"])
     rows = d["order"].long()
     d["x"][rows[3], 5], d["x"][rows[130], 7] = float("nan"), float("inf")
-    d["x"][rows[195]] = float("nan")                          # no adapter: not read
+    d["x"][rows[m - 5]] = float("nan")                        # no adapter: not read
     d["down"][1], d["up"][1] = float("nan"), float("inf")     # an adapter without rows
     out, t = gg.lora_forward(d["x"], d["down"], d["up"], d["sizes"], d["order"], d["scale"], d["base_n"])
-    keep = torch.ones(200, dtype=torch.bool, device=DEV)
+    keep = torch.ones(m, dtype=torch.bool, device=DEV)
     keep[[3, 130]] = False
     assert torch.equal(t[keep], clean_t[keep]) and torch.equal(out[rows[keep]], clean[rows[keep]])
     assert torch.isnan(out[rows[3]]).all() and torch.isnan(t[3]).all()
@@ -240,16 +261,18 @@ def test_a_row_keeps_its_nan_to_itself():
     assert torch.equal(torch.isnan(got), torch.isnan(want)) and torch.equal(got[~torch.isnan(want)], want[~torch.isnan(want)])
 
 
-def test_bad_order_entries_count_as_none():
+@pytest.mark.parametrize("m", [100, 5000])
+def test_bad_order_entries_count_as_none(m):
     """An entry outside [0, M) is skipped: its row is not written and adds nothing to the gradients."""
-    d = make(100, 64, 64, 2, 8, [50, 40], True, 7)
+    sizes = [50, m - 60]
+    d = make(m, 64, 64, 2, 8, sizes, True, 7)
     bad = d["order"].clone()
-    bad[10], bad[60], bad[95] = -1, 100, 2 ** 31 - 1
-    out = torch.full((100, 64), 7.0, dtype=torch.bfloat16, device=DEV)
+    bad[10], bad[60], bad[m - 5] = -1, m, 2 ** 31 - 1
+    out = torch.full((m, 64), 7.0, dtype=torch.bfloat16, device=DEV)
     gg.rdot_lora_forward(d["x"], d["down"], d["up"], d["sizes"], out, order=bad, scale=d["scale"], base=d["base_n"])
-    ref, _, tol, _ = reference(d["x"], d["down"], d["up"], [50, 40], d["order"], d["scale"], d["base_n"])
-    keep = torch.ones(100, dtype=torch.bool, device=DEV)
-    keep[d["order"][[10, 60, 95]].long()] = False
+    ref, _, tol, _ = reference(d["x"], d["down"], d["up"], sizes, d["order"], d["scale"], d["base_n"])
+    keep = torch.ones(m, dtype=torch.bool, device=DEV)
+    keep[d["order"][[10, 60, m - 5]].long()] = False
     close(out[keep], ref[keep], tol[keep])
     assert torch.all(out[~keep] == 7)
     t = d["dy"][:, :8].contiguous()
@@ -260,8 +283,9 @@ def test_bad_order_entries_count_as_none():
         assert torch.equal(gg.lora_grad_weight(t, z, d["sizes"], bad, zs), gg.lora_grad_weight(want, z, d["sizes"], d["order"], zs))
 
 
-def test_same_result_every_time():
-    d = make(1000, 2048, 1408, 5, 64, [300, 1, 0, 500, 150], True, 8)
+@pytest.mark.parametrize("more", [0, 7000])
+def test_same_result_every_time(more):
+    d = make(1000 + more, 2048, 1408, 5, 64, [300, 1, 0, 500 + more, 150], True, 8)
     a = [gg.lora_forward(d["x"], d["down"], d["up"], d["sizes"], d["order"], d["scale"], d["base_n"]) for _ in range(5)]
     w = [gg.lora_grad_weight(a[0][1], d["dy"], d["sizes"], d["order"]) for _ in range(5)]
     for i in range(1, 5):
@@ -282,10 +306,10 @@ def test_strided_and_64_bit_inputs():
                        gg.lora_grad_weight(ref[1], d["x"], d["sizes"], d["order"]))
 
 
-def test_more_than_32_bits_of_offsets():
+@pytest.mark.parametrize("m", [2100, 4200])
+def test_more_than_32_bits_of_offsets(m):
     """Rows behind the 2^32nd byte and the 2^31st element of x, out and dw."""
-    k, r = 1 << 20, 8
-    m, g = 2100, 2
+    k, r, g = 1 << 20, 8, 2
     gen = torch.Generator(device=DEV).manual_seed(10)
     x = torch.zeros((m, k), dtype=torch.bfloat16, device=DEV)
     x[-3:] = randn(gen, (3, k))
@@ -308,9 +332,10 @@ def test_more_than_32_bits_of_offsets():
     assert torch.all(dw[0] == 0)
 
 
-def test_two_streams_at_once():
+@pytest.mark.parametrize("more", [0, 4000])
+def test_two_streams_at_once(more):
     """Calls hold no shared workspace: the same shapes on two streams at once give the same results."""
-    ds = [make(600, 1024, 1408, 4, 32, [100, 200, 0, 250], True, s) for s in (11, 12)]
+    ds = [make(600 + more, 1024, 1408, 4, 32, [100, 200, 0, 250 + more], True, s) for s in (11, 12)]
     run = lambda d, s: gg.lora_forward(d["x"], d["down"], d["up"], d["sizes"], d["order"], d["scale"], d["base_n"], stream=s)
     refs = [run(d, None) for d in ds]
     refs_w = [gg.lora_grad_weight(r[1], d["dy"], d["sizes"], d["order"]) for r, d in zip(refs, ds)]
@@ -324,10 +349,11 @@ def test_two_streams_at_once():
             assert torch.equal(o[0], r[0]) and torch.equal(o[1], r[1]) and torch.equal(w, rw)
 
 
-def test_captured_step_follows_its_inputs():
+@pytest.mark.parametrize("m", [130, 5000])
+def test_captured_step_follows_its_inputs(m):
     """A captured group + forward + gradients replays with other ids, rows and sizes than it was captured with, on
     a grid that its shapes alone decide."""
-    m, k, n, g, r = 130, 256, 384, 6, 16
+    k, n, g, r = 256, 384, 6, 16
     d = make(m, k, n, g, r, [0] * g, False, 13)
     ids = torch.zeros(m, dtype=torch.int32, device=DEV)
 
@@ -353,12 +379,13 @@ def test_captured_step_follows_its_inputs():
             assert torch.equal(a, b)
 
 
-def test_a_training_step_of_a_projection():
+@pytest.mark.parametrize("m", [333, 5000])
+def test_a_training_step_of_a_projection(m):
     """The calls together, as a frozen projection with adapters trains: forward beside the projection, the input
     kept in 8 bits, the backward pass through both, against autograd in 64 bits. The adapters' gradients see the
     kept input, so the 64-bit gradient of down takes the checkpoint's values. Errors of t and dt, rounded to bf16
     for the gradients, are H of them."""
-    m, k, n, g, r = 333, 288, 416, 5, 24
+    k, n, g, r = 288, 416, 5, 24
     d = make(m, k, n, g, r, [0] * g, False, 15)
     gen = torch.Generator(device=DEV).manual_seed(16)
     ids = torch.randint(-1, g, (m,), generator=gen, device=DEV, dtype=torch.int32)
@@ -428,3 +455,35 @@ def test_gradients_are_differences_of_the_forward():
         # each gradient element is off by about H of the terms it sums: bounded by their absolute sum
         bound = 3 * H * float((grads[which].double().abs() * v.abs()).sum()) + 3 * H * float(grads[which].abs().max()) * v.abs().sum() * 0.1
         assert abs(got - diff) <= float(bound)
+
+
+def test_a_wait_limit_stops_the_call_and_is_reported():
+    """A limit of a nanosecond makes waits run out: the calls end early, free what they hold and set the device's status
+    bit, which stays until it is cleared; the next calls are right. The few-row form has no such waits."""
+    d = make(5000, 2048, 1408, 3, 64, [3000, 0, 1900], True, 19)
+    args = (d["down"], d["up"], d["sizes"], d["order"], d["scale"])
+    gg.rdot_lora_clear_status()
+    ref = gg.lora_forward(d["x"], *args, d["base_n"])
+    codes = gg.quantize_mxfp8(d["x"])
+    ref_w = [gg.lora_grad_weight(ref[1], d["dy"], d["sizes"], d["order"]), gg.lora_grad_weight(ref[1], codes[0], d["sizes"], d["order"], codes[1])]
+    assert gg.rdot_lora_read_status() == 0
+    calls = (lambda: gg.lora_forward(d["x"], *args, d["base_n"]), lambda: gg.lora_forward(d["x"], *args[:3], scale=d["scale"]),
+             lambda: gg.lora_grad_weight(ref[1], d["dy"], d["sizes"], d["order"]),
+             lambda: gg.lora_grad_weight(ref[1], codes[0], d["sizes"], d["order"], codes[1]),
+             lambda: gg.lora_grad_weight(ref[1], d["dy"], d["sizes"]))
+    try:
+        for call in calls:
+            gg.rdot_lora_set_wait_timeout(1)
+            call()
+            assert gg.rdot_lora_read_status() == gg.RDOT_STATUS_BIT_TIMEOUT
+            gg.rdot_lora_set_wait_timeout(0)
+            call()
+            assert gg.rdot_lora_read_status() == gg.RDOT_STATUS_BIT_TIMEOUT     # sticky
+            gg.rdot_lora_clear_status()
+            assert gg.rdot_lora_read_status() == 0
+    finally:
+        gg.rdot_lora_set_wait_timeout(0)
+    again = gg.lora_forward(d["x"], *args, d["base_n"])
+    assert torch.equal(again[0], ref[0]) and torch.equal(again[1], ref[1])
+    assert torch.equal(calls[2](), ref_w[0]) and torch.equal(calls[3](), ref_w[1])
+    assert gg.rdot_lora_read_status() == 0

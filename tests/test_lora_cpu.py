@@ -87,6 +87,11 @@ def test_group_refusals(lib):
             assert f(args[0], 4, 4, args[1], args[2], None) == INVALID
 
 
+def test_status_calls(lib):
+    assert lib.rdot_lora_read_status(None, None) == INVALID
+    assert lib.rdot_lora_set_wait_timeout(5) == OK and lib.rdot_lora_set_wait_timeout(0) == OK
+
+
 def test_quantize_refusals(lib):
     q, d = lib.rdot_quantize_mxfp8, lib.rdot_dequantize_mxfp8
     for dtype, rows, k, status in ((gg.RDOT_E4M3, 4, 64, INVALID), (gg.RDOT_F32, -1, 64, INVALID),
