@@ -77,6 +77,19 @@ __device__ __forceinline__ void st_shared_cluster_u4(uint32_t addr, const uint4&
     asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
 
+// Whether the phase has completed, without waiting; the same in every lane.
+__device__ __forceinline__ bool mbar_test_uniform(uint64_t* bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    return __all_sync(0xffffffffu, ok);
+}
+
 // Sum over a block of THREADS threads of `v`, and of the threads before this one. `part`: shared, an entry a warp;
 // the caller synchronises between uses.
 template <int THREADS>
