@@ -71,7 +71,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::BLOCKS)
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int C = static_cast<int>(cluster_ctas()), rank = static_cast<int>(cluster_ctarank());
 
-    grid_dependency_enter();
+    grid_dependency_wait();
     const LoraTile tile = lora_find_tile<ROWS, THREADS>(a.group_sizes, a.G, a.M, static_cast<int>(blockIdx.x) / C);
     if (tile.rows == 0) return;   // the whole cluster
     lora_tile_rows<ROWS, THREADS>(row_of, tile, a.order, a.M);
@@ -114,6 +114,9 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::BLOCKS)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    // Only now may the next kernel's blocks come: one of them beside this block could else take the tensor memory that this
+    // one is about to ask for, and hold it while it waits for this grid to end.
+    grid_launch_dependents();
     const uint32_t tmem = tmem_holder;
     const WaitGuard guard{&abort_flag, &g_status, timeout_ns};
 
