@@ -30,16 +30,22 @@ __global__ void __launch_bounds__(GROUP_THREADS) lora_group_kernel(const int32_t
     int32_t* mine = counts + warp * B;
 
     grid_dependency_enter();
-    const long long units = (static_cast<long long>(M) + 31) / 32;   // of 32 rows
-    const long long w = static_cast<long long>(rank) * GROUP_WARPS + warp, W = static_cast<long long>(C) * GROUP_WARPS;
-    const long long u0 = units * w / W, u1 = units * (w + 1) / W;
+    // units of 32 rows, `per` to a warp: the first `tables` warps of a block have some (64 rows of 256 adapters with all 32
+    // warps' tables cleared and added up: 5.5 us, with two 4.7)
+    const long long units = (static_cast<long long>(M) + 31) / 32;
+    const int shift = 5 + 31 - __clz(C);   // log2 of the warps; C is a power of two
+    const long long per = (units + (1LL << shift) - 1) >> shift;
+    const long long w = static_cast<long long>(rank) * GROUP_WARPS + warp;
+    const long long u0 = min(units, w * per), u1 = min(units, u0 + per);
+    const int tables = static_cast<int>(min(units, static_cast<long long>(GROUP_WARPS)));
     const auto bin = [&](long long u) -> int {   // -1 past the end
         const long long r = 32 * u + lane;
         if (r >= M) return -1;
         const int id = __ldg(ids + r);
         return id >= 0 && id < G ? id : G;
     };
-    for (int b = lane; b < B; b += 32) mine[b] = 0;
+    if (warp < tables)
+        for (int b = lane; b < B; b += 32) mine[b] = 0;
     __syncwarp();
     constexpr int U = 8;   // loads in flight
     for (long long u = u0; u < u1; u += U) {
@@ -55,7 +61,7 @@ __global__ void __launch_bounds__(GROUP_THREADS) lora_group_kernel(const int32_t
     for (int b = tid; b < B; b += GROUP_THREADS) {
         int32_t run = 0;
 #pragma unroll 8
-        for (int v = 0; v < GROUP_WARPS; ++v) {
+        for (int v = 0; v < tables; ++v) {
             const int32_t c = counts[v * B + b];
             counts[v * B + b] = run;
             run += c;
@@ -96,7 +102,8 @@ __global__ void __launch_bounds__(GROUP_THREADS) lora_group_kernel(const int32_t
     if (tid < B) totals[tid] = base + incl - all + before;   // the block's first place of each bin
     if (B > GROUP_THREADS && tid == 0) totals[GROUP_THREADS] = sum + extra;
     __syncthreads();
-    for (int b = lane; b < B; b += 32) mine[b] += totals[b];
+    if (warp < tables)
+        for (int b = lane; b < B; b += 32) mine[b] += totals[b];
     __syncwarp();
     for (long long u = u0; u < u1; u += U) {
         int id[U];
@@ -124,7 +131,8 @@ cudaError_t launch_lora_group(const int32_t* ids, int M, int G, int32_t* group_s
     const size_t shm = static_cast<size_t>(GROUP_WARPS + 1) * (G + 1) * sizeof(int32_t);
     const cudaError_t e = cudaFuncSetAttribute(lora_group_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(shm));
     if (e != cudaSuccess) return e;
-    const int C = M <= 4096 ? 1 : M <= 16384 ? 4 : 8;
+    // (16384 rows of 64 adapters: 17.0, 10.6, 7.9 and 7.0 us with 1, 2, 4 and 8 blocks; 64 rows of 256: 4.7 with one)
+    const int C = M <= 1024 ? 1 : M <= 4096 ? 4 : 8;
     return launch_pdl_cluster(lora_group_kernel, dim3(C), dim3(GROUP_THREADS), C, shm, stream, ids, M, G, group_sizes, order);
 }
 
