@@ -286,11 +286,17 @@ def rdot_router_topk(logits, topk: int, weights_mode: int, topk_ids, topk_weight
                                    _ptr(topk_weights), _stream(stream, logits.device)), "rdot_router_topk")
 
 
+_float_codes = {}      # the codes of torch's dtypes, once torch has been imported
+
+
 def _float_dtype(t, what: str) -> int:
-    import torch
-    dt = {torch.float32: RDOT_F32, torch.bfloat16: RDOT_BF16}.get(t.dtype)
+    dt = _float_codes.get(t.dtype)
     if dt is None:
-        raise TypeError(f"{what} must be float32 or bfloat16")
+        import torch
+        _float_codes.update({torch.float32: RDOT_F32, torch.bfloat16: RDOT_BF16})
+        dt = _float_codes.get(t.dtype)
+        if dt is None:
+            raise TypeError(f"{what} must be float32 or bfloat16")
     return dt
 
 
@@ -354,20 +360,21 @@ def rdot_router_topk_grad(logits, topk_ids, topk_weights, dweights, weights_mode
 
 def rdot_quantize_mxfp8(x, codes, scales, stream=None) -> None:
     """x [rows, K] (fp32 or bf16) -> codes uint8 [rows, K], scales uint8 [rows, K/32]."""
-    _check(load().rdot_quantize_mxfp8(_ptr(x), _float_dtype(x, "x"), int(x.shape[0]), int(x.shape[1]), _ptr(codes),
-                                      _ptr(scales), _stream(stream, x.device)), "rdot_quantize_mxfp8")
+    rows, k = x.shape
+    _check(load().rdot_quantize_mxfp8(x.data_ptr(), _float_dtype(x, "x"), rows, k, codes.data_ptr(), scales.data_ptr(),
+                                      _stream(stream, x.device)), "rdot_quantize_mxfp8")
 
 
 def rdot_dequantize_mxfp8(codes, scales, out, stream=None) -> None:
     """codes uint8 [rows, K], scales uint8 [rows, K/32] -> out [rows, K] (fp32 or bf16)."""
-    _check(load().rdot_dequantize_mxfp8(_ptr(codes), _ptr(scales), int(out.shape[0]), int(out.shape[1]),
-                                        _float_dtype(out, "out"), _ptr(out), _stream(stream, out.device)),
-           "rdot_dequantize_mxfp8")
+    rows, k = out.shape
+    _check(load().rdot_dequantize_mxfp8(codes.data_ptr(), scales.data_ptr(), rows, k, _float_dtype(out, "out"),
+                                        out.data_ptr(), _stream(stream, out.device)), "rdot_dequantize_mxfp8")
 
 
 def rdot_lora_group(ids, groups: int, group_sizes, order, stream=None) -> None:
     """ids int32 [M] -> group_sizes int32 [groups], order int32 [M]."""
-    _check(load().rdot_lora_group(_ptr(ids), int(ids.shape[0]), int(groups), _ptr(group_sizes), _ptr(order),
+    _check(load().rdot_lora_group(ids.data_ptr(), ids.shape[0], int(groups), group_sizes.data_ptr(), order.data_ptr(),
                                   _stream(stream, group_sizes.device)), "rdot_lora_group")
 
 
@@ -394,8 +401,8 @@ def rdot_lora_set_wait_timeout(timeout_ns: int) -> None:
 
 def _lora_apply(name, x, down, up, group_sizes, order, scale, base, out, t, stream):
     g, r, k = down.shape
-    _check(getattr(load(), name)(_ptr(x), _ptr(down), _ptr(up), _ptr(group_sizes), _ptr(order), _ptr(scale), _ptr(base),
-                                 int(x.shape[0]), k, int(up.shape[2]), g, r, _ptr(out), _ptr(t),
+    _check(getattr(load(), name)(x.data_ptr(), down.data_ptr(), up.data_ptr(), group_sizes.data_ptr(), _ptr(order),
+                                 _ptr(scale), _ptr(base), x.shape[0], k, up.shape[2], g, r, out.data_ptr(), _ptr(t),
                                  _stream(stream, out.device)), name)
 
 
@@ -413,9 +420,9 @@ def rdot_lora_grad_weight(t, z, group_sizes, dw, order=None, z_scale=None, strea
     """t bf16 [M, r], z bf16 [M, width] (or E4M3 codes uint8 with z_scale uint8 [M, width/32]) -> dw [G, r, width]
     (fp32 or bf16)."""
     g, r, width = dw.shape
-    _check(load().rdot_lora_grad_weight(_ptr(t), _ptr(z), RDOT_BF16 if z_scale is None else RDOT_E4M3, _ptr(z_scale),
-                                        _ptr(group_sizes), _ptr(order), int(t.shape[0]), width, g, r,
-                                        _float_dtype(dw, "dw"), _ptr(dw), _stream(stream, dw.device)),
+    _check(load().rdot_lora_grad_weight(t.data_ptr(), z.data_ptr(), RDOT_BF16 if z_scale is None else RDOT_E4M3,
+                                        _ptr(z_scale), group_sizes.data_ptr(), _ptr(order), t.shape[0], width, g, r,
+                                        _float_dtype(dw, "dw"), dw.data_ptr(), _stream(stream, dw.device)),
            "rdot_lora_grad_weight")
 
 

@@ -1,5 +1,5 @@
 // lora.cuh -- what the low-rank adapter kernels share: asynchronous row copies, the 16 x 8 x 16 bf16 MMA on
-// register fragments, and the scan that finds a block's rows.
+// register fragments, the scan that finds a block's rows, and launches in clusters.
 #pragma once
 
 #include <stdint.h>
@@ -193,6 +193,27 @@ __device__ __forceinline__ void split_bf16x2(float a, float b, uint32_t& hi, uin
     hi = pack_bf16x2(a, b);
     const float fa = __uint_as_float(hi << 16), fb = __uint_as_float(hi & 0xffff0000u);
     lo = pack_bf16x2(isfinite(fa) ? a - fa : 0.f, isfinite(fb) ? b - fb : 0.f);
+}
+
+// launch_pdl (pdl.cuh) with clusters of `cluster` blocks along x, chosen at the launch.
+template <typename... Params, typename... Args>
+cudaError_t launch_pdl_cluster(void (*kern)(Params...), dim3 grid, dim3 block, int cluster, size_t shm,
+                               cudaStream_t stream, Args&&... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = shm;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cluster;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, kern, static_cast<Args&&>(args)...);
 }
 
 }  // namespace rdot
