@@ -1708,8 +1708,7 @@ rdot_status rdot_lora_grad_weight(const void* t, const void* z, int32_t z_dtype,
     if (!group_sizes || !dw || !aligned4(group_sizes) || !aligned16(dw)) return RDOT_ERR_INVALID_ARG;
     if (m > 0) {
         if (!t || !z || (z_dtype == RDOT_E4M3 && !z_scale)) return RDOT_ERR_INVALID_ARG;
-        if (!aligned16(t) || !aligned16(z) || !aligned4(order) || (z_dtype == RDOT_E4M3 && !aligned4(z_scale)))
-            return RDOT_ERR_INVALID_ARG;
+        if (!aligned16(t) || !aligned16(z) || !aligned4(order)) return RDOT_ERR_INVALID_ARG;
     }
     const int sms = current_sm_count();
     if (sms <= 0) return cuda_fail(cudaGetLastError(), "cudaDeviceGetAttribute");

@@ -14,11 +14,6 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool l
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
 }
 
-// 4 bytes of which the first `bytes` are read, the others 0.
-__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, int bytes) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
-
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 
 // An arrival on `bar`, one of those it was initialised for, once this thread's copies so far have landed.

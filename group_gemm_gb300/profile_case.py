@@ -29,13 +29,15 @@ def main():
     ap.add_argument("--kernel", choices=["fwd", "dgrad", "wgrad", "padded", "mxfp8", "mxdgrad", "mxwgrad", "gated",
                                          "permute",
                                          "unpermute", "topk", "mxfp4", "mx4rows", "mx4weight", "unpermute_grad",
-                                         "permute_grad", "topk_grad"], default="fwd")
+                                         "permute_grad", "topk_grad", "lora", "lora_dgrad", "lora_wgrad",
+                                         "lora_wgrad8", "mx8rows", "mx8restore"], default="fwd")
     ap.add_argument("--workload", default="mixtral_bf16")
     ap.add_argument("--tokens", type=int, default=2048)
     ap.add_argument("--iters", type=int, default=3)
     ap.add_argument("--groups", type=int, default=0, help="override the workload's expert count")
     ap.add_argument("--flags", type=lambda v: int(v, 0), default=0, help="rdot_problem.flags of the plan")
     ap.add_argument("--tile-n", type=int, default=0, help="rdot_problem.tile_n of the plan (0: the plan's choice)")
+    ap.add_argument("--rank", type=int, default=16, help="rank of the low-rank adapters")
     ap.add_argument("--out", choices=["f32", "bf16"], default="f32", help="dw type of the weight gradients")
     args = ap.parse_args()
 
@@ -118,6 +120,42 @@ def main():
             def run():
                 gg.rdot_quantize_mxfp4_weight(w, wq, ws, wv, stream)
         flops = 2.0 * m * k * n if args.kernel == "mxfp4" else 0.0
+    elif args.kernel in ("lora", "lora_dgrad", "lora_wgrad", "lora_wgrad8", "mx8rows", "mx8restore"):
+        # an adapter for each of the workload's groups: forward, gradient of the input, and of the down matrices from
+        # bf16 rows or their 8-bit checkpoint; the checkpoint itself
+        r = args.rank
+        x = ri.device_normal((m, k), 1, 1.0, dev, torch.bfloat16)
+        codes, scales = gg.quantize_mxfp8(x)
+        down = ri.device_normal((g, r, k), 2, 0.02, dev, torch.bfloat16)
+        up = ri.device_normal((g, r, n), 3, 0.02, dev, torch.bfloat16)
+        t = ri.device_normal((m, r), 4, 1.0, dev, torch.bfloat16)
+        plan = None
+        if args.kernel in ("lora", "lora_dgrad"):
+            base = ri.device_normal((m, n), 5, 1.0, dev, torch.bfloat16)
+            out = torch.empty((m, n if args.kernel == "lora" else k), dtype=torch.bfloat16, device=dev)
+
+            def run():
+                if args.kernel == "lora":
+                    gg.rdot_lora_forward(x, down, up, gs_d, out, t, base=base, stream=stream)
+                else:
+                    gg.rdot_lora_grad_input(base, down, up, gs_d, out, t, base=x, stream=stream)
+            flops = 2.0 * m * r * (k + n)
+        elif args.kernel in ("lora_wgrad", "lora_wgrad8"):
+            dw = torch.empty((g, r, k), dtype=torch.float32 if args.out == "f32" else torch.bfloat16, device=dev)
+
+            def run():
+                if args.kernel == "lora_wgrad":
+                    gg.rdot_lora_grad_weight(t, x, gs_d, dw, stream=stream)
+                else:
+                    gg.rdot_lora_grad_weight(t, codes, gs_d, dw, z_scale=scales, stream=stream)
+            flops = 2.0 * m * r * k
+        else:
+            def run():
+                if args.kernel == "mx8rows":
+                    gg.rdot_quantize_mxfp8(x, codes, scales, stream)
+                else:
+                    gg.rdot_dequantize_mxfp8(codes, scales, x, stream)
+            flops = 0.0
     elif args.kernel in ("unpermute_grad", "permute_grad", "topk_grad"):
         # the gradients of the routing kernels below, rows of width K
         t = args.tokens

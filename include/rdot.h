@@ -458,8 +458,8 @@ RDOT_API rdot_status rdot_dequantize_mxfp8(const uint8_t* codes, const uint8_t* 
  * Sums are fp32 in a fixed order. t enters the second product with an error of 2^-16, out is rounded to
  * bf16 once. m = 0 launches nothing, except that the weight gradient still writes its zeros. k % 8 == 0,
  * n % 8 == 0 (at most 2^30), r % 8 == 0 and r <= RDOT_LORA_MAX_RANK (pad smaller adapters with zero rows),
- * m < 2^31, G <= RDOT_MAX_GROUPS, else RDOT_ERR_UNSUPPORTED; 16-byte alignment, 4 for group_sizes, order,
- * scale and z_scale. */
+ * m < 2^31, G <= RDOT_MAX_GROUPS, else RDOT_ERR_UNSUPPORTED; 16-byte alignment, 4 for group_sizes, order
+ * and scale, any for z_scale. */
 #define RDOT_LORA_MAX_RANK 128
 
 /* The forward and the gradient of the input wait on barriers of their own where groups have many rows. A wait

@@ -200,6 +200,21 @@ def test_grad_weight_codes_of_any_kind():
     assert torch.isfinite(dw[:, 32:]).all()
 
 
+def test_scales_of_any_alignment():
+    """A checkpoint's scales may start at any byte, with rows of any number of them."""
+    gen = torch.Generator(device=DEV).manual_seed(20)
+    m, width, r = 150, 160, 8
+    t, z = randn(gen, (m, r)), randn(gen, (m, width))
+    codes, scales = gg.quantize_mxfp8(z)
+    gs = torch.tensor([100, 30], dtype=torch.int32, device=DEV)
+    ref = gg.lora_grad_weight(t, codes, gs, z_scale=scales)
+    buf = torch.empty(scales.numel() + 3, dtype=torch.uint8, device=DEV)
+    for shift in (1, 2, 3):
+        odd = buf[shift:shift + scales.numel()].view(scales.shape)
+        odd.copy_(scales)
+        assert torch.equal(gg.lora_grad_weight(t, codes, gs, z_scale=odd), ref)
+
+
 @pytest.mark.parametrize("m,g", [(1, 1), (31, 4), (32, 1), (33, 1024), (64, 256), (1000, 7), (4096, 64), (4097, 1023),
                                  (16384, 64), (16385, 1024), (70001, 300), (300000, 1)])
 def test_group(m, g):
