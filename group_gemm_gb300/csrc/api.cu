@@ -1619,12 +1619,13 @@ rdot_status lora_apply(const void* x, const void* first, const void* second, con
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const long long routed = std::min<long long>(m, groups);   // groups that can have a row
     const long long rows = (m + routed - 1) / routed;          // rows of an average one
-    // Tiles of 16 rows while they give an SM no more than one and a third, or groups have no more rows; else the 128-row
-    // tcgen05 form (4096 -> 4096, 4 groups through an order, rank 16: 2048 rows 24 against 43 us, 4096 rows 47 / 35;
-    // rank 64: 39 / 51 and 73 / 39).
+    // Tiles of 16 rows where groups have no more rows, or while such tiles give an SM no more than one and a third, past
+    // rank 64 no more than a 16th; else the 128-row tcgen05 form (4096 -> 4096 through an order; 4 groups, rank 16: 2048
+    // rows 24 against 43 us, 4096 rows 47 / 35; rank 64: 39 / 51 and 73 / 39; rank 128: 64 rows of 2 groups 22 / 30, 256
+    // rows of 2 38 / 33, 256 rows of 16 39 / 53, 1024 rows of 16 57 / 39).
     const long long tiles16 = routed * ((rows + LORA_FEW_ROWS - 1) / LORA_FEW_ROWS);
     int C = 1;
-    if (rows <= LORA_FEW_ROWS || 3 * tiles16 <= 4LL * sms) {
+    if (rows <= LORA_FEW_ROWS || (rank <= 64 ? 3 * tiles16 <= 4LL * sms : 16 * tiles16 <= sms)) {
         // Clusters up to two blocks per SM (256 rows of 64 groups, 4096 -> 4096: C = 4 16.4, C = 8 22.5 us); up to four where
         // a row or two of a group leave each block long strips of weights (64 rows of 256 groups, 4096 -> 14336:
         // C = 4 26.6, C = 8 20.4 us).
@@ -1635,9 +1636,10 @@ rdot_status lora_apply(const void* x, const void* first, const void* second, con
     }
     // Of the 128-row form, one block per SM with a deep ring where clusters of it fill the SMs (8192 rows of 8 groups,
     // 4096 -> 4096, rank 64: 49 us against 57 for two blocks), else two (8192 rows of 32 groups through an order,
-    // rank 16: 77 against 90).
+    // rank 16: 77 against 90). Clusters of 8 such blocks fit on four fifths of the SMs (512 rows of 16 groups, rank 128:
+    // 56 us where they wait for a second round, 37 in clusters of 4).
     const long long tiles = m / LORA_TALL_ROWS + (3 * routed + 3) / 4;   // three groups in four end inside one, about
-    while (C < 8 && tiles * C * 2 <= sms) C *= 2;
+    while (C < 8 && tiles * C * 2 <= (C == 4 ? 4LL * sms / 5 : sms)) C *= 2;
     const bool deep = rank > 64 || (5 * tiles * C >= 4LL * sms && tiles * C <= sms);
     if (!deep)
         while (C < 8 && tiles * C * 2 <= 2LL * sms) C *= 2;
