@@ -1619,30 +1619,45 @@ rdot_status lora_apply(const void* x, const void* first, const void* second, con
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const long long routed = std::min<long long>(m, groups);   // groups that can have a row
     const long long rows = (m + routed - 1) / routed;          // rows of an average one
-    // Tiles of 16 rows where groups have no more rows, or while such tiles give an SM no more than one and a third, past
-    // rank 64 no more than a 16th; else the 128-row tcgen05 form (4096 -> 4096 through an order; 4 groups, rank 16: 2048
-    // rows 24 against 43 us, 4096 rows 47 / 35; rank 64: 39 / 51 and 73 / 39; rank 128: 64 rows of 2 groups 22 / 30, 256
-    // rows of 2 38 / 33, 256 rows of 16 39 / 53, 1024 rows of 16 57 / 39).
-    const long long tiles16 = routed * ((rows + LORA_FEW_ROWS - 1) / LORA_FEW_ROWS);
+    // How many groups have rows, about (all of few, most of as many groups as rows), and the tiles of either form.
+    const long long used = std::min<long long>(routed, 6LL * m * groups / (5LL * (m + groups)) + 1);
+    const long long tiles16 = std::max(used, m / LORA_FEW_ROWS + used / 2);
+    const long long tiles128 = std::max(used, m / LORA_TALL_ROWS + (3 * used + 3) / 4);   // three in four end inside one
+    // Tiles of 16 rows read a group's weights for each 16 of its rows, tiles of 128 rows are few and half empty where groups
+    // are short. All times in us, 16-row tiles / 128-row tiles, 4096 -> 4096 through an order. Up to rank 32: 2048 rows of 4
+    // groups 22 / 31, 3000 of 4 35 / 33, 3000 of 32 29 / 45, 6000 of 32 59 / 54, 8192 of 128 59 / 97 (without an order
+    // 59 / 70; 4096 of 32, rank 32 41 / 41). Up to rank 64: 900 rows of 32 groups 26 / 35, 1200 of 32 39 / 37, and, where
+    // clusters of four 128-row blocks are more than the SMs, 2000 of 32 41 / 43, 2500 of 32 66 / 45. Above: 512 rows of 2
+    // groups 27 / 33, 800 of 40 42 / 70, 1024 of 8 38 / 34, 5120 of 256 225 / 172.
+    const bool crowded = 4 * tiles128 > sms;
+    const bool few = rows <= (rank <= 64 ? LORA_FEW_ROWS : LORA_FEW_ROWS / 2) ||
+                     (rank <= 32 ? tiles16 <= sms || rows <= (a.order ? 128 : 96)
+                                 : (rank <= 64 ? 1 : 2) * tiles16 <= (crowded ? sms : sms / 2));
     int C = 1;
-    if (rows <= LORA_FEW_ROWS || (rank <= 64 ? 3 * tiles16 <= 4LL * sms : 16 * tiles16 <= sms)) {
-        // Clusters up to two blocks per SM (256 rows of 64 groups, 4096 -> 4096: C = 4 16.4, C = 8 22.5 us); up to four where
-        // a row or two of a group leave each block long strips of weights (64 rows of 256 groups, 4096 -> 14336:
-        // C = 4 26.6, C = 8 20.4 us).
-        while (C < 8 && tiles16 * C * 2 <= 2LL * sms + 16) C *= 2;
-        if (C < 8 && rows <= 2 && tiles16 * C * 2 <= 4LL * sms && (k + n) / (128 * 2 * C) >= 16) C *= 2;
-        const cudaError_t e = launch_lora_apply(a, C, s);
+    if (few) {
+        // Clusters as large as the SMs hold at once, with what a cluster's shape leaves over (256 rows of 64 groups, 4096 ->
+        // 4096, rank 64: C = 2 33, C = 4 27, C = 8 35 us; 64 rows of 256 groups, 4096 -> 14336, rank 16: C = 4 28,
+        // C = 8 23); past eight blocks the output's columns are divided among D clusters of a tile, each with the whole
+        // first product (16 rows of 16 groups, 4096 -> 14336, rank 16: D = 1 16, D = 2 14, D = 4 14; rank 64: 25, 22, 31).
+        const auto fits = [&](int c, int blocks) {
+            return 20 * tiles16 * c <= 1LL * blocks * sms * (c >= 8 ? 18 : c == 4 && rank > 32 ? 19 : 21);
+        };
+        int blocks = lora_apply_blocks(rank);
+        while (C < 8 && fits(2 * C, blocks)) C *= 2;
+        int D = 1;
+        while (C == 8 && fits(C * D * 2, 2) && 128LL * C * D * 2 <= n) D *= 2;
+        while (blocks > 1 && fits(C * D, blocks - 1)) --blocks;
+        const cudaError_t e = launch_lora_apply(a, C, D, blocks, s);
         return e == cudaSuccess ? RDOT_OK : cuda_fail(e, "lora launch");
     }
     // Of the 128-row form, one block per SM with a deep ring where clusters of it fill the SMs (8192 rows of 8 groups,
     // 4096 -> 4096, rank 64: 49 us against 57 for two blocks), else two (8192 rows of 32 groups through an order,
     // rank 16: 77 against 90). Clusters of 8 such blocks fit on four fifths of the SMs (512 rows of 16 groups, rank 128:
     // 56 us where they wait for a second round, 37 in clusters of 4).
-    const long long tiles = m / LORA_TALL_ROWS + (3 * routed + 3) / 4;   // three groups in four end inside one, about
-    while (C < 8 && tiles * C * 2 <= (C == 4 ? 4LL * sms / 5 : sms)) C *= 2;
-    const bool deep = rank > 64 || (5 * tiles * C >= 4LL * sms && tiles * C <= sms);
+    while (C < 8 && tiles128 * C * 2 <= (C == 4 ? 4LL * sms / 5 : sms)) C *= 2;
+    const bool deep = rank > 64 || (5 * tiles128 * C >= 4LL * sms && tiles128 * C <= sms);
     if (!deep)
-        while (C < 8 && tiles * C * 2 <= 2LL * sms) C *= 2;
+        while (C < 8 && tiles128 * C * 2 <= 2LL * sms) C *= 2;
     CUtensorMap maps[4];
     const uint32_t box_rows = LORA_TALL_BOX_ROWS;
     rdot_status ms = encode_2d(&maps[0], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, x, k, m, k * 2, 64, box_rows);

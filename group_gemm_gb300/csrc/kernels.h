@@ -269,9 +269,11 @@ struct LoraArgs {
     void* t;                     // device bf16 [M, rank], or null
     int M, K, N, G, rank;
 };
-// Few rows: tiles of LORA_FEW_ROWS rows. C: blocks per cluster.
-cudaError_t launch_lora_apply(const LoraArgs& a, int C, cudaStream_t stream);
+// Few rows: tiles of LORA_FEW_ROWS rows, D clusters of C blocks to each, `blocks` of them on an SM at once (at most
+// lora_apply_blocks).
+cudaError_t launch_lora_apply(const LoraArgs& a, int C, int D, int blocks, cudaStream_t stream);
 constexpr int LORA_FEW_ROWS = 16;
+constexpr int lora_apply_blocks(int rank) { return rank <= 16 ? 5 : rank <= 32 ? 4 : 2; }
 // Many rows, the tcgen05 form (lora_tall.cu): 128-row tiles. maps: x and base [M, width], boxes
 // (64, 32), neither read with an order; first and second [G, rank, width], boxes (64, lora_tall_box_rank, 1); all
 // 128-byte swizzled. Without a base its map is not read. C: blocks per cluster; deep: one block per SM with a

@@ -10,8 +10,12 @@
 // A cluster of C blocks takes a tile: each contracts its share of the columns of x, the fp32 partial sums are
 // added through distributed shared memory in a fixed order, and each then writes its share of the output's
 // columns. So a few rows still spread over many SMs, and results do not depend on timing. 64 rows over 256
-// adapters, 4096 -> 14336, rank 16: 20.4 us with C = 8, 72 us with C = 1. Stages of 128 columns, six in the ring:
-// 64 columns, four in the ring, 24.6 us.
+// adapters, 4096 -> 14336, rank 16: 18.3 us with C = 8, 72 us with C = 1. With very few tiles D clusters take one:
+// each forms all of t, and writes a D-th of the columns (1 row, 4096 -> 14336, rank 64: D = 1 23.6, D = 8 14.3 us).
+// The ring is as deep as it can be with the blocks that have to share an SM: a second round of blocks costs more than
+// the loads a longer ring has in flight (the 64 rows above: six stages, three blocks on an SM 24.8, five 18.3, four
+// 20.2; 128 rows of 128 adapters: 25.4, 25.5 and 20.8; rank 128, 64 rows of 16: one block with five stages 38, two with
+// three 27). Stages of 128 columns: of 64 a fifth slower.
 //
 // t keeps fp32 accuracy into the second product: it enters as two bf16 terms, t = hi + lo with lo the rounded
 // rest (relative error 2^-16, below the output's own rounding of 2^-8), two MMAs in place of one. hi is also
@@ -26,7 +30,7 @@ namespace rdot {
 
 namespace {
 
-template <int RP_>
+template <int RP_, int STAGES_>
 struct ApplyCfg {
     static constexpr int R = LORA_FEW_ROWS;            // rows of a tile: an MMA's
     static constexpr int RP = RP_;                     // rank, rounded up
@@ -34,7 +38,7 @@ struct ApplyCfg {
     static constexpr int BK = RP <= 64 ? 128 : 64;     // columns per stage
     static constexpr int PITCH = 2 * BK + 16;          // bytes: 16 off a multiple of 128, so ldmatrix has no conflicts
     static constexpr int SLOT = (R + RP) * PITCH;      // x or base rows, then weight rows
-    static constexpr int STAGES = RP <= 16 ? 6 : RP <= 32 ? 5 : RP <= 64 ? 4 : 5;
+    static constexpr int STAGES = STAGES_;
     static constexpr int PP = RP + 4;                  // pitch of the partial sums (fp32)
     static constexpr int TP = RP + 8;                  // pitch of hi and lo (bf16)
     static constexpr int PART = WK * R * PP * 4;
@@ -42,7 +46,7 @@ struct ApplyCfg {
 };
 
 template <class Cfg>
-__global__ void __launch_bounds__(LORA_THREADS) lora_apply_kernel(LoraArgs a) {
+__global__ void __launch_bounds__(LORA_THREADS) lora_apply_kernel(LoraArgs a, int D) {
     constexpr int R = Cfg::R, RP = Cfg::RP, WK = Cfg::WK, BK = Cfg::BK, PITCH = Cfg::PITCH;
     constexpr int S = Cfg::STAGES, PP = Cfg::PP, TP = Cfg::TP;
     extern __shared__ __align__(128) uint8_t smem[];
@@ -54,17 +58,19 @@ __global__ void __launch_bounds__(LORA_THREADS) lora_apply_kernel(LoraArgs a) {
     const int C = static_cast<int>(cluster_ctas()), rank = static_cast<int>(cluster_ctarank());
 
     grid_dependency_enter();
-    const LoraTile tile = lora_find_tile<R, LORA_THREADS>(a.group_sizes, a.G, a.M, static_cast<int>(blockIdx.x) / C);
+    const LoraTile tile = lora_find_tile<R, LORA_THREADS>(a.group_sizes, a.G, a.M, static_cast<int>(blockIdx.x) / (C * D));
     if (tile.rows == 0) return;   // the whole cluster
+    const int part_n = static_cast<int>(blockIdx.x) / C % D;
     const bool live = tile.g < a.G;
     lora_tile_rows<R, LORA_THREADS>(row_of, tile, a.order, a.M);
     __syncthreads();
 
     const int nk = live ? (a.K + BK - 1) / BK : 0, nn = (a.N + BK - 1) / BK;
-    // this block's stages: chunks rank, rank + C, ... of both widths, so that the cluster reads and writes
-    // neighbouring columns at a time
+    // this block's stages: chunks rank, rank + C, ... of x's width, so that the cluster reads neighbouring columns at a
+    // time; of the output's the same over the tile's D clusters
+    const int rank_n = part_n * C + rank, step_n = C * D;
     const int first_stages = nk > rank ? (nk - rank + C - 1) / C : 0;
-    int second_stages = nn > rank ? (nn - rank + C - 1) / C : 0;
+    int second_stages = nn > rank_n ? (nn - rank_n + step_n - 1) / step_n : 0;
     if (!live && a.base == a.out) second_stages = 0;   // rows without an adapter, in place: they stay as they are
     const int stages = first_stages + second_stages;
     const uint32_t ring = smem_u32(smem);
@@ -75,7 +81,7 @@ __global__ void __launch_bounds__(LORA_THREADS) lora_apply_kernel(LoraArgs a) {
             constexpr int V = BK / 8;   // pieces of a row
             const bool one = i < first_stages;
             const int width = one ? a.K : a.N;
-            const int c0 = ((one ? i : i - first_stages) * C + rank) * BK + (tid % V) * 8;
+            const int c0 = (one ? i * C + rank : (i - first_stages) * step_n + rank_n) * BK + (tid % V) * 8;
             const uint16_t* rows = static_cast<const uint16_t*>(one ? a.x : a.base);
             const uint16_t* weight = static_cast<const uint16_t*>(one ? a.first : a.second);
             const bool in = c0 < width;
@@ -173,7 +179,7 @@ __global__ void __launch_bounds__(LORA_THREADS) lora_apply_kernel(LoraArgs a) {
             split_bf16x2(v[2], v[3], hi.y, lo.y);
             *reinterpret_cast<uint2*>(thi + r * TP + c) = hi;
             *reinterpret_cast<uint2*>(tlo + r * TP + c) = lo;
-            if (rank == 0 && a.t && r < tile.rows && in)
+            if (rank_n == 0 && a.t && r < tile.rows && in)
                 *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.t) + static_cast<long long>(tile.p0 + r) * a.rank + c) = hi;
         }
         if (C > 1) {
@@ -181,7 +187,7 @@ __global__ void __launch_bounds__(LORA_THREADS) lora_apply_kernel(LoraArgs a) {
             cluster_arrive();   // this block has read the others' sums
         }
         __syncthreads();
-    } else if (rank == 0 && a.t) {
+    } else if (rank_n == 0 && a.t) {
         for (long long e = tid; e < static_cast<long long>(tile.rows) * a.rank / 4; e += LORA_THREADS)
             reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.t) + static_cast<long long>(tile.p0) * a.rank)[e] = make_uint2(0u, 0u);
     }
@@ -249,7 +255,7 @@ __global__ void __launch_bounds__(LORA_THREADS) lora_apply_kernel(LoraArgs a) {
         __syncwarp();
         // the warp's rows and columns of the stage, 16 bytes a lane
         constexpr int V = COLS / 8;
-        const int c0 = ((i - first_stages) * C + rank) * BK + wk * COLS + (lane % V) * 8;
+        const int c0 = ((i - first_stages) * step_n + rank_n) * BK + wk * COLS + (lane % V) * 8;
 #pragma unroll
         for (int r = lane / V; r < 16; r += 32 / V) {
             const int row = row_of[r];
@@ -262,23 +268,29 @@ __global__ void __launch_bounds__(LORA_THREADS) lora_apply_kernel(LoraArgs a) {
 }
 
 template <class Cfg>
-cudaError_t launch_cfg(const LoraArgs& a, long long tiles, int C, cudaStream_t stream) {
+cudaError_t launch_cfg(const LoraArgs& a, long long tiles, int C, int D, cudaStream_t stream) {
     auto kern = lora_apply_kernel<Cfg>;
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::SMEM);
     if (e != cudaSuccess) return e;
-    return launch_pdl_cluster(kern, dim3(static_cast<unsigned>(tiles * C)), dim3(LORA_THREADS), C, Cfg::SMEM, stream, a);
+    return launch_pdl_cluster(kern, dim3(static_cast<unsigned>(tiles * C * D)), dim3(LORA_THREADS), C, Cfg::SMEM, stream, a, D);
 }
 
 }  // namespace
 
-cudaError_t launch_lora_apply(const LoraArgs& a, int C, cudaStream_t stream) {
+cudaError_t launch_lora_apply(const LoraArgs& a, int C, int D, int blocks, cudaStream_t stream) {
     constexpr int R = LORA_FEW_ROWS;
     // a tile more for each group that ends inside one, one more for the rows of no group
     const long long tiles = (static_cast<long long>(a.M) + R - 1) / R + (a.G < a.M ? a.G : a.M) + 1;
-    if (a.rank <= 16) return launch_cfg<ApplyCfg<16>>(a, tiles, C, stream);
-    if (a.rank <= 32) return launch_cfg<ApplyCfg<32>>(a, tiles, C, stream);
-    if (a.rank <= 64) return launch_cfg<ApplyCfg<64>>(a, tiles, C, stream);
-    return launch_cfg<ApplyCfg<128>>(a, tiles, C, stream);
+    // the deepest ring with which that many blocks fit an SM's shared memory
+    if (a.rank <= 16)
+        return blocks <= 3 ? launch_cfg<ApplyCfg<16, 6>>(a, tiles, C, D, stream)
+             : blocks <= 4 ? launch_cfg<ApplyCfg<16, 5>>(a, tiles, C, D, stream)
+                           : launch_cfg<ApplyCfg<16, 4>>(a, tiles, C, D, stream);
+    if (a.rank <= 32)
+        return blocks <= 2 ? launch_cfg<ApplyCfg<32, 5>>(a, tiles, C, D, stream)
+                           : launch_cfg<ApplyCfg<32, 3>>(a, tiles, C, D, stream);
+    if (a.rank <= 64) return launch_cfg<ApplyCfg<64, 4>>(a, tiles, C, D, stream);
+    return launch_cfg<ApplyCfg<128, 3>>(a, tiles, C, D, stream);
 }
 
 }  // namespace rdot

@@ -108,6 +108,12 @@ for _i, (_m, _g) in enumerate([(4100, 1), (4100, 3), (8000, 3), (12000, 40), (70
 APPLY += [(4500, 8, 8, 8, [4500], True, True, True), (4500, 2056, 8, 16, [4000, 100], False, True, True),
           (4500, 64, 2056, 32, [100, 129, 4200], True, False, True), (4500, 64, 64, 64, [0, 0], True, False, False),
           (4500, 64, 64, 64, [0, 0], True, True, False), (5000, 72, 136, 16, [-3, 2000, 1 << 30, 5], True, True, True)]
+# Few tiles, whose columns several clusters divide; 16-row tiles beside the border to the 128-row form at each size of rank
+APPLY += [(1, 4096, 14336, 32, [0, 1, 0], True, True, True), (2, 264, 8200, 64, [1], False, True, True),
+          (9, 4096, 14336, 16, [1, 0, 3, 1, 1], True, True, True), (20, 520, 5000, 128, [7, 1, 9], True, False, True)]
+for _i, (_m, _g) in enumerate([(90, 80), (128, 128), (520, 16), (768, 24), (800, 40), (1200, 32), (2000, 32), (3000, 32), (3000, 4)]):
+    for _r in (16, 32, 56, 104):
+        APPLY.append((_m, 328 - 8 * _i, 200 + 64 * _i, _r, ragged(_m, _g, 50 + _i, 9), _i % 4 != 1, _i % 3 != 2, _r != 32))
 
 
 @pytest.mark.parametrize("m,k,n,r,sizes,order,base,scale", APPLY)
