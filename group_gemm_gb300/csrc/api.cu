@@ -1652,9 +1652,9 @@ rdot_status lora_apply(const void* x, const void* first, const void* second, con
     }
     // Of the 128-row form, one block per SM with a deep ring where clusters of it fill the SMs (8192 rows of 8 groups,
     // 4096 -> 4096, rank 64: 49 us against 57 for two blocks), else two (8192 rows of 32 groups through an order,
-    // rank 16: 77 against 90). Clusters of 8 such blocks fit on four fifths of the SMs (512 rows of 16 groups, rank 128:
-    // 56 us where they wait for a second round, 37 in clusters of 4).
-    while (C < 8 && tiles128 * C * 2 <= (C == 4 ? 4LL * sms / 5 : sms)) C *= 2;
+    // rank 16: 77 against 90). Clusters of 8 such blocks fit on four fifths of the SMs, of 4 on 19 in 20 (512 rows of 16
+    // groups, rank 128: 56 us where clusters of 8 wait for a second round, 37 in clusters of 4).
+    while (C < 8 && tiles128 * C * 2 <= (C == 4 ? 4LL * sms / 5 : C == 2 ? 19LL * sms / 20 : sms)) C *= 2;
     const bool deep = rank > 64 || (5 * tiles128 * C >= 4LL * sms && tiles128 * C <= sms);
     if (!deep)
         while (C < 8 && tiles128 * C * 2 <= 2LL * sms) C *= 2;

@@ -527,7 +527,10 @@ cudaError_t launch_lora_grad(const LoraGradArgs& a, bool codes, bool out_bf16, i
     const long long items = groups * ((a.C + GC - 1) / GC);
     const long long stages = (a.M + groups * GR - 1) / (groups * GR);
     int C = 1;
-    while (C < 8 && items * C * 2 <= sm_count && 2 * C <= stages) C *= 2;
+    // Clusters of blocks that fill an SM each: of two on all SMs, of four on 19 in 20, of eight on four in five; with more,
+    // some wait for a second round (one group, 16384 rows of 1024 columns, rank 16: C = 1 79 us, C = 8 20; of 2048: C = 4 30,
+    // C = 8 39; of 4608: C = 2 49, C = 4 39; of 4736: 49 and 61).
+    while (C < 8 && items * C * 2 <= (C == 4 ? 4 * sm_count / 5 : C == 2 ? 19 * sm_count / 20 : sm_count) && 2 * C <= stages) C *= 2;
     const int slots = sm_count;
     if (codes) return a.order ? launch_rank<true, true>(a, out_bf16, C, slots, timeout_ns, stream) : launch_rank<true, false>(a, out_bf16, C, slots, timeout_ns, stream);
     return a.order ? launch_rank<false, true>(a, out_bf16, C, slots, timeout_ns, stream) : launch_rank<false, false>(a, out_bf16, C, slots, timeout_ns, stream);
