@@ -453,7 +453,8 @@ RDOT_API rdot_status rdot_dequantize_mxfp8(const uint8_t* codes, const uint8_t* 
  * (rdot_moe_permute) need no order. A negative size counts as 0 and ends are clamped to M, as in the
  * products; positions past the last group have no adapter: their rows of out are base's (zeros without a
  * base), their rows of t zeros. order must hold every row once; an entry outside [0, M) counts as none (its
- * row is not written). There is no workspace; every call can be captured in a CUDA graph. They run on the calling thread's current device and never synchronise the host.
+ * row is not written). There is no workspace; every call can be captured in a CUDA graph. They run on the
+ * calling thread's current device and never synchronise the host.
  *
  * Sums are fp32 in a fixed order. t enters the second product with an error of 2^-16, out is rounded to
  * bf16 once. m = 0 launches nothing, except that the weight gradient still writes its zeros. k % 8 == 0,
@@ -462,9 +463,9 @@ RDOT_API rdot_status rdot_dequantize_mxfp8(const uint8_t* codes, const uint8_t* 
  * and scale, any for z_scale. */
 #define RDOT_LORA_MAX_RANK 128
 
-/* The forward and the gradient of the input wait on barriers of their own where groups have many rows. A wait
- * that runs out (a broken pipeline; 2 s by default) ends its kernel early with RDOT_STATUS_BIT_TIMEOUT in a word
- * that the library keeps on each device, sticky until it is cleared.
+/* The weight gradient, and where groups have many rows the forward and the gradient of the input, wait on
+ * barriers of their own. A wait that runs out (a broken pipeline; 2 s by default) ends its kernel early with
+ * RDOT_STATUS_BIT_TIMEOUT in a word that the library keeps on each device, sticky until it is cleared.
  * rdot_lora_read_status copies the current device's word into *flags, synchronises the stream and returns
  * RDOT_ERR_DEVICE_TIMEOUT if the bit is set, else RDOT_OK; rdot_lora_clear_status clears it on the stream.
  * rdot_lora_set_wait_timeout overrides the limit (ns) for later calls of this process; 0 restores the default. */
