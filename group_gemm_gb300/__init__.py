@@ -920,6 +920,14 @@ def dequantize_mxfp8(codes, scales, dtype=None, stream=None):
     return out
 
 
+def _rows32(rows):
+    """Row numbers or ids as contiguous int32; what 32 bits do not hold stays outside every range."""
+    import torch
+    if rows.dtype == torch.int64:
+        rows = rows.clamp(-1, 2 ** 31 - 1)
+    return rows.to(torch.int32).contiguous()
+
+
 def lora_group(ids, n_adapters, stream=None):
     """Sorts a batch's rows by adapter for the calls below: returns ``(group_sizes int32 [n_adapters], order
     int32 [M])`` for ids int [M] (outside [0, n_adapters): no adapter, sorted last)."""
@@ -928,11 +936,9 @@ def lora_group(ids, n_adapters, stream=None):
         raise ValueError("ids must be [M]")
     s = _run_stream(stream, ids.device)
     with torch.cuda.stream(s):
-        if ids.dtype != torch.int32:     # an id past 32 bits stays outside the range
-            ids = ids.clamp(-1, 2 ** 31 - 1).to(torch.int32)
         sizes = torch.empty(n_adapters, dtype=torch.int32, device=ids.device)
         order = torch.empty(ids.shape[0], dtype=torch.int32, device=ids.device)
-        rdot_lora_group(ids.contiguous(), n_adapters, sizes, order, s)
+        rdot_lora_group(_rows32(ids), n_adapters, sizes, order, s)
     return sizes, order
 
 
@@ -957,7 +963,7 @@ def _lora(call, x, first, second, down, up, group_sizes, order, scale, base, out
             out = torch.empty((m, width), dtype=torch.bfloat16, device=x.device)
         t = torch.empty((m, r), dtype=torch.bfloat16, device=x.device)
         call(x.contiguous(), down.contiguous(), up.contiguous(), group_sizes.to(torch.int32).contiguous(), out, t,
-             order=None if order is None else order.to(torch.int32).contiguous(),
+             order=None if order is None else _rows32(order),
              scale=None if scale is None else scale.to(torch.float32).contiguous(),
              base=None if base is None else base.contiguous(), stream=s)
     return out, t
@@ -1005,7 +1011,7 @@ def lora_grad_weight(t, z, group_sizes, order=None, z_scale=None, out_dtype=None
         if dw is None:
             dw = torch.empty((g, r, width), dtype=out_dtype, device=t.device)
         rdot_lora_grad_weight(t.contiguous(), z.contiguous(), group_sizes.to(torch.int32).contiguous(), dw,
-                              order=None if order is None else order.to(torch.int32).contiguous(),
+                              order=None if order is None else _rows32(order),
                               z_scale=None if z_scale is None else z_scale.contiguous(), stream=s)
     return dw
 

@@ -64,6 +64,7 @@ struct GradCfg {
     static constexpr int SMEM = 1024 + RING + ROWS_BYTES;        // and the G + 1 offsets
     static constexpr uint32_t TMEM_COLS = RP <= 16 ? 128 : ACCS * RP;   // (they are read 32 columns at a time)
     static_assert(RP * 512 <= RING, "the partial sums fit the ring");
+    static_assert(SMEM + (RDOT_MAX_GROUPS + 1) * 4 <= 227 * 1024 - 2048, "with the static shared memory it fits a block");
 };
 
 __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
@@ -505,7 +506,9 @@ cudaError_t launch_cfg(const LoraGradArgs& a, bool out_bf16, int C, int slots, u
     using Cfg = GradCfg<RP, CODES, ORDER>;
     auto kern = lora_grad_kernel<Cfg>;
     const int shm = Cfg::SMEM + (a.G + 1) * static_cast<int>(sizeof(int32_t));
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, shm);
+    // one limit for every call: another thread may launch with other groups in between
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               Cfg::SMEM + (RDOT_MAX_GROUPS + 1) * static_cast<int>(sizeof(int32_t)));
     if (e != cudaSuccess) return e;
     const int blocks = (a.C + GC - 1) / GC;
     const long long items = static_cast<long long>(a.G) * blocks;

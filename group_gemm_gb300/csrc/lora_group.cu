@@ -128,8 +128,10 @@ __global__ void __launch_bounds__(GROUP_THREADS) lora_group_kernel(const int32_t
 
 cudaError_t launch_lora_group(const int32_t* ids, int M, int G, int32_t* group_sizes, int32_t* order,
                               cudaStream_t stream) {
-    const size_t shm = static_cast<size_t>(GROUP_WARPS + 1) * (G + 1) * sizeof(int32_t);
-    const cudaError_t e = cudaFuncSetAttribute(lora_group_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(shm));
+    const auto bytes = [](int groups) { return (GROUP_WARPS + 1) * (groups + 1) * static_cast<int>(sizeof(int32_t)); };
+    const size_t shm = bytes(G);
+    // one limit for every call: another thread may launch with other groups in between
+    const cudaError_t e = cudaFuncSetAttribute(lora_group_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes(RDOT_MAX_GROUPS));
     if (e != cudaSuccess) return e;
     // (16384 rows of 64 adapters: 17.0, 10.6, 7.9 and 7.0 us with 1, 2, 4 and 8 blocks; 64 rows of 256: 4.7 with one)
     const int C = M <= 1024 ? 1 : M <= 4096 ? 4 : 8;

@@ -370,6 +370,51 @@ def test_two_streams_at_once(more):
             assert torch.equal(o[0], r[0]) and torch.equal(o[1], r[1]) and torch.equal(w, rw)
 
 
+def test_threads_with_different_groups():
+    """Host threads call with few and many groups at once, each on its own stream."""
+    import threading
+    failed = []
+
+    def work(i, g):
+        try:
+            stream = torch.cuda.Stream()
+            with torch.cuda.stream(stream):
+                gen = torch.Generator(device=DEV).manual_seed(100 + i)
+                ids = torch.randint(-1, g, (300,), generator=gen, device=DEV, dtype=torch.int32)
+                t, z = randn(gen, (300, 8)), randn(gen, (300, 64))
+                key = torch.where(ids < 0, g, ids).long()
+                want = None
+                for _ in range(40):
+                    sizes, order = gg.lora_group(ids, g, stream=stream)
+                    dw = gg.lora_grad_weight(t, z, sizes, order, stream=stream)
+                    want = dw if want is None else want
+                    if not (torch.equal(order.long(), torch.argsort(key, stable=True)) and torch.equal(dw, want)):
+                        failed.append((g, "another result"))
+        except Exception as e:   # a thread's exception would be lost
+            failed.append((g, repr(e)))
+
+    threads = [threading.Thread(target=work, args=(i, g)) for i, g in enumerate((1, 1024, 17, 600))]
+    for th in threads:
+        th.start()
+    for th in threads:
+        th.join()
+    torch.cuda.synchronize()
+    assert not failed, failed
+
+
+def test_row_numbers_past_32_bits():
+    """An int64 entry of the order that 32 bits do not hold counts as none, not as the row of its low bits."""
+    d = make(40, 64, 64, 1, 8, [40], True, 30)
+    row = int(d["order"][3])
+    wide = d["order"].long()
+    wide[3] = 2 ** 32 + int(d["order"][5])
+    out = torch.full((40, 64), 7.0, dtype=torch.bfloat16, device=DEV)
+    gg.lora_forward(d["x"], d["down"], d["up"], d["sizes"], wide, d["scale"], d["base_n"], out=out)
+    ref = gg.lora_forward(d["x"], d["down"], d["up"], d["sizes"], d["order"], d["scale"], d["base_n"])[0]
+    keep = torch.arange(40, device=DEV) != row
+    assert torch.equal(out[keep], ref[keep]) and torch.all(out[row] == 7)
+
+
 @pytest.mark.parametrize("m", [130, 5000])
 def test_captured_step_follows_its_inputs(m):
     """A captured group + forward + gradients replays with other ids, rows and sizes than it was captured with, on
