@@ -1622,42 +1622,52 @@ rdot_status lora_apply(const void* x, const void* first, const void* second, con
     // How many groups have rows, about (all of few, most of as many groups as rows), and the tiles of either form.
     const long long used = std::min<long long>(routed, 6LL * m * groups / (5LL * (m + groups)) + 1);
     const long long tiles16 = std::max(used, m / LORA_FEW_ROWS + used / 2);
-    const long long tiles128 = std::max(used, m / LORA_TALL_ROWS + (3 * used + 3) / 4);   // three in four end inside one
-    // Tiles of 16 rows read a group's weights for each 16 of its rows, tiles of 128 rows are few and half empty where groups
-    // are short. All times in us, 16-row tiles / 128-row tiles, 4096 -> 4096 through an order. Up to rank 32: 2048 rows of 4
-    // groups 22 / 31, 3000 of 4 35 / 33, 3000 of 32 29 / 45, 6000 of 32 59 / 54, 8192 of 128 59 / 97 (without an order
-    // 59 / 70; 4096 of 32, rank 32 41 / 41). Up to rank 64: 900 rows of 32 groups 26 / 35, 1200 of 32 39 / 37, and, where
-    // clusters of four 128-row blocks are more than the SMs, 2000 of 32 41 / 43, 2500 of 32 66 / 45. Above: 512 rows of 2
-    // groups 27 / 33, 800 of 40 42 / 70, 1024 of 8 38 / 34, 5120 of 256 225 / 172.
-    const bool crowded = 4 * tiles128 > sms;
-    const bool few = rows <= (rank <= 64 ? LORA_FEW_ROWS : LORA_FEW_ROWS / 2) ||
-                     (rank <= 32 ? tiles16 <= sms || rows <= (a.order ? 128 : 96)
-                                 : (rank <= 64 ? 1 : 2) * tiles16 <= (crowded ? sms : sms / 2));
-    int C = 1;
+    const long long tiles128 = std::max(used, m / LORA_TALL_ROWS + (5 * used + 7) / 8);
+    // Tiles of 16 rows read a group's weights for each 16 of its rows; tiles of 128 rows are few, and half empty where groups
+    // are short, the more so where clusters of four of their blocks are more than the SMs hold. All times in us, 16-row tiles /
+    // 128-row tiles, 4096 -> 4096 through an order. Up to rank 32: 2048 rows of 4 groups 22 / 29, 4096 of 4 35 / 35, 8192 of
+    // 4 58 / 49, 3000 of 32 29 / 39, 6000 of 32 59 / 48, 8192 of 128 59 / 74; without an order, rank 32: 1500 of 4 22 / 24,
+    // 8192 of 128 72 / 66. Up to rank 64: 1200 rows of 4 groups 29 / 29, 1200 of 32 30 / 37, 1600 of 4 38 / 30, 2000 of 32
+    // 38 / 37, 2560 of 128 66 / 80. Above: 512 rows of 2 groups 27 / 33, 800 of 40 42 / 47, 1024 of 8 38 / 34, 1024 of 32
+    // 49 / 43, 2048 of 256 131 / 162, 5120 of 256 225 / 172.
+    // Clusters of 128-row blocks, one on an SM or two: eight stages or more to a block, which the join costs (5000 rows of 3
+    // groups, rank 64, 128 -> 128: C = 1 14, C = 3 18; 1024 -> 1024: 30 and 24).
+    const int most = static_cast<int>(std::max<long long>(1, std::min<long long>(8, (k + n) / (8 * 64))));
+    const int Cd = std::min(lora_cluster(tiles128, 1, sms), most), Cs = std::min(lora_cluster(tiles128, 2, sms), most);
+    // Of 16-row blocks: as large as the SMs hold at once (256 rows of 64 groups, 4096 -> 4096, rank 64: C = 2 33, C = 4 27,
+    // C = 8 35; 1200 rows of 4 groups: C = 2 37, C = 3 29), with room for more groups than expected above four (64 rows of 64
+    // groups, 1024 -> 1024, rank 64: C = 6 14, C = 7 20). Up to rank 32 more of them share an SM, and even shares count for
+    // more (1500 rows of 32 groups: C = 6 22, C = 4 20).
+    const int room = lora_apply_blocks(rank) * sms;
+    int Cf = 8;
+    if (rank > 32) {
+        Cf = lora_cluster(tiles16, lora_apply_blocks(rank), sms);
+        while (rows <= LORA_FEW_ROWS && Cf > 4 && 100 * tiles16 * Cf > 82LL * room) --Cf;
+    } else {
+        while (Cf > 1 && 20 * tiles16 * Cf > (Cf == 8 ? 18LL : Cf == 3 || (Cf == 4 && rank <= 16) ? 19LL : 21LL) * room)
+            Cf = Cf == 4 ? 3 : Cf == 3 ? 2 : Cf / 2;
+    }
+    const bool few = rank <= 32   ? tiles16 <= sms || (a.order && 3 * tiles16 <= 4LL * sms) || rows <= (a.order ? 128 : rank <= 16 ? 96 : 48)
+                     : rank <= 64 ? rows <= 20 || Cf >= (400 * tiles128 > 95LL * sms ? 2 : 3)
+                                  : rows <= 8 || Cf >= (400 * tiles128 > 95LL * sms ? 4 : 7);
     if (few) {
-        // Clusters as large as the SMs hold at once, with what a cluster's shape leaves over (256 rows of 64 groups, 4096 ->
-        // 4096, rank 64: C = 2 33, C = 4 27, C = 8 35 us; 64 rows of 256 groups, 4096 -> 14336, rank 16: C = 4 28,
-        // C = 8 23); past eight blocks the output's columns are divided among D clusters of a tile, each with the whole
-        // first product (16 rows of 16 groups, 4096 -> 14336, rank 16: D = 1 16, D = 2 14, D = 4 14; rank 64: 25, 22, 31).
-        const auto fits = [&](int c, int blocks) {
-            return 20 * tiles16 * c <= 1LL * blocks * sms * (c >= 8 ? 18 : c == 4 && rank > 32 ? 19 : 21);
-        };
-        int blocks = lora_apply_blocks(rank);
-        while (C < 8 && fits(2 * C, blocks)) C *= 2;
-        int D = 1;
-        while (C == 8 && fits(C * D * 2, 2) && 128LL * C * D * 2 <= n) D *= 2;
-        while (blocks > 1 && fits(C * D, blocks - 1)) --blocks;
-        const cudaError_t e = launch_lora_apply(a, C, D, blocks, s);
+        // Past eight blocks the output's columns are divided among D clusters of a tile, each with the whole first product (16
+        // rows of 16 groups, 4096 -> 14336, rank 16: D = 1 16, D = 2 14, D = 4 14; rank 64: 25, 22, 31). Two stages or more to
+        // a block (16 rows of 16 groups, 128 -> 128, rank 16: C = 1 8, C = 8 10).
+        Cf = static_cast<int>(std::max<long long>(1, std::min<long long>(Cf, (k + n) / (2 * 128))));
+        int blocks = lora_apply_blocks(rank), D = 1;
+        while (Cf == 8 && 10 * tiles16 * 8 * D <= 9LL * sms && 128LL * 8 * D * 2 <= n) D *= 2;
+        while (blocks > 1 && 100 * tiles16 * Cf * D <= 85LL * (blocks - 1) * sms) --blocks;
+        const cudaError_t e = launch_lora_apply(a, Cf, D, blocks, s);
         return e == cudaSuccess ? RDOT_OK : cuda_fail(e, "lora launch");
     }
-    // Of the 128-row form, one block per SM with a deep ring where clusters of it fill the SMs (8192 rows of 8 groups,
-    // 4096 -> 4096, rank 64: 49 us against 57 for two blocks), else two (8192 rows of 32 groups through an order,
-    // rank 16: 77 against 90). Clusters of 8 such blocks fit on four fifths of the SMs, of 4 on 19 in 20 (512 rows of 16
-    // groups, rank 128: 56 us where clusters of 8 wait for a second round, 37 in clusters of 4).
-    while (C < 8 && tiles128 * C * 2 <= (C == 4 ? 4LL * sms / 5 : C == 2 ? 19LL * sms / 20 : sms)) C *= 2;
-    const bool deep = rank > 64 || (5 * tiles128 * C >= 4LL * sms && tiles128 * C <= sms);
-    if (!deep)
-        while (C < 8 && tiles128 * C * 2 <= 2LL * sms) C *= 2;
+    // Of the 128-row form, one block on an SM with a deep ring, or two. One where its clusters fill the SMs as well as two
+    // would, and tiles are half full or ranks high (4096 -> 4096: 8192 rows of 8 groups, rank 64 49 us against 57 for two;
+    // 2000 of 4 33 / 39; 4096 of 4 35 / 39; but 8192 of 4 through an order, rank 16 55 / 49, 1500 of 128 80 / 64, 8192 of 32 84 / 71 at rank 64,
+    // where one leaves half of the SMs without a tile).
+    const bool deep = rank > 64 || (2 * Cd >= Cs && tiles128 <= sms &&
+                                    ((rank > 32 && Cd > 1) || ((rank > 32 || !a.order || Cd >= 4) && m >= 64 * tiles128)));
+    const int C = deep ? Cd : Cs;
     CUtensorMap maps[4];
     const uint32_t box_rows = LORA_TALL_BOX_ROWS;
     rdot_status ms = encode_2d(&maps[0], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, x, k, m, k * 2, 64, box_rows);

@@ -273,6 +273,19 @@ struct LoraArgs {
 // lora_apply_blocks).
 cudaError_t launch_lora_apply(const LoraArgs& a, int C, int D, int blocks, cudaStream_t stream);
 constexpr int LORA_FEW_ROWS = 16;
+// Of a hundred blocks that the SMs could hold, how many of clusters of C find room at once, with one block on an SM or with
+// more (a cluster lies within one of the SMs' hardware groups, and leaves over what it does not divide). Measured as the
+// largest grids without a second round.
+constexpr int lora_cluster_room(int C, int per_sm) {
+    constexpr int one[9] = {0, 100, 100, 93, 95, 89, 86, 69, 79};
+    return per_sm == 1 ? one[C] : C <= 2 ? 105 : C <= 4 ? 95 : 92;
+}
+// The largest cluster, at most 8, of which `tiles` find room at once; 1 where none does.
+constexpr int lora_cluster(long long tiles, int per_sm, int sms) {
+    int C = 8;
+    while (C > 1 && 100 * tiles * C > static_cast<long long>(lora_cluster_room(C, per_sm)) * per_sm * sms) --C;
+    return C;
+}
 constexpr int lora_apply_blocks(int rank) { return rank <= 16 ? 5 : rank <= 32 ? 4 : 2; }
 // Many rows, the tcgen05 form (lora_tall.cu): 128-row tiles. maps: x and base [M, width], boxes
 // (64, 32), neither read with an order; first and second [G, rank, width], boxes (64, lora_tall_box_rank, 1); all

@@ -91,17 +91,17 @@ struct Items {
     const int32_t* off;     // [G + 1] shared: the groups' first positions
     int G, blocks;
     int dg, dcb;            // from one of the block's items to its next: groups, column blocks (no division on the way)
-    int rank, shift;        // the block's share of a group's stages: part `rank` of 2^shift
+    int rank, C;            // the block's share of a group's stages: part `rank` of C
 
     // The block's rows of group g: n from sorted position p0 on.
     __device__ __forceinline__ void share(int g, int& p0, int& n) const {
         p0 = off[g];
         n = off[g + 1] - p0;
-        if (shift == 0) return;
-        const long long all = (static_cast<long long>(n) + GR - 1) / GR;
-        const long long s0 = all * rank >> shift, s1 = all * (rank + 1) >> shift;
+        if (C == 1) return;
+        const unsigned all = (static_cast<unsigned>(n) + GR - 1) / GR;   // < 2^25
+        const unsigned s0 = all * rank / C, s1 = all * (rank + 1) / C;
         p0 += static_cast<int>(s0 * GR);
-        n = static_cast<int>(min(s1 * GR, static_cast<long long>(n)) - s0 * GR);
+        n = static_cast<int>(min(s1 * GR, static_cast<unsigned>(n)) - s0 * GR);
     }
     __device__ __forceinline__ void step(int& g, int& cb) const {
         g += dg;
@@ -204,10 +204,9 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1) lora_grad_kernel(LoraGradArgs
     tc_fence_after();
     const uint32_t tmem = tmem_holder;
     const WaitGuard guard{&abort_flag, &g_status, timeout_ns};
-    const int shift = 31 - __clz(C);   // C is a power of two
-    const int first = static_cast<int>(blockIdx.x) >> shift, step = static_cast<int>(gridDim.x) >> shift;
+    const int first = static_cast<int>(blockIdx.x) / C, step = static_cast<int>(gridDim.x) / C;
     const int first_g = first / blocks, first_cb = first - first_g * blocks;
-    const Items it{off, a.G, blocks, step / blocks, step % blocks, rank, shift};
+    const Items it{off, a.G, blocks, step / blocks, step % blocks, rank, C};
     const int ranks = (a.rank + 15) & ~15;   // the MMAs' N; t's columns past the rank are zeros
 
     if (warp < LOADERS) {
@@ -530,12 +529,13 @@ cudaError_t launch_lora_grad(const LoraGradArgs& a, bool codes, bool out_bf16, i
                              cudaStream_t stream) {
     const long long groups = a.G < a.M ? a.G : a.M > 0 ? a.M : 1;   // groups that can have a row
     const long long items = groups * ((a.C + GC - 1) / GC);
-    const long long stages = (a.M + groups * GR - 1) / (groups * GR);
-    int C = 1;
-    // Clusters of blocks that fill an SM each: of two on all SMs, of four on 19 in 20, of eight on four in five; with more,
-    // some wait for a second round (one group, 16384 rows of 1024 columns, rank 16: C = 1 79 us, C = 8 20; of 2048: C = 4 30,
-    // C = 8 39; of 4608: C = 2 49, C = 4 39; of 4736: 49 and 61).
-    while (C < 8 && items * C * 2 <= (C == 4 ? 4 * sm_count / 5 : C == 2 ? 19 * sm_count / 20 : sm_count) && 2 * C <= stages) C *= 2;
+    const int stages = static_cast<int>((a.M + groups * GR - 1) / (groups * GR));
+    // Few items: clusters as large as the SMs hold (one group, rank 16, 16384 rows of 1024 columns: C = 1 79 us, C = 8 20; of
+    // 2048: C = 4 30, C = 6 27, C = 8 39; of 4736: C = 2 49, C = 3 43, C = 4 61), unless they save fewer stages than the
+    // join costs (8 groups, rank 64, 4096 x 640: C = 1 12.3, C = 2 14.4).
+    int C = lora_cluster(items, 1, sm_count);
+    while (C > 1 && 2 * C > stages) --C;
+    if (stages * (C - 1) < (a.rank <= 64 ? 6 : 10) * C) C = 1;
     const int slots = sm_count;
     if (codes) return a.order ? launch_rank<true, true>(a, out_bf16, C, slots, timeout_ns, stream) : launch_rank<true, false>(a, out_bf16, C, slots, timeout_ns, stream);
     return a.order ? launch_rank<false, true>(a, out_bf16, C, slots, timeout_ns, stream) : launch_rank<false, false>(a, out_bf16, C, slots, timeout_ns, stream);

@@ -280,19 +280,20 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::BLOCKS)
                 *reinterpret_cast<uint4*>(tmat + place(r, RP + h)) = lo;
             }
         } else {
-            // Each block adds the partial sums of ROWS / C rows and gives every block hi and lo of them. (Each adding all
+            // Each block adds the partial sums of a C-th of the rows and gives every block hi and lo of them. (Each adding all
             // rows reads C times as much from the others: 8192 rows, rank 64, clusters of 8: 88 us against 74.)
             float4* mine = part + c0 / 4 * ROWS + r;
 #pragma unroll
             for (int c = 0; c < QUADS; ++c) mine[c * ROWS] = v[c];
             cluster_sync();
             constexpr int PIECES = RP / 8, MAX = (ROWS / 2 * PIECES + 255) / 256;   // a lane's pieces: MAX with two blocks
-            const int share = ROWS / C;
+            const int share = (ROWS + C - 1) / C;   // the last block's may be shorter
             uint4 hi[MAX], lo[MAX];
 #pragma unroll
             for (int k = 0; k < MAX; ++k) {
                 const int e = tid - 64 + 256 * k, row = rank * share + e % share, h = e / share * 8;
                 if (e >= share * PIECES) break;
+                if (row >= ROWS) continue;
                 float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
                 const uint32_t addr = smem_u32(part + h / 4 * ROWS + row);
 #pragma unroll 4
@@ -310,6 +311,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::BLOCKS)
             for (int k = 0; k < MAX; ++k) {
                 const int e = tid - 64 + 256 * k, row = rank * share + e % share, h = e / share * 8;
                 if (e >= share * PIECES) break;
+                if (row >= ROWS) continue;
                 for (int p = 0; p < C; ++p) {
                     const uint32_t peer = mapa_shared(smem_u32(tmat), p);
                     st_shared_cluster_u4(peer + place(row, h), hi[k]);

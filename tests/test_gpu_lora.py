@@ -114,6 +114,10 @@ APPLY += [(1, 4096, 14336, 32, [0, 1, 0], True, True, True), (2, 264, 8200, 64, 
 for _i, (_m, _g) in enumerate([(90, 80), (128, 128), (520, 16), (768, 24), (800, 40), (1200, 32), (2000, 32), (3000, 32), (3000, 4)]):
     for _r in (16, 32, 56, 104):
         APPLY.append((_m, 328 - 8 * _i, 200 + 64 * _i, _r, ragged(_m, _g, 50 + _i, 9), _i % 4 != 1, _i % 3 != 2, _r != 32))
+# Clusters of 7, 6, 5 and 3 blocks, which do not divide a tile's rows
+for _i, _m in enumerate([4000, 4700, 5500, 3000]):
+    for _r in (16, 32, 64, 72):
+        APPLY.append((_m, 1032 + 8 * _i, 960, _r, ragged(_m, 12 if _i < 3 else 60, 70 + _i, 40), _r != 32 or _i == 3, True, True))
 
 
 @pytest.mark.parametrize("m,k,n,r,sizes,order,base,scale", APPLY)
@@ -140,6 +144,7 @@ WEIGHT = [      # m, width, r, group sizes, order
     (515, 2048, 40, [100, 415], False), (700, 1056, 128, [333, 0, 300], True), (4099, 512, 64, [4000, 64, 30], True),
     (300, 64, 16, [0, 0], True), (128, 64, 8, [-5, 60, 1 << 30, 7], False), (2000, 224, 96, [1] * 1000 + [1000], True),
     (9000, 128, 16, [9000], False),
+    (3000, 2048, 16, [2990], True), (3000, 4736, 8, [3000], False), (2600, 3200, 40, [2600], True),
 ]
 
 
