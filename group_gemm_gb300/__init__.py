@@ -33,8 +33,9 @@ __all__ = [
     "quantize_mxfp4", "quantize_mxfp4_weight", "ragged_dot_mxfp4",
     "moe_unpermute_grad", "moe_permute_grad", "router_topk_grad",
     "rdot_quantize_mxfp8", "rdot_dequantize_mxfp8", "rdot_lora_group", "rdot_lora_forward", "rdot_lora_grad_input",
-    "rdot_lora_grad_weight", "rdot_lora_read_status", "rdot_lora_clear_status", "rdot_lora_set_wait_timeout", "quantize_mxfp8", "dequantize_mxfp8", "lora_group", "lora_forward", "lora_grad_input",
-    "lora_grad_weight", "EXPORTED_SYMBOLS",
+    "rdot_lora_grad_weight", "rdot_lora_read_status", "rdot_lora_clear_status", "rdot_lora_set_wait_timeout",
+    "quantize_mxfp8", "dequantize_mxfp8", "lora_group", "lora_forward", "lora_grad_input", "lora_grad_weight",
+    "EXPORTED_SYMBOLS",
 ]
 
 RDOT_OK, RDOT_ERR_INVALID_ARG, RDOT_ERR_UNSUPPORTED, RDOT_ERR_CUDA = 0, 1, 2, 3

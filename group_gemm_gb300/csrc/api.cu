@@ -1759,6 +1759,6 @@ const char* rdot_status_string(rdot_status status) {
 
 const char* rdot_last_cuda_error(void) { return g_last_cuda_error.c_str(); }
 
-int rdot_version(void) { return 104; }
+int rdot_version(void) { return 105; }
 
 }  // extern "C"
