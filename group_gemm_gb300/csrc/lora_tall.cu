@@ -5,9 +5,9 @@
 //   warp 0        producer: per stage 64 columns of the tile's rows (of x, then of base) and of the adapter's r
 //                 weight rows, by TMA into an S-slot ring, in boxes of 32 rows: a short tile loads no row past
 //                 its last box.
-//   warp 1        tcgen05.mma: t's sums [128 x r] over the columns of x, then, per 64 output columns, hi and lo
+//   warp 1        tcgen05.mma: t's sums [128 x r] over the columns of x, in stretches of 512, then, per 64 output columns, hi and lo
 //                 times the weights (K = 2r) into one of two accumulators.
-//   warps 2..9    t: tensor memory -> (sum over the cluster) -> scale -> hi, lo as the second product's A operand
+//   warps 2..9    t: tensor memory -> (sum of the stretches) -> (sum over the cluster) -> scale -> hi, lo as the second product's A operand
 //                 in shared memory; then the accumulators onto base, in base's own slot, and out as whole
 //                 128-byte lines. Warps 2..5 take the even stages, 6..9 the odd ones.
 //   warps 10..13  only with `order`: the rows by asynchronous 16-byte copies. (Four rows a TMA gather took
@@ -34,8 +34,12 @@ namespace {
 constexpr int ROWS = 128;
 constexpr int COLS = 64;            // columns per stage: one 128-byte swizzle row
 constexpr int BOX_ROWS = 32;
-constexpr uint32_t TMEM_COLS = 256; // t at 0, accumulators at 128 and 192
+constexpr uint32_t TMEM_COLS = 256; // t's sums at 0 and 128, then the accumulators at 128 and 192
 constexpr uint32_t ACC0 = 128;
+// Stages of a stretch of t's sums, 512 columns. The MMAs cut their sums to 24 bits at each step of 16 columns, always towards
+// 0 (1e-5 of t over 14336 columns), so they add up a stretch at most; the epilogue warps add the stretches, rounded.
+constexpr int STRETCH = 8;
+constexpr uint32_t U1 = 128;        // a stretch's sums lie at 0, the next one's here
 
 // Status bits of the waits that ran out in any call on this device, until they are cleared: the adapter calls have
 // no workspace to report into.
@@ -65,7 +69,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::BLOCKS)
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t* tmat = smem + S * Cfg::SLOT;
-    __shared__ __align__(8) uint64_t full[S], empty1[S], empty2[S], u_full, t_ready, acc_full[2], acc_empty[2], drain;
+    __shared__ __align__(8) uint64_t full[S], empty1[S], empty2[S], u_full[2], u_empty[2], t_ready, acc_full[2], acc_empty[2], drain;
     __shared__ uint32_t tmem_holder;
     __shared__ int abort_flag;
     __shared__ __align__(16) int row_of[ROWS];
@@ -98,9 +102,10 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::BLOCKS)
             mbar_init(&empty1[s], 1);   // first product: the MMAs have read the slot
             mbar_init(&empty2[s], 4);   // second: the epilogue warps have stored from it
         }
-        mbar_init(&u_full, 1);
         mbar_init(&t_ready, 256);
         for (int i = 0; i < 2; ++i) {
+            mbar_init(&u_full[i], 1);
+            mbar_init(&u_empty[i], 8);
             mbar_init(&acc_full[i], 1);
             mbar_init(&acc_empty[i], 4);
         }
@@ -180,8 +185,9 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::BLOCKS)
         const bool elected = elect_one();
         bool ok = true;
         for (int i = 0; i < n1; ++i) {
-            const int slot = i % S;
-            ok = mx4_wait_uniform(&full[slot], (i / S) & 1, guard);
+            const int slot = i % S, c = i / STRETCH, u = c & 1;
+            if (i % STRETCH == 0) ok = mx4_wait_uniform(&u_empty[u], ((c >> 1) & 1) ^ 1, guard);
+            ok = ok && mx4_wait_uniform(&full[slot], (i / S) & 1, guard);
             if (!ok) break;
             if (ORDER) fence_proxy_async_smem();   // the copies were made in the generic proxy
             tc_fence_after();
@@ -189,10 +195,10 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::BLOCKS)
             if (elected) {
 #pragma unroll
                 for (int kk = 0; kk < COLS / 16; ++kk)
-                    mma_f16(tmem, smem_desc_sw128(sa + kk * 32, 16, 1024), smem_desc_sw128(sb + kk * 32, 16, 1024), idesc1,
-                            (i | kk) != 0 ? 1u : 0u);
+                    mma_f16(tmem + u * U1, smem_desc_sw128(sa + kk * 32, 16, 1024), smem_desc_sw128(sb + kk * 32, 16, 1024), idesc1,
+                            (i % STRETCH | kk) != 0 ? 1u : 0u);
                 mma_commit(&empty1[slot]);
-                if (i == n1 - 1) mma_commit(&u_full);
+                if (i % STRETCH == STRETCH - 1 || i == n1 - 1) mma_commit(&u_full[u]);
             }
             __syncwarp();
         }
@@ -233,25 +239,32 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::BLOCKS)
         const uint32_t trow = tmem + (static_cast<uint32_t>(32 * q) << 16);
         float4* part = reinterpret_cast<float4*>(tmat);   // partial sums, [rank / 4][row]
         const float scale = a.scale ? __ldg(a.scale + tile.g) : 1.f;
-        bool ok = n1 == 0 || mx4_wait_warp(&u_full, 0, guard);
-        tc_fence_after();
         constexpr int QUADS = RP / 8;        // this warp's columns of t, four at a time
         const int c0 = half * (RP / 2);
         float4 v[QUADS];
 #pragma unroll
         for (int c = 0; c < QUADS; ++c) v[c] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (ok && n1 > 0) {
+        bool ok = true;
+        for (int i = 0; i * STRETCH < n1; ++i) {
+            ok = mx4_wait_warp(&u_full[i & 1], (i >> 1) & 1, guard);
+            if (!ok) break;
+            tc_fence_after();
 #pragma unroll
-            for (int c = 0; c < QUADS; c += 8) {   // 32 columns; past this warp's own they are not used
-                uint32_t u[32];
-                tmem_ld_32x32b_x32(trow + c0 + 4 * c, u);
+            for (int c = 0; c < QUADS; c += 2) {
+                uint32_t u[8];
+                tmem_ld_32x32b_x8(trow + (i & 1) * U1 + c0 + 4 * c, u);
                 tmem_ld_wait();
 #pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    if (c + j < QUADS)
-                        v[c + j] = make_float4(__uint_as_float(u[4 * j]), __uint_as_float(u[4 * j + 1]),
-                                               __uint_as_float(u[4 * j + 2]), __uint_as_float(u[4 * j + 3]));
+                for (int j = 0; j < 2; ++j) {
+                    v[c + j].x += __uint_as_float(u[4 * j]);
+                    v[c + j].y += __uint_as_float(u[4 * j + 1]);
+                    v[c + j].z += __uint_as_float(u[4 * j + 2]);
+                    v[c + j].w += __uint_as_float(u[4 * j + 3]);
+                }
             }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&u_empty[i & 1]);
         }
         // eight columns of a row of t: a 16-byte piece of hi and of lo
         const auto split = [&](int h, const float4& x, const float4& y, uint4& hi, uint4& lo) {

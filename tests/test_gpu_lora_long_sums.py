@@ -1,0 +1,56 @@
+"""Long contractions of the low-rank adapters: the tensor cores cut the sums they accumulate, so the kernels add up
+stretches of 512 terms at most there and join the stretches in rounded fp32 additions.
+
+Tolerances: within a stretch a term is off by at most a whole step of the sum, 2 U of it with U = 2^-24, so n terms in
+stretches of 512 by (2 * 512 + n / 512) U times the sum of their magnitudes, however long the contraction. Each
+test sets a one before many terms of less than a step, which a single cut sum loses.
+"""
+import pytest
+import torch
+
+import group_gemm_gb300 as gg
+
+pytestmark = pytest.mark.gpu
+DEV = torch.device("cuda", 0)
+U = 2.0 ** -24
+STRETCH = 512
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    gg.build()
+    gg.load()
+
+
+@pytest.mark.parametrize("m,k,groups,order", [
+    (800 * 16, 57344, 800, False),      # 16-row tiles, a block each: four warps divide the columns
+    (800 * 16, 57344, 800, True),
+    (152 * 128 - 500, 57344, 1, False),  # 128-row tiles, a block each
+    (152 * 128 - 500, 57344, 1, True),
+])
+@pytest.mark.parametrize("call", ["lora_forward", "lora_grad_input"])
+@pytest.mark.parametrize("r", [8, 32, 56, 128])
+def test_first_product_of_many_columns(m, k, groups, order, call, r):
+    """Each row sums to a number just above the middle of two bf16 neighbours, so t is the upper one; without the
+    terms that a single sum cuts off it would be the lower."""
+    small = 1.5 * 2.0 ** -24                  # three quarters of a step of sums from 1 to 2, in each 16 columns
+    steps = k // 16
+    margin = 7.2e-5
+    ref = 1 + 2.0 ** -8 + margin
+    assert margin > (2 * STRETCH + k / STRETCH / 4 + 16) * U * ref
+    w = torch.zeros(k, dtype=torch.float64)
+    w[16::16] = small
+    rest = ref - (steps - 1) * small
+    for i in range(4):                        # its value in bf16 terms
+        w[i] = float(torch.tensor(rest).to(torch.bfloat16))
+        rest -= float(w[i])
+    assert abs(rest) < 2.0 ** -30
+    w = w.to(torch.bfloat16).to(DEV)
+    first = w.expand(groups, r, k).contiguous()
+    second = torch.zeros((groups, r, 64), dtype=torch.bfloat16, device=DEV)
+    x = torch.ones((m, k), dtype=torch.bfloat16, device=DEV)
+    gs = torch.full((groups,), m // groups, dtype=torch.int32, device=DEV)
+    at = torch.arange(m - 1, -1, -1, dtype=torch.int32, device=DEV) if order else None
+    down, up = (first, second) if call == "lora_forward" else (second, first)
+    _, t = getattr(gg, call)(x, down, up, gs, at)
+    assert torch.all(t == 1 + 2.0 ** -7)
