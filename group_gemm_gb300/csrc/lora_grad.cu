@@ -13,7 +13,7 @@
 //                 team's next stage while it widens the last. They run ahead over the items' ends, so short
 //                 groups follow one another without a pause. (All loaders on every stage: 51 us against
 //                 33 for 16384 x 4096 codes, rank 16; each stage's waits then lie in a row.)
-//   warp 14       tcgen05.mma into one of four accumulators
+//   warp 14       tcgen05.mma into one of four accumulators (three above rank 64), a stretch of 512 rows at most into each
 //   warps 15..18  epilogue: a lane a column, so that each rank's row of dw is stored in whole lines
 // Few items: a cluster divides the group's rows, a block a share, and adds the fp32 partial sums through distributed
 // shared memory in rank order. No atomics: the same result every time.
@@ -39,7 +39,10 @@ constexpr int GR = 64;            // rows of a stage
 constexpr int LT = 64;            // threads of a team of loaders
 constexpr int CHUNK = GR * 128;   // 64 columns x 64 rows of bf16: 8 KB
 constexpr int ROW_RING = 4;       // a team's stages whose row numbers are held
-constexpr int ACCS = 4;           // accumulators
+// Rows of a stretch. The MMAs cut their sums to 24 bits at each step of 16 rows, always towards 0, so an accumulator that
+// ran over a group of 131072 rows was off by 8e-5. It takes 512 at most (5e-7); the epilogue adds the stretches up
+// in fp32, rounded, in tensor memory. (16384 x 4096 of 8 groups: rank 16 1 % slower for it, rank 128 3 %.)
+constexpr int STRETCH = 8 * GR;
 constexpr int MASKS = 16;         // items whose NaN columns are held
 
 __device__ int32_t g_status;      // bits of the waits that ran out, until they are cleared
@@ -62,7 +65,9 @@ struct GradCfg {
     static constexpr int RING = S * SLOT;                        // also the cluster's partial sums: RP x 512 bytes
     static constexpr int ROWS_BYTES = ORDER ? TEAMS * ROW_RING * GR * 4 : 0;
     static constexpr int SMEM = 1024 + RING + ROWS_BYTES;        // and the G + 1 offsets
-    static constexpr uint32_t TMEM_COLS = RP <= 16 ? 128 : ACCS * RP;   // (they are read 32 columns at a time)
+    static constexpr int ACCS = RP <= 64 ? 4 : 3;                // accumulators; behind them the sums of an item's stretches
+    static constexpr uint32_t TMEM_COLS = RP <= 16 ? 128 : RP <= 32 ? 256 : 512;
+    static_assert(ACCS * RP + (RP + 31) / 32 * 32 <= TMEM_COLS, "they are read 32 columns at a time");
     static_assert(RP * 512 <= RING, "the partial sums fit the ring");
     static_assert(SMEM + (RDOT_MAX_GROUPS + 1) * 4 <= 227 * 1024 - 2048, "with the static shared memory it fits a block");
 };
@@ -146,7 +151,7 @@ struct Stage {
 
 template <class Cfg>
 __global__ void __launch_bounds__(Cfg::THREADS, 1) lora_grad_kernel(LoraGradArgs a, int blocks, bool out_bf16, uint64_t timeout_ns) {
-    constexpr int RP = Cfg::RP, S = Cfg::S, TEAMS = Cfg::TEAMS, LOADERS = Cfg::LOADERS, THREADS = Cfg::THREADS;
+    constexpr int RP = Cfg::RP, S = Cfg::S, TEAMS = Cfg::TEAMS, LOADERS = Cfg::LOADERS, THREADS = Cfg::THREADS, ACCS = Cfg::ACCS;
     constexpr bool CODES = Cfg::CODES, ORDER = Cfg::ORDER;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -372,31 +377,32 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1) lora_grad_kernel(LoraGradArgs
         for (int g = first_g, cb = first_cb; ok && g < a.G; it.step(g, cb)) {
             int p0, n;
             it.share(g, p0, n);
-            if (n == 0) continue;
-            const int b = count % ACCS;
-            ok = mx4_wait_uniform(&acc_empty[b], ((count / ACCS) & 1) ^ 1, guard);
-            for (int left = n; ok && left > 0; left -= GR) {
-                ok = ready || mx4_wait_uniform(&full[slot], phase, guard);
-                if (!ok) break;
-                tc_fence_after();
-                const uint64_t da = da0 + static_cast<uint32_t>(slot) * (Cfg::SLOT >> 4), db = db0 + static_cast<uint32_t>(slot) * (Cfg::SLOT >> 4);
-                const uint32_t fresh = left == n ? 0u : 1u;
-                uint64_t* const done = &empty[slot];
-                if (++slot == S) {
-                    slot = 0;
-                    phase ^= 1;
-                }
-                ready = mbar_test_uniform(&full[slot], phase);
-                if (elected) {
+            for (int left = n; ok && left > 0;) {
+                const int b = count % ACCS, from = left, to = max(left - STRETCH, 0);
+                ok = mx4_wait_uniform(&acc_empty[b], ((count / ACCS) & 1) ^ 1, guard);
+                for (; ok && left > to; left -= GR) {
+                    ok = ready || mx4_wait_uniform(&full[slot], phase, guard);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint64_t da = da0 + static_cast<uint32_t>(slot) * (Cfg::SLOT >> 4), db = db0 + static_cast<uint32_t>(slot) * (Cfg::SLOT >> 4);
+                    const uint32_t fresh = left == from ? 0u : 1u;
+                    uint64_t* const done = &empty[slot];
+                    if (++slot == S) {
+                        slot = 0;
+                        phase ^= 1;
+                    }
+                    ready = mbar_test_uniform(&full[slot], phase);
+                    if (elected) {
 #pragma unroll
-                    for (int kk = 0; kk < GR / 16; ++kk)   // 16 rows: two groups of 8, 2 KB
-                        if (16 * kk < left) mma_f16(tmem + b * RP, da + kk * 128, db + kk * 128, idesc, kk == 0 ? fresh : 1u);
-                    mma_commit(done);
-                    if (left <= GR) mma_commit(&acc_full[b]);
+                        for (int kk = 0; kk < GR / 16; ++kk)   // 16 rows: two groups of 8, 2 KB
+                            if (16 * kk < left) mma_f16(tmem + b * RP, da + kk * 128, db + kk * 128, idesc, kk == 0 ? fresh : 1u);
+                        mma_commit(done);
+                        if (left - GR <= to) mma_commit(&acc_full[b]);
+                    }
+                    __syncwarp();
                 }
-                __syncwarp();
+                ++count;
             }
-            ++count;
         }
         // all MMAs issued by this thread complete before teardown frees tensor memory
         if (elected) {
@@ -410,21 +416,54 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1) lora_grad_kernel(LoraGradArgs
         const int q = warp & 3;                        // the lane quarter of tensor memory that this warp may read
         const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * q) << 16);
         float* part = reinterpret_cast<float*>(smem);  // [rank][128 columns], once the ring is done with
-        int count = 0;
+        int count = 0, items = 0;                      // stretches, items with a row
         for (int g = first_g, cb = first_cb; g < a.G; it.step(g, cb)) {
             const int col = cb * GC + 32 * q + lane;
             int p0, n;
             it.share(g, p0, n);
-            const int b = count % ACCS;
+            int b = count % ACCS;
             bool nan = false;
             if (n > 0) {
                 if (!mx4_wait_warp(&acc_full[b], (count / ACCS) & 1, guard)) break;
                 tc_fence_after();
+                if (n > STRETCH) {
+                    // every stretch, the last one too, into the sums
+                    bool ok = true;
+                    for (int left = n;;) {
+#pragma unroll 1
+                        for (int j0 = 0; j0 < a.rank; j0 += 16) {
+                            uint32_t v[16], u[16];
+                            tmem_ld_32x32b_x16(lanes + b * RP + j0, v);
+                            if (left < n) {
+                                tmem_ld_32x32b_x16(lanes + ACCS * RP + j0, u);
+                                tmem_ld_wait();
+#pragma unroll
+                                for (int j = 0; j < 16; ++j) v[j] = __float_as_uint(__uint_as_float(u[j]) + __uint_as_float(v[j]));
+                            } else {
+                                tmem_ld_wait();
+                            }
+                            tmem_st_32x32b_x16(lanes + ACCS * RP + j0, v);
+                        }
+                        tmem_st_wait();
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&acc_empty[b]);
+                        ++count;
+                        left -= STRETCH;
+                        if (left <= 0) break;
+                        b = count % ACCS;
+                        ok = mx4_wait_warp(&acc_full[b], (count / ACCS) & 1, guard);
+                        if (!ok) break;
+                        tc_fence_after();
+                    }
+                    if (!ok) break;
+                    b = ACCS;   // the item's sums
+                }
                 if (CODES) {
-                    const uint32_t mask = nan_cols[count % MASKS][q];
+                    const uint32_t mask = nan_cols[items % MASKS][q];
                     nan = mask >> lane & 1;
                     __syncwarp();
-                    if (lane == 0 && mask) nan_cols[count % MASKS][q] = 0;
+                    if (lane == 0 && mask) nan_cols[items % MASKS][q] = 0;
                 }
             }
 #pragma unroll 1
@@ -459,10 +498,13 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1) lora_grad_kernel(LoraGradArgs
                 }
             }
             if (n > 0) {
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&acc_empty[b]);
-                ++count;
+                if (b < ACCS) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&acc_empty[b]);
+                    ++count;
+                }
+                ++items;
             }
         }
         __syncwarp();

@@ -22,6 +22,53 @@ def _built():
     gg.load()
 
 
+# one long group of few columns (its rows divided over a cluster), and as many items as fill the SMs (undivided)
+@pytest.mark.parametrize("groups,rows,r", [(1, 1 << 20, 16), (1, 1 << 20, 40), (1, 1 << 20, 64), (1, 1 << 20, 128),
+                                           (160, 1 << 16, 16), (160, 1 << 16, 128)])
+@pytest.mark.parametrize("codes", [False, True])
+@pytest.mark.parametrize("order", [False, True])
+def test_weight_gradient_of_many_rows(groups, rows, r, codes, order):
+    m, width = groups * rows, 64
+    small = 2.0 ** -28
+    t = torch.full((groups, rows, r), small, dtype=torch.bfloat16, device=DEV)
+    t[:, 0] = 1
+    t = t.view(m, r)
+    z = torch.ones((m, width), dtype=torch.bfloat16, device=DEV)
+    scales = None
+    if codes:
+        z, scales = gg.quantize_mxfp8(z)
+    gs = torch.full((groups,), rows, dtype=torch.int32, device=DEV)
+    at = torch.arange(m - 1, -1, -1, dtype=torch.int32, device=DEV) if order else None
+    dw = gg.lora_grad_weight(t, z, gs, at, scales).double()
+    ref = 1 + (rows - 1) * small
+    assert (dw - ref).abs().max() <= ((2 * STRETCH + rows / STRETCH) * U + U) * ref
+
+
+@pytest.mark.parametrize("order", [False, True])
+@pytest.mark.parametrize("r", [16, 128])
+def test_nan_codes_in_groups_of_several_stretches(r, order):
+    """A NaN code reaches the sums of its group's column alone, whether the group has one stretch of rows or more,
+    with several items to a block."""
+    gen = torch.Generator(device=DEV).manual_seed(1)
+    sizes = [0, 1500, 3, 513, 512, 1024, 0, 64, 2049, 700] * 5
+    m, width, groups = sum(sizes), 1152, len(sizes)
+    t = torch.randn((m, r), generator=gen, device=DEV).to(torch.bfloat16)
+    codes, scales = gg.quantize_mxfp8(torch.randn((m, width), generator=gen, device=DEV))
+    at = torch.randperm(m, generator=gen, device=DEV).int() if order else None
+    rows = torch.arange(m, device=DEV) if at is None else at.long()
+    gs = torch.tensor(sizes, dtype=torch.int32, device=DEV)
+    clean = gg.lora_grad_weight(t, codes, gs, at, scales)
+    group = torch.repeat_interleave(torch.arange(groups, device=DEV), gs.long())
+    hit = torch.randint(0, m, (300,), generator=gen, device=DEV)
+    col = torch.randint(0, width, (300,), generator=gen, device=DEV)
+    codes[rows[hit], col] = 0x7f
+    want = torch.zeros((groups, width), dtype=torch.bool, device=DEV)
+    want[group[hit], col] = True
+    dw = gg.lora_grad_weight(t, codes, gs, at, scales)
+    want = want.unsqueeze(1).expand_as(dw)
+    assert torch.equal(torch.isnan(dw), want) and torch.equal(dw[~want], clean[~want])
+
+
 @pytest.mark.parametrize("m,k,groups,order", [
     (800 * 16, 57344, 800, False),      # 16-row tiles, a block each: four warps divide the columns
     (800 * 16, 57344, 800, True),
