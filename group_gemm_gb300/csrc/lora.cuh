@@ -183,7 +183,9 @@ __device__ __forceinline__ void lora_tile_rows(int* row_of, const LoraTile& tile
 }
 
 // bf16 of a value and of what the rounding left, so that hi + lo has a relative error of 2^-16. Of an infinity or
-// NaN, hi alone.
+// NaN, hi alone. (lo may be 0 or of the other sign, so an infinite weight may give NaN for an infinity. Cutting hi
+// would leave lo of hi's sign and the product right, for twice the error; looking for such results in each stage took 3
+// to 9 % of a decode batch's time.)
 __device__ __forceinline__ void split_bf16x2(float a, float b, uint32_t& hi, uint32_t& lo) {
     hi = pack_bf16x2(a, b);
     const float fa = __uint_as_float(hi << 16), fb = __uint_as_float(hi & 0xffff0000u);

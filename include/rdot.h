@@ -456,11 +456,17 @@ RDOT_API rdot_status rdot_dequantize_mxfp8(const uint8_t* codes, const uint8_t* 
  * row is not written). There is no workspace; every call can be captured in a CUDA graph. They run on the
  * calling thread's current device and never synchronise the host.
  *
- * Sums are fp32 in a fixed order. t enters the second product with an error of 2^-16, out is rounded to
- * bf16 once. m = 0 launches nothing, except that the weight gradient still writes its zeros. k % 8 == 0,
- * n % 8 == 0 (at most 2^30), r % 8 == 0 and r <= RDOT_LORA_MAX_RANK (pad smaller adapters with zero rows),
- * m < 2^31, G <= RDOT_MAX_GROUPS, else RDOT_ERR_UNSUPPORTED; 16-byte alignment, 4 for group_sizes, order
- * and scale, any for z_scale. */
+ * Sums are fp32 in a fixed order: on the tensor cores, which cut a sum to 24 bits at each step of 16 terms, in
+ * stretches of 512 terms, joined in rounded additions. t enters the second product as two bf16 terms, with an
+ * error of 2^-16 (beyond bf16's range as an infinity); out is rounded to bf16 once.
+ * An infinity or NaN in x, dy, base or scale, or in a weight of the first product, gives what the formula gives.
+ * One in a weight of the second product (up in the forward, down in the gradient of the input) makes its column of
+ * its adapter's rows not finite, an infinity or NaN: the two terms of t may differ in sign, or one be 0. No
+ * other element of the result is touched by it.
+ * m = 0 launches nothing, except that the weight gradient still writes its zeros. k % 8 == 0, n % 8 == 0 (at
+ * most 2^30), r % 8 == 0 and r <= RDOT_LORA_MAX_RANK (pad smaller adapters with zero rows), m < 2^31,
+ * G <= RDOT_MAX_GROUPS, else RDOT_ERR_UNSUPPORTED; 16-byte alignment, 4 for group_sizes, order and scale, any
+ * for z_scale. */
 #define RDOT_LORA_MAX_RANK 128
 
 /* The weight gradient, and where groups have many rows the forward and the gradient of the input, wait on
