@@ -179,11 +179,13 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1) lora_grad_kernel(LoraGradArgs
         fence_mbar_init();
     }
     if (tid < MASKS * (GC / 32)) nan_cols[tid / (GC / 32)][tid % (GC / 32)] = 0;
+    // As in lora_tall.cu: tensor memory only once the kernel before has ended, the next one's blocks only once this block has
+    // its own. Else a block could hold what a block of the kernel that it waits for is about to ask for.
+    grid_dependency_wait();
     if (warp == LOADERS) {
         tmem_alloc(&tmem_holder, Cfg::TMEM_COLS);
         tmem_relinquish();
     }
-    grid_dependency_enter();
     {
         // the groups' first positions, ends clamped to M, a negative size as 0
         constexpr int PER = (RDOT_MAX_GROUPS + THREADS - 1) / THREADS;
@@ -207,6 +209,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1) lora_grad_kernel(LoraGradArgs
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    grid_launch_dependents();
     const uint32_t tmem = tmem_holder;
     const WaitGuard guard{&abort_flag, &g_status, timeout_ns};
     const int first = static_cast<int>(blockIdx.x) / C, step = static_cast<int>(gridDim.x) / C;
