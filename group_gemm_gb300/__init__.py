@@ -922,7 +922,8 @@ def dequantize_mxfp8(codes, scales, dtype=None, stream=None):
 
 
 def _rows32(rows):
-    """Row numbers or ids as contiguous int32; what 32 bits do not hold stays outside every range."""
+    """Row numbers, ids or group sizes as contiguous int32; what 32 bits do not hold stays outside every range, a
+    size past all rows."""
     import torch
     if rows.dtype == torch.int64:
         rows = rows.clamp(-1, 2 ** 31 - 1)
@@ -963,7 +964,7 @@ def _lora(call, x, first, second, down, up, group_sizes, order, scale, base, out
         if out is None:
             out = torch.empty((m, width), dtype=torch.bfloat16, device=x.device)
         t = torch.empty((m, r), dtype=torch.bfloat16, device=x.device)
-        call(x.contiguous(), down.contiguous(), up.contiguous(), group_sizes.to(torch.int32).contiguous(), out, t,
+        call(x.contiguous(), down.contiguous(), up.contiguous(), _rows32(group_sizes), out, t,
              order=None if order is None else _rows32(order),
              scale=None if scale is None else scale.to(torch.float32).contiguous(),
              base=None if base is None else base.contiguous(), stream=s)
@@ -1011,7 +1012,7 @@ def lora_grad_weight(t, z, group_sizes, order=None, z_scale=None, out_dtype=None
     with torch.cuda.stream(s):
         if dw is None:
             dw = torch.empty((g, r, width), dtype=out_dtype, device=t.device)
-        rdot_lora_grad_weight(t.contiguous(), z.contiguous(), group_sizes.to(torch.int32).contiguous(), dw,
+        rdot_lora_grad_weight(t.contiguous(), z.contiguous(), _rows32(group_sizes), dw,
                               order=None if order is None else _rows32(order),
                               z_scale=None if z_scale is None else z_scale.contiguous(), stream=s)
     return dw
