@@ -1623,8 +1623,10 @@ rdot_status lora_apply(const void* x, const void* first, const void* second, con
     const long long used = std::min<long long>(routed, 6LL * m * groups / (5LL * (m + groups)) + 1);
     const long long tiles16 = std::max(used, m / LORA_FEW_ROWS + used / 2);
     const long long tiles128 = std::max(used, m / LORA_TALL_ROWS + (5 * used + 7) / 8);
-    // Tiles of 16 rows read a group's weights for each 16 of its rows; tiles of 128 rows are few, and half empty where groups
-    // are short, the more so where clusters of four of their blocks are more than the SMs hold. All times in us, 16-row tiles /
+    // Tiles of 16 rows read a group's weights, 2 rank (K + N) bytes, for each 16 of its rows; tiles of 128 rows are few, and half
+    // empty where groups are short, the more so where clusters of four of their blocks are more than the SMs hold. So 16 rows
+    // are for calls whose 128-row tiles would leave SMs idle or whose groups are short, the shorter the higher the rank (the
+    // weights' bytes). The borders lie where the two met, by the average group, as sizes are known on the device alone. All times in us, 16-row tiles /
     // 128-row tiles, 4096 -> 4096 through an order. Up to rank 32: 2048 rows of 4 groups 22 / 29, 4096 of 4 35 / 35, 8192 of
     // 4 58 / 49, 3000 of 32 29 / 39, 6000 of 32 59 / 48, 8192 of 128 59 / 74; without an order, rank 32: 1500 of 4 22 / 24,
     // 8192 of 128 72 / 66. Up to rank 64: 1200 rows of 4 groups 29 / 29, 1200 of 32 30 / 37, 1600 of 4 38 / 30, 2000 of 32

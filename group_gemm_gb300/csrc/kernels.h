@@ -273,9 +273,10 @@ struct LoraArgs {
 // lora_apply_blocks).
 cudaError_t launch_lora_apply(const LoraArgs& a, int C, int D, int blocks, cudaStream_t stream);
 constexpr int LORA_FEW_ROWS = 16;
-// Of a hundred blocks that the SMs could hold, how many of clusters of C find room at once, with one block on an SM or with
-// more (a cluster lies within one of the SMs' hardware groups, and leaves over what it does not divide). Measured as the
-// largest grids without a second round.
+// The blocks of clusters of C that run at once, in percent of those that the SMs could hold, with one block on an SM or with
+// more (a cluster lies within one of the SMs' hardware groups, and leaves over what it does not divide). Measured on one GPU
+// of 152 SMs as the largest grids without a second round; elsewhere it decides over speed alone. 105: a little over what fits
+// is let through, as the tiles that a call has are only expected, and a few late clusters cost less than smaller ones.
 constexpr int lora_cluster_room(int C, int per_sm) {
     constexpr int one[9] = {0, 100, 100, 93, 95, 89, 86, 69, 79};
     return per_sm == 1 ? one[C] : C <= 2 ? 105 : C <= 4 ? 95 : 92;

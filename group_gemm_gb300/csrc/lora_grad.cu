@@ -7,7 +7,7 @@
 //
 // A work item is 128 columns of a group: D [128 columns x rank] in tensor memory, z as the MMA's A operand and t
 // as its B, both as they lie in memory (MN-major), 64 rows a stage. z is read once; t, C/128 times from L2.
-// Persistent blocks, one per SM, 19 warps:
+// Persistent blocks, one per SM, 19 warps (above rank 64, where the ring has six slots, 17: six teams):
 //   warps 0..13   loaders, seven teams of two warps that take the stages in turn: z and t by asynchronous 16-byte
 //                 copies into swizzled slots, zeros past the group's last row; codes instead through registers, a
 //                 team's next stage while it widens the last. They run ahead over the items' ends, so short
@@ -348,7 +348,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1) lora_grad_kernel(LoraGradArgs
                 fetch(nx, i + 1);
             }
             // the stage has landed; written in the generic proxy, read by the MMAs in the async one. (The fence once for all
-            // by the MMA warp: 0.35 us a stage, which it bound.)
+            // by the MMA warp: 33 against 30 us for 16384 x 4096 codes.)
             cp_async_wait<0>();
             fence_proxy_async_smem();
             __syncwarp();
@@ -368,9 +368,9 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1) lora_grad_kernel(LoraGradArgs
         __syncwarp();
     } else if (warp == LOADERS) {
         // ---------------------------------------------------------------- MMA issuer (uniform, one lane elected)
-        // Its own instructions, not the MMAs, take a stage's time here (650 clocks; four MMAs fewer change nothing), so they
-        // are few: counters for divisions, descriptors made outside the elected branch (in uniform registers), the next
-        // stage's barrier looked at ahead of this one's MMAs. 16384 x 4096 codes: 30.3 against 32.0 us.
+        // Its own instructions cost more than the MMAs (four MMAs fewer change nothing), so they are few: counters for divisions,
+        // descriptors made outside the elected branch (in uniform registers), the next stage's barrier looked at ahead of
+        // this one's MMAs (16384 x 4096 codes: 1.7 us less).
         const bool elected = elect_one();
         const uint32_t idesc = idesc_f16(GC, ranks, true, true, true, true);
         const uint64_t da0 = smem_desc_sw128(smem_u32(smem), CHUNK, 1024), db0 = smem_desc_sw128(smem_u32(smem) + 2 * CHUNK, CHUNK, 1024);
@@ -546,7 +546,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1) lora_grad_kernel(LoraGradArgs
 }
 
 template <int RP, bool CODES, bool ORDER>
-cudaError_t launch_cfg(const LoraGradArgs& a, bool out_bf16, int C, int slots, uint64_t timeout_ns, cudaStream_t stream) {
+cudaError_t launch_cfg(const LoraGradArgs& a, bool out_bf16, int C, int sm_count, uint64_t timeout_ns, cudaStream_t stream) {
     using Cfg = GradCfg<RP, CODES, ORDER>;
     auto kern = lora_grad_kernel<Cfg>;
     const int shm = Cfg::SMEM + (a.G + 1) * static_cast<int>(sizeof(int32_t));
@@ -556,16 +556,16 @@ cudaError_t launch_cfg(const LoraGradArgs& a, bool out_bf16, int C, int slots, u
     if (e != cudaSuccess) return e;
     const int blocks = (a.C + GC - 1) / GC;
     const long long items = static_cast<long long>(a.G) * blocks;
-    const long long grid = C > 1 ? items * C : items < slots ? items : slots;
+    const long long grid = C > 1 ? items * C : items < sm_count ? items : sm_count;   // a persistent block an SM
     return launch_pdl_cluster(kern, dim3(static_cast<unsigned>(grid)), dim3(Cfg::THREADS), C, shm, stream, a, blocks, out_bf16, timeout_ns);
 }
 
 template <bool CODES, bool ORDER>
-cudaError_t launch_rank(const LoraGradArgs& a, bool out_bf16, int C, int slots, uint64_t timeout_ns, cudaStream_t stream) {
-    if (a.rank <= 16) return launch_cfg<16, CODES, ORDER>(a, out_bf16, C, slots, timeout_ns, stream);
-    if (a.rank <= 32) return launch_cfg<32, CODES, ORDER>(a, out_bf16, C, slots, timeout_ns, stream);
-    if (a.rank <= 64) return launch_cfg<64, CODES, ORDER>(a, out_bf16, C, slots, timeout_ns, stream);
-    return launch_cfg<128, CODES, ORDER>(a, out_bf16, C, slots, timeout_ns, stream);
+cudaError_t launch_rank(const LoraGradArgs& a, bool out_bf16, int C, int sm_count, uint64_t timeout_ns, cudaStream_t stream) {
+    if (a.rank <= 16) return launch_cfg<16, CODES, ORDER>(a, out_bf16, C, sm_count, timeout_ns, stream);
+    if (a.rank <= 32) return launch_cfg<32, CODES, ORDER>(a, out_bf16, C, sm_count, timeout_ns, stream);
+    if (a.rank <= 64) return launch_cfg<64, CODES, ORDER>(a, out_bf16, C, sm_count, timeout_ns, stream);
+    return launch_cfg<128, CODES, ORDER>(a, out_bf16, C, sm_count, timeout_ns, stream);
 }
 
 }  // namespace
@@ -581,9 +581,8 @@ cudaError_t launch_lora_grad(const LoraGradArgs& a, bool codes, bool out_bf16, i
     int C = lora_cluster(items, 1, sm_count);
     while (C > 1 && 2 * C > stages) --C;
     if (stages * (C - 1) < (a.rank <= 64 ? 6 : 10) * C) C = 1;
-    const int slots = sm_count;
-    if (codes) return a.order ? launch_rank<true, true>(a, out_bf16, C, slots, timeout_ns, stream) : launch_rank<true, false>(a, out_bf16, C, slots, timeout_ns, stream);
-    return a.order ? launch_rank<false, true>(a, out_bf16, C, slots, timeout_ns, stream) : launch_rank<false, false>(a, out_bf16, C, slots, timeout_ns, stream);
+    if (codes) return a.order ? launch_rank<true, true>(a, out_bf16, C, sm_count, timeout_ns, stream) : launch_rank<true, false>(a, out_bf16, C, sm_count, timeout_ns, stream);
+    return a.order ? launch_rank<false, true>(a, out_bf16, C, sm_count, timeout_ns, stream) : launch_rank<false, false>(a, out_bf16, C, sm_count, timeout_ns, stream);
 }
 
 cudaError_t lora_grad_status(int32_t** word) {

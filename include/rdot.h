@@ -463,10 +463,10 @@ RDOT_API rdot_status rdot_dequantize_mxfp8(const uint8_t* codes, const uint8_t* 
  * One in a weight of the second product (up in the forward, down in the gradient of the input) makes its column of
  * its adapter's rows not finite, an infinity or NaN: the two terms of t may differ in sign, or one be 0. No
  * other element of the result is touched by it.
- * m = 0 launches nothing, except that the weight gradient still writes its zeros. k % 8 == 0, n % 8 == 0 (at
- * most 2^30), r % 8 == 0 and r <= RDOT_LORA_MAX_RANK (pad smaller adapters with zero rows), m < 2^31,
- * G <= RDOT_MAX_GROUPS, else RDOT_ERR_UNSUPPORTED; 16-byte alignment, 4 for group_sizes, order and scale, any
- * for z_scale. */
+ * m = 0 launches nothing, except that rdot_lora_group and the weight gradient still write their zeros.
+ * k % 8 == 0, n % 8 == 0 (at most 2^30), r % 8 == 0 and r <= RDOT_LORA_MAX_RANK (pad smaller adapters with zero
+ * rows), m < 2^31, G <= RDOT_MAX_GROUPS, else RDOT_ERR_UNSUPPORTED; 16-byte alignment, 4 for group_sizes, order
+ * and scale, any for z_scale. */
 #define RDOT_LORA_MAX_RANK 128
 
 /* The weight gradient, and where groups have many rows the forward and the gradient of the input, wait on
