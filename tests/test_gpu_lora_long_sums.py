@@ -2,13 +2,14 @@
 stretches of 512 terms at most there and join the stretches in rounded fp32 additions.
 
 Tolerances: within a stretch a term is off by at most a whole step of the sum, 2 U of it with U = 2^-24, so n terms in
-stretches of 512 by (2 * 512 + n / 512) U times the sum of their magnitudes, however long the contraction. Each
-test sets a one before many terms of less than a step, which a single cut sum loses.
+stretches of 512 by (2 * 512 + n / 512) U times the sum of their magnitudes, however long the contraction. The
+tests of many rows and columns set a one before many terms of less than a step, which a single cut sum loses.
 """
 import pytest
 import torch
 
 import group_gemm_gb300 as gg
+from tests.test_gpu_lora import H, close, make, ragged, reference
 
 pytestmark = pytest.mark.gpu
 DEV = torch.device("cuda", 0)
@@ -101,3 +102,19 @@ def test_first_product_of_many_columns(m, k, groups, order, call, r):
     down, up = (first, second) if call == "lora_forward" else (second, first)
     _, t = getattr(gg, call)(x, down, up, gs, at)
     assert torch.all(t == 1 + 2.0 ** -7)
+
+
+# several stretches in a block, in clusters of all sizes, with stages that do not fill the last stretch
+@pytest.mark.parametrize("m,k,groups", [(1700, 14336, 1), (2600, 8200, 1), (3300, 12296, 1), (4100, 7240, 1), (5200, 14336, 1), (7000, 4168, 2),
+                                        (9000, 2056, 3), (2000, 6408, 40), (700, 14344, 6)])
+@pytest.mark.parametrize("r", [16, 32, 64, 128])
+@pytest.mark.parametrize("order", [False, True])
+def test_first_product_of_several_stretches(m, k, groups, r, order):
+    d = make(m, k, 136, groups, r, ragged(m, groups, r, 70) if groups > 1 else [m - 70], order, k)
+    out, t = gg.lora_forward(d["x"], d["down"], d["up"], d["sizes"], d["order"], d["scale"], d["base_n"])
+    ref, ref_t, tol, tol_t = reference(d["x"], d["down"], d["up"], d["sizes"].tolist(), d["order"], d["scale"], d["base_n"])
+    close(t, ref_t, tol_t)
+    close(out, ref, tol)
+    # and t to what the stretches leave: a rounding to bf16 of a value that is off by their sums' errors
+    _, exact, _, _ = reference(d["x"].abs(), d["down"].abs(), d["up"], d["sizes"].tolist(), d["order"], d["scale"].abs(), None)
+    close(t, ref_t, H * ref_t.abs() + (1 + H) * (2 * STRETCH + k / STRETCH + 32) * U * exact)
