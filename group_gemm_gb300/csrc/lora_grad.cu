@@ -18,11 +18,12 @@
 // Few items: a cluster divides the group's rows, a block a share, and adds the fp32 partial sums through distributed
 // shared memory in rank order. No atomics: the same result every time.
 //
-// What bounds it: bf16, the loads (5 TB/s of z in the steady state, and 16384 x 4096 of 8 groups is 256 items for 152
-// SMs, two rounds: 30 us, floor 20); codes, the widening and the MMA warp's loop, 0.36 us a stage (28.2 us, floor 10.6);
-// short groups, the epilogue's stores (4099 rows of 24 groups x 7168, rank 64: 21.4 us, floor 11.1); where one group has
-// most rows, its items. Tried for those: each block a run of items of equal cost (stages and epilogues) in place of
-// every 152nd, no faster with groups of one length or of skewed ones (31 us against 31, 38 against 35 for the last case).
+// What bounds it (times of the kernel replayed): bf16, the loads (5 TB/s of z in the steady state, and 16384 x 4096 of 8
+// groups is 256 items for 152 SMs, two rounds: 29 us, floor 20); codes, 0.36 us a 64-row stage, of which widening, loads
+// and MMAs each hide most of the others (30 us, floor 10.6); short groups, the epilogue's stores (4099 rows of 24 groups
+// x 7168, rank 64: 23.5 us, floor 11.1); where one group has most rows, its items. Tried for those: each block a run of
+// items of equal cost (stages and epilogues) in place of every 152nd, no faster with groups of one length or of skewed
+// ones (31 us against 31, 38 against 35 for the last case).
 #include <cuda_bf16.h>
 
 #include "kernels.h"

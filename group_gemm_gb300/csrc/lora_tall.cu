@@ -12,8 +12,8 @@
 //                 128-byte lines. Warps 2..5 take the even stages, 6..9 the odd ones.
 //   warps 10..13  only with `order`: the rows by asynchronous 16-byte copies. (Four rows a TMA gather took
 //                 58 ns to issue, 1.9 us a stage.)
-// HBM bounds it: base and out pass once. 16384 rows of 8 groups, 4096 -> 14336, rank 16: 184 us, 5.8 TB/s (86 % of a
-// copy's rate; tiles of 112 rows, one on each SM, the same), 14336 -> 4096 123 us. TMA takes the loads off the
+// HBM bounds it: base and out pass once. 16384 rows of 8 groups, 4096 -> 14336, rank 16: 185 us, 5.8 TB/s (86 % of a
+// copy's rate; tiles of 112 rows, one on each SM, the same), 14336 -> 4096 125 us. TMA takes the loads off the
 // load/store pipe, which bounds the mma.sync form (242 and 182 us: 58 % of its wavefronts at 65 % of HBM's rate).
 //
 // Rows of the tile past its last (or with no valid row number) hold whatever the boxes or an earlier use left:
