@@ -4,16 +4,11 @@
 // on the stream is still running: its CTAs take the SMs that kernel has already left, set up what
 // touches no global memory (barriers, tensor memory, prefetch of tensor maps passed as
 // parameters), and only then wait until the previous grid has completed and its writes are
-// visible (griddepcontrol.wait). Every kernel here also signals early that the next one may be
-// scheduled (griddepcontrol.launch_dependents): that kernel's CTAs still find room only on SMs
-// this one has left, and they wait the same way, so a chain of launches never runs ahead of its
-// data. Between launches this hides the launch latency and the prologue of the next kernel behind
-// the tail of the previous one.
-//
-// Most signal at their start, once they hold their tensor memory; their shared memory leaves no
-// room on the SM for another kernel that takes some. lora_tall.cu, two blocks of which share an SM,
-// and lora_grad.cu take theirs only after the wait and signal after that, so that no CTA holds
-// tensor memory while it waits for a grid one of whose CTAs is still to get its own.
+// visible (griddepcontrol.wait). Every kernel here also signals at its start that the next one
+// may be scheduled (griddepcontrol.launch_dependents): that kernel's CTAs still find room only
+// on SMs this one has left, and they wait the same way, so a chain of launches never runs ahead
+// of its data. Between launches this hides the launch latency and the prologue of the next
+// kernel behind the tail of the previous one.
 #pragma once
 
 #include <cuda_runtime.h>
