@@ -13,14 +13,14 @@
 //                 team's next stage while it widens the last. They run ahead over the items' ends, so short
 //                 groups follow one another without a pause. (All loaders on every stage: 51 us against
 //                 33 for 16384 x 4096 codes, rank 16; each stage's waits then lie in a row.)
-//   warp 14       tcgen05.mma into one of four accumulators (three above rank 64), a stretch of 512 rows at most into each
+//   warp 14       tcgen05.mma into one of four accumulators (three above rank 64), a stretch of 512 or 1024 rows at most into each
 //   warps 15..18  epilogue: a lane a column, so that each rank's row of dw is stored in whole lines
 // Few items: a cluster divides the group's rows, a block a share, and adds the fp32 partial sums through distributed
 // shared memory in rank order. No atomics: the same result every time.
 //
 // What bounds it (times of the kernel replayed): bf16, the loads (5 TB/s of z in the steady state, and 16384 x 4096 of 8
 // groups is 256 items for 152 SMs, two rounds: 29 us, floor 20); codes, 0.36 us a 64-row stage, of which widening, loads
-// and MMAs each hide most of the others (30 us, floor 10.6); short groups, the epilogue's stores (4099 rows of 24 groups
+// and MMAs each hide most of the others (29 us, floor 10.6); short groups, the epilogue's stores (4099 rows of 24 groups
 // x 7168, rank 64: 23.5 us, floor 11.1); where one group has most rows, its items. Tried for those: each block a run of
 // items of equal cost (stages and epilogues) in place of every 152nd, no faster with groups of one length or of skewed
 // ones (31 us against 31, 38 against 35 for the last case).
@@ -40,10 +40,6 @@ constexpr int GR = 64;            // rows of a stage
 constexpr int LT = 64;            // threads of a team of loaders
 constexpr int CHUNK = GR * 128;   // 64 columns x 64 rows of bf16: 8 KB
 constexpr int ROW_RING = 4;       // a team's stages whose row numbers are held
-// Rows of a stretch. The MMAs cut their sums to 24 bits at each step of 16 rows, always towards 0, so an accumulator that
-// ran over a group of 131072 rows was off by 8e-5. It takes 512 at most (5e-7); the epilogue adds the stretches up
-// in fp32, rounded, in tensor memory. (16384 x 4096 of 8 groups: rank 16 1 % slower for it, rank 128 3 %.)
-constexpr int STRETCH = 8 * GR;
 constexpr int MASKS = 16;         // items whose NaN columns are held
 
 __device__ int32_t g_status;      // bits of the waits that ran out, until they are cleared
@@ -66,6 +62,12 @@ struct GradCfg {
     static constexpr int RING = S * SLOT;                        // also the cluster's partial sums: RP x 512 bytes
     static constexpr int ROWS_BYTES = ORDER ? TEAMS * ROW_RING * GR * 4 : 0;
     static constexpr int SMEM = 1024 + RING + ROWS_BYTES;        // and the G + 1 offsets
+    // Rows of a stretch. The MMAs cut their sums to 24 bits at each step of 16 rows, always towards 0, so an accumulator that
+    // ran over a group of 131072 rows was off by 8e-5 (codes 3e-5: their products have fewer bits). It takes so many at
+    // most that it stays within 6e-7, and the epilogue adds the stretches up in fp32, rounded, in tensor memory. (16384 x
+    // 4096 of 8 groups, rank 16: codes 29.0 us, in stretches of 512 29.8, of any length 28.6; bf16 28.6, 28.2 of 1024,
+    // 27.8 of any length.)
+    static constexpr int STRETCH = CODES ? 1024 : 512;
     static constexpr int ACCS = RP <= 64 ? 4 : 3;                // accumulators; behind them the sums of an item's stretches
     static constexpr uint32_t TMEM_COLS = RP <= 16 ? 128 : RP <= 32 ? 256 : 512;
     static_assert(ACCS * RP + (RP + 31) / 32 * 32 <= TMEM_COLS, "they are read 32 columns at a time");
@@ -153,6 +155,7 @@ struct Stage {
 template <class Cfg>
 __global__ void __launch_bounds__(Cfg::THREADS, 1) lora_grad_kernel(LoraGradArgs a, int blocks, bool out_bf16, uint64_t timeout_ns) {
     constexpr int RP = Cfg::RP, S = Cfg::S, TEAMS = Cfg::TEAMS, LOADERS = Cfg::LOADERS, THREADS = Cfg::THREADS, ACCS = Cfg::ACCS;
+    constexpr int STRETCH = Cfg::STRETCH;
     constexpr bool CODES = Cfg::CODES, ORDER = Cfg::ORDER;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));

@@ -457,8 +457,8 @@ RDOT_API rdot_status rdot_dequantize_mxfp8(const uint8_t* codes, const uint8_t* 
  * calling thread's current device and never synchronise the host.
  *
  * Sums are fp32 in a fixed order: on the tensor cores, which cut a sum to 24 bits at each step of 16 terms, in
- * stretches of 512 terms, joined in rounded additions. t enters the second product as two bf16 terms, with an
- * error of 2^-16 (beyond bf16's range as an infinity); out is rounded to bf16 once.
+ * stretches of 512 terms (1024 of codes), joined in rounded additions. t enters the second product as two bf16
+ * terms, with an error of 2^-16 (beyond bf16's range as an infinity); out is rounded to bf16 once.
  * An infinity or NaN in x, dy, base or scale, or in a weight of the first product, gives what the formula gives.
  * One in a weight of the second product (up in the forward, down in the gradient of the input) makes its column of
  * its adapter's rows not finite, an infinity or NaN: the two terms of t may differ in sign, or one be 0. No
